@@ -1,6 +1,7 @@
 /*
- * mhc.h -- C ABI of the fused mHC pre-mapping forward, and of the MhcPre backward, for
- * AMD Instinct MI355X (gfx950).
+ * mhc.h -- C ABI of the fused mHC pre-mapping forward, of the MhcPre backward, of hc_post
+ * and its backward, of 8-bit activation checkpoints for the two backward passes, and of the
+ * gated projection of the sub-layer in between, for AMD Instinct MI355X (gfx950).
  *
  * What one call computes, per token t (x viewed as xFlat of length K = n*D):
  *   invRms = (mean(xFlat^2) + normEps)^(-1/2)
@@ -460,6 +461,99 @@ typedef struct mhc_post_tensors {
 } mhc_post_tensors;
 
 mhc_status mhc_post(const mhc_post_params* params, const mhc_post_tensors* tensors, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit checkpoints
+ *
+ * Activations kept from the forward to the backward pass in 8 bits: the n streams are the
+ * largest tensors that an mHC layer keeps, n times a plain residual network's. A row of D
+ * values is cut into blocks of 32 along D (the last may be shorter). With a = the largest
+ * magnitude in a block, its step is 2^e, e = floor(log2 a) - 6, but not below the least
+ * value of the format (fp16: e >= -24; bf16: e >= -126); a value's code is its nearest
+ * multiple of the step (ties to even) within +-127, as a signed byte; the block's scale
+ * byte is e + 127. A value is off by at most half a step, a/128 (those above 127.5 steps by
+ * less than a step), and code * step is exact in the 16-bit format it came from. A block
+ * that holds a NaN or an infinity has the scale byte 255, and all its values come back
+ * NaN. Scale bytes are 1 .. 248 and 255; a byte that the library did not write scales by
+ * 2^(byte - 127) too (0 by zero), never out of bounds.
+ *   rows      >= 0; D: a multiple of 8 in [8, 16384]
+ *   x         x_dtype [rows, D], 16-byte aligned
+ *   codes     int8    [rows, D], 16-byte aligned
+ *   scales    uint8   [rows, ceil(D / 32)]
+ * Pointers may be NULL only when rows == 0 (nothing is launched). Asynchronous on `stream`,
+ * no workspace, no allocation; outputs must not alias inputs. Errors: NULLPTR,
+ * PARAM_INVALID (also where rows need more than 2^31 - 1 workgroups of 256 octets of
+ * values), RUNTIME. */
+typedef struct mhc_checkpoint_params {
+    int64_t rows;       /* T * n for the streams, T for a [T, D] tensor */
+    int32_t D;
+    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16 */
+} mhc_checkpoint_params;
+
+/* x to codes and scales. */
+mhc_status mhc_checkpoint(const mhc_checkpoint_params* params, const uint16_t* x, int8_t* codes, uint8_t* scales,
+                          void* stream);
+
+/* Codes and scales back to x_dtype values. */
+mhc_status mhc_checkpoint_restore(const mhc_checkpoint_params* params, const int8_t* codes, const uint8_t* scales,
+                                  uint16_t* x, void* stream);
+
+/* mhc_post, bit for bit, and the checkpoint of its out (codes int8 [T, n, D], 16-byte
+ * aligned; scales uint8 [T, n, ceil(D / 32)]) written from the same registers: what
+ * mhc_checkpoint of out gives, without reading out again. Rules and errors as mhc_post's. */
+mhc_status mhc_post_checkpoint(const mhc_post_params* params, const mhc_post_tensors* tensors, int8_t* codes,
+                               uint8_t* scales, void* stream);
+
+/* mhc_pre_backward with x as its checkpoint (x_codes int8 [T, n, D], 16-byte aligned;
+ * x_scales uint8 [T, n, ceil(D / 32)], of the format params->x_f16 names): bit for bit what
+ * mhc_pre_backward gives for the restored x, without restoring it to memory. tensors->x
+ * must be NULL. The same workspace; rules and errors otherwise as mhc_pre_backward's
+ * (x_codes and x_scales may be NULL with T == 0). */
+mhc_status mhc_pre_backward_checkpoint(const mhc_pre_bwd_params* params, const mhc_pre_bwd_tensors* tensors,
+                                       const int8_t* x_codes, const uint8_t* x_scales, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ hc_post backward
+ *
+ * The gradients of mhc_post (out[t][j][d] = post[t][j] x[t][d] + sum_i comb[t][i][j]
+ * residual[t][i][d]) for the scalar whose gradient with respect to out is grad_out:
+ *   grad_x[t][d]           = sum_j post[t][j] grad_out[t][j][d]
+ *   grad_residual[t][i][d] = sum_j comb[t][i][j] grad_out[t][j][d]
+ *   grad_post[t][j]        = sum_d grad_out[t][j][d] x[t][d]
+ *   grad_comb[t][i][j]     = sum_d residual[t][i][d] grad_out[t][j][d]
+ * fp32 fused multiply-adds and sums in a fixed order (results are bitwise reproducible),
+ * one rounding to the 16-bit format. grad_residual is what mhc_pre_backward takes as
+ * grad_x_post, grad_post and grad_comb what it takes as grad_h_post and grad_h_res. x and residual, each by itself, come as 16-bit tensors or as
+ * 8-bit checkpoints (the pointers of the other form NULL).
+ *   params as for mhc_post
+ *   grad_out x_dtype [T, n, D]  16-byte aligned
+ *   x        x_dtype [T, D]     16-byte aligned, or x_codes [T, D] (16-byte aligned) and
+ *                               x_scales [T, ceil(D / 32)]
+ *   residual x_dtype [T, n, D]  16-byte aligned, or residual_codes [T, n, D] (16-byte
+ *                               aligned) and residual_scales [T, n, ceil(D / 32)]
+ *   post f32 [T, n], comb f32 [T, n, n]
+ *   grad_x x_dtype [T, D], grad_residual x_dtype [T, n, D] (16-byte aligned),
+ *   grad_post f32 [T, n], grad_comb f32 [T, n, n]: outputs, which must not alias inputs or
+ *   each other
+ * Pointers may be NULL only when T == 0 (nothing is launched). Asynchronous on `stream`, no
+ * workspace, no allocation. Errors: NULLPTR (neither form of x or of residual given, or a
+ * checkpoint without its scales), PARAM_INVALID (both forms given), RUNTIME. */
+typedef struct mhc_post_bwd_tensors {
+    const uint16_t* grad_out;
+    const uint16_t* x;
+    const uint16_t* residual;
+    const int8_t* x_codes;
+    const uint8_t* x_scales;
+    const int8_t* residual_codes;
+    const uint8_t* residual_scales;
+    const float* post;
+    const float* comb;
+    uint16_t* grad_x;
+    uint16_t* grad_residual;
+    float* grad_post;
+    float* grad_comb;
+} mhc_post_bwd_tensors;
+
+mhc_status mhc_post_backward(const mhc_post_params* params, const mhc_post_bwd_tensors* tensors, void* stream);
 
 #ifdef __cplusplus
 }

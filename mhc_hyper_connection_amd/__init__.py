@@ -12,18 +12,22 @@ the library's kernels, and nothing here falls back to another implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import math
+from collections import namedtuple
 
 from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        MHC_ERR_RUNTIME, MHC_OK, STAGES, MhcError, Params, bwd_workspace_size,
-                       forward_path, raw_inv_rms, raw_post, raw_sinkhorn,
+                       forward_path, raw_inv_rms, raw_post, raw_sinkhorn, raw_checkpoint,
+                       raw_checkpoint_restore, raw_post_checkpoint, raw_post_backward, raw_backward_checkpoint,
                        load, make_bwd_params, make_params, packed_size, raw_backward,
                        raw_forward, raw_forward_noalloc, raw_forward_timed, raw_prepack, raw_wait_status,
                        status_string,
                        version, workspace_size)
 
 __all__ = ["PreForward", "PreBackward", "mhc_pre", "mhc_pre_backward", "mhc_post", "mhc_pre_inv_rms",
-           "mhc_pre_sinkhorn", "prepack", "version",
+           "mhc_pre_sinkhorn", "prepack", "version", "Checkpoint", "mhc_checkpoint", "mhc_checkpoint_restore",
+           "mhc_post_checkpoint", "mhc_post_backward",
            "status_string", "MhcError", "FORWARD_EVENTS", "STAGES",
            "make_params", "packed_size", "workspace_size", "load",
            "MHC_OK", "MHC_ERR_NULLPTR", "MHC_ERR_PARAM_INVALID", "MHC_ERR_RUNTIME"]
@@ -64,6 +68,37 @@ def _check(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
     if t.get_device() != (device.index if device.type == "cuda" else -1):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+CHECKPOINT_BLOCK = 32   # values along the last dimension that share one scale
+
+Checkpoint = namedtuple("Checkpoint", ("codes", "scales", "dtype"))
+Checkpoint.__doc__ = """An activation tensor [..., D] kept in 8 bits (mhc_checkpoint in include/mhc.h): codes int8
+[..., D], scales uint8 [..., ceil(D / 32)], and the dtype (torch.bfloat16 or torch.float16) it came from and
+is restored to."""
+
+
+def _check_checkpoint(ck, name, dtype, shape, device):
+    if ck.dtype != dtype:
+        raise ValueError(f"{name}: a checkpoint of {ck.dtype}, expected {dtype}")
+    torch = _torch()
+    _check(ck.codes, f"{name}.codes", torch.int8, shape, device)
+    _check(ck.scales, f"{name}.scales", torch.uint8, (*shape[:-1], -(-shape[-1] // CHECKPOINT_BLOCK)), device)
+
+
+def _on_gpu(device):
+    """What a launch on `device` runs under: that device as the current one."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors on a GPU expected, got {device}")
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else contextlib.nullcontext()
+
+
+def _x_dtype(t, name):
+    torch = _torch()
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16 or torch.float16")
+    return t.dtype
 
 
 class PreForward:
@@ -286,10 +321,17 @@ class PreBackward:
 
     def __call__(self, x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms, h_mix, h_pre,
                  h_post, gamma=None, grad_x_post=None, *, sum_out=None, norm_out=None, out=None):
+        """x: the tensor, or its Checkpoint (mhc_pre_backward_checkpoint then)."""
         torch = _torch()
+        ck = x if isinstance(x, Checkpoint) else None
         T, n, D, M, dev = self.T, self.n, self.D, self.M, self.device
         bf = torch.float16 if self.x_f16 else torch.bfloat16
         f32 = torch.float32
+        if ck is not None:
+            _check_checkpoint(ck, "x", bf, (T, n, D), dev)
+            x = None
+        elif x is None:
+            raise ValueError("x: a tensor or a Checkpoint expected")
         for t, name, dt, shape in ((x, "x", bf, (T, n, D)), (phi, "phi", f32, (M, n * D)),
                                    (alpha, "alpha", f32, (3,)), (grad_h_in, "grad_h_in", bf, (T, D)),
                                    (grad_h_post, "grad_h_post", f32, (T, n)),
@@ -323,6 +365,13 @@ class PreBackward:
                 "sum_out": _ptr(sum_out) if it else None, "norm_out": _ptr(norm_out) if it else None}
         for k, v in out.items():
             ptrs[k] = _ptr(v)
+        if ck is not None:
+            with _on_gpu(dev):
+                st = raw_backward_checkpoint(self.params, ptrs, _ptr(ck.codes), _ptr(ck.scales), _ptr(self.workspace),
+                                             self.ws_bytes, _stream(dev))
+            if st != MHC_OK:
+                raise MhcError(st, "mhc_pre_backward_checkpoint")
+            return out
         st = raw_backward(self.params, ptrs, _ptr(self.workspace), self.ws_bytes, _stream(dev))
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_backward")
@@ -338,20 +387,31 @@ def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms,
     """MhcPre backward (num_iters == 0) or MhcPreSinkhorn backward (num_iters >= 1, with
     the forward's sum_out [2it, ..., n] and norm_out [2it, ..., n, n]). x: bf16 or fp16
     [T, n, D] or [B, S, n, D] (grad_h_in, grad_x_post and the returned grad_x in the same
-    format); the other per-token tensors follow x's leading dimensions. Returns dict
-    grad_x, grad_phi, grad_alpha, grad_bias (and grad_gamma when gamma is given)."""
-    lead = tuple(x.shape[:-2])
-    n, D = int(x.shape[-2]), int(x.shape[-1])
+    format); the other per-token tensors follow x's leading dimensions. x may also be the
+    Checkpoint of that tensor: bit for bit the gradients of the restored x, in a workspace of
+    the call's own (calls on several streams, or captured ones, then share nothing). Returns
+    dict grad_x, grad_phi, grad_alpha, grad_bias (and grad_gamma when gamma is given)."""
+    ck = x if isinstance(x, Checkpoint) else None
+    xt = x if ck is None else ck.codes
+    lead = tuple(xt.shape[:-2])
+    n, D = int(xt.shape[-2]), int(xt.shape[-1])
     T = math.prod(lead) if lead else 1
     f16 = x.dtype == _torch().float16
-    key = (T, n, D, hc_eps, num_iters, f16, str(x.device))
-    r = _BWD_RUNNERS.get(key)
-    if r is None:
-        r = _BWD_RUNNERS[key] = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters,
-                                            x_f16=f16, device=x.device)
+    if ck is not None:
+        if D % 8:
+            raise ValueError(f"x: D = {D}, expected a multiple of 8")
+        r = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters, x_f16=f16, device=xt.device)
+        x2 = Checkpoint(ck.codes.reshape(T, n, D), ck.scales.reshape(T, n, -(-D // CHECKPOINT_BLOCK)), ck.dtype)
+    else:
+        key = (T, n, D, hc_eps, num_iters, f16, str(x.device))
+        r = _BWD_RUNNERS.get(key)
+        if r is None:
+            r = _BWD_RUNNERS[key] = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters,
+                                                x_f16=f16, device=x.device)
+        x2 = x.reshape(T, n, D)
     M = n * n + 2 * n
     rs = lambda t, *shape: None if t is None else t.reshape(*shape)
-    out = r(x.reshape(T, n, D), phi, alpha, rs(grad_h_in, T, D), rs(grad_h_post, T, n),
+    out = r(x2, phi, alpha, rs(grad_h_in, T, D), rs(grad_h_post, T, n),
             rs(grad_h_res, T, n, n), rs(inv_rms, T), rs(h_mix, T, M), rs(h_pre, T, n),
             rs(h_post, T, n), gamma, rs(grad_x_post, T, n, D),
             sum_out=rs(sum_out, 2 * num_iters, T, n), norm_out=rs(norm_out, 2 * num_iters, T, n, n))
@@ -380,6 +440,121 @@ def mhc_post(x, residual, post, comb, *, out=None):
                   xdt == torch.float16)
     if st != MHC_OK:
         raise MhcError(st, "mhc_post")
+    return out
+
+
+def mhc_checkpoint(x, *, out=None):
+    """x (bf16 or fp16 [..., D], D a multiple of 8) as its 8-bit Checkpoint: a signed byte per
+    value and, per run of 32 values along D, a power of two (mhc_checkpoint in include/mhc.h
+    has the format: half a step of error, 1/128 of the run's largest magnitude at most; a run with a NaN
+    or an infinity comes back as NaN). out: a Checkpoint to fill. The stream is torch's
+    current stream on x's device."""
+    torch = _torch()
+    xdt = _x_dtype(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x: at least one dimension expected")
+    shape, D, dev = tuple(x.shape), int(x.shape[-1]), x.device
+    _check(x, "x", xdt, shape, dev)
+    if out is None:
+        out = Checkpoint(torch.empty(shape, dtype=torch.int8, device=dev),
+                         torch.empty((*shape[:-1], -(-D // CHECKPOINT_BLOCK)), dtype=torch.uint8, device=dev), xdt)
+    _check_checkpoint(out, "out", xdt, shape, dev)
+    with _on_gpu(dev):
+        st = raw_checkpoint(math.prod(shape[:-1]), D, xdt == torch.float16, _ptr(x), _ptr(out.codes),
+                            _ptr(out.scales), _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_checkpoint")
+    return out
+
+
+def mhc_checkpoint_restore(checkpoint, *, out=None):
+    """The 16-bit tensor [..., D] (in checkpoint.dtype) that a Checkpoint stands for."""
+    torch = _torch()
+    xdt = checkpoint.dtype
+    if xdt not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"checkpoint: of dtype {xdt}, expected torch.bfloat16 or torch.float16")
+    shape, dev = tuple(checkpoint.codes.shape), checkpoint.codes.device
+    if not shape:
+        raise ValueError("checkpoint: at least one dimension expected")
+    _check_checkpoint(checkpoint, "checkpoint", xdt, shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=xdt, device=dev)
+    _check(out, "out", xdt, shape, dev)
+    with _on_gpu(dev):
+        st = raw_checkpoint_restore(math.prod(shape[:-1]), shape[-1], xdt == torch.float16, _ptr(checkpoint.codes),
+                                    _ptr(checkpoint.scales), _ptr(out), _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_checkpoint_restore")
+    return out
+
+
+def mhc_post_checkpoint(x, residual, post, comb, *, out=None, checkpoint=None):
+    """mhc_post (same arguments, same bits) that also writes the Checkpoint of its result from
+    registers. Returns (out, checkpoint); both may be given to be filled."""
+    torch = _torch()
+    xdt = _x_dtype(residual, "residual")
+    if residual.dim() != 3:
+        raise ValueError(f"residual: shape {tuple(residual.shape)}, expected [T, n, D]")
+    T, n, D = residual.shape
+    dev = residual.device
+    _check(x, "x", xdt, (T, D), dev)
+    _check(residual, "residual", xdt, (T, n, D), dev)
+    _check(post, "post", torch.float32, (T, n), dev)
+    _check(comb, "comb", torch.float32, (T, n, n), dev)
+    if out is None:
+        out = torch.empty((T, n, D), dtype=xdt, device=dev)
+    _check(out, "out", xdt, (T, n, D), dev)
+    if checkpoint is None:
+        checkpoint = Checkpoint(torch.empty((T, n, D), dtype=torch.int8, device=dev),
+                                torch.empty((T, n, -(-D // CHECKPOINT_BLOCK)), dtype=torch.uint8, device=dev), xdt)
+    _check_checkpoint(checkpoint, "checkpoint", xdt, (T, n, D), dev)
+    with _on_gpu(dev):
+        st = raw_post_checkpoint(T, n, D, xdt == torch.float16, _ptr(x), _ptr(residual), _ptr(post), _ptr(comb), _ptr(out),
+                                 _ptr(checkpoint.codes), _ptr(checkpoint.scales), _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_post_checkpoint")
+    return out, checkpoint
+
+
+def mhc_post_backward(grad_out, x, residual, post, comb, *, out=None):
+    """mhc_post's gradients. grad_out [T, n, D] (bf16 or fp16) is the gradient with respect to
+    mhc_post's result; x ([T, D]) and residual ([T, n, D]) are what mhc_post took, each a
+    tensor of grad_out's dtype or the Checkpoint of one. Returns (or fills) dict grad_x
+    [T, D], grad_residual [T, n, D] (mhc_pre_backward's grad_x_post), grad_post f32 [T, n]
+    (its grad_h_post) and grad_comb f32 [T, n, n] (its grad_h_res). The sums run in a fixed
+    order."""
+    torch = _torch()
+    xdt = _x_dtype(grad_out, "grad_out")
+    if grad_out.dim() != 3:
+        raise ValueError(f"grad_out: shape {tuple(grad_out.shape)}, expected [T, n, D]")
+    T, n, D = grad_out.shape
+    dev = grad_out.device
+    _check(grad_out, "grad_out", xdt, (T, n, D), dev)
+    ptrs = {"grad_out": _ptr(grad_out), "post": _ptr(post), "comb": _ptr(comb)}
+    for t, name, shape in ((x, "x", (T, D)), (residual, "residual", (T, n, D))):
+        if isinstance(t, Checkpoint):
+            _check_checkpoint(t, name, xdt, shape, dev)
+            ptrs[name + "_codes"], ptrs[name + "_scales"] = _ptr(t.codes), _ptr(t.scales)
+        elif t is None:
+            raise ValueError(f"{name}: a tensor or a Checkpoint expected")
+        else:
+            _check(t, name, xdt, shape, dev)
+            ptrs[name] = _ptr(t)
+    _check(post, "post", torch.float32, (T, n), dev)
+    _check(comb, "comb", torch.float32, (T, n, n), dev)
+    want = {"grad_x": (xdt, (T, D)), "grad_residual": (xdt, (T, n, D)), "grad_post": (torch.float32, (T, n)),
+            "grad_comb": (torch.float32, (T, n, n))}
+    if out is None:
+        out = {k: torch.empty(shape, dtype=dt, device=dev) for k, (dt, shape) in want.items()}
+    elif set(out) != set(want):
+        raise ValueError(f"out must hold exactly {sorted(want)}")
+    for k, (dt, shape) in want.items():
+        _check(out[k], k, dt, shape, dev)
+        ptrs[k] = _ptr(out[k])
+    with _on_gpu(dev):
+        st = raw_post_backward(T, n, D, xdt == torch.float16, ptrs, _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_post_backward")
     return out
 
 

@@ -58,7 +58,8 @@ EXPORTS = ("mhc_version", "mhc_status_string", "mhc_pre_packed_size",
            "mhc_pre_workspace_size", "mhc_pre_prepack", "mhc_pre_forward",
            "mhc_pre_forward_timed", "mhc_pre_forward_path", "mhc_pre_backward_workspace_size",
            "mhc_pre_backward", "mhc_post", "mhc_pre_inv_rms", "mhc_pre_sinkhorn",
-           "mhc_pre_wait_status", "mhc_pre_forward_noalloc")
+           "mhc_pre_wait_status", "mhc_pre_forward_noalloc", "mhc_checkpoint", "mhc_checkpoint_restore",
+           "mhc_post_checkpoint", "mhc_post_backward", "mhc_pre_backward_checkpoint")
 
 # MHC_FORWARD_EVENTS: events of mhc_pre_forward_timed (before the first kernel, then one
 # after each of pack, projection, epilogue, hIn)
@@ -83,6 +84,18 @@ SINKHORN_TENSOR_FIELDS = ("x", "h_mix", "inv_rms", "alpha", "bias", "pre_mix", "
 
 class SinkhornTensors(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in SINKHORN_TENSOR_FIELDS]
+
+
+class CheckpointParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("x_dtype", ctypes.c_int32)]
+
+
+POST_BWD_TENSOR_FIELDS = ("grad_out", "x", "residual", "x_codes", "x_scales", "residual_codes",
+                          "residual_scales", "post", "comb", "grad_x", "grad_residual", "grad_post", "grad_comb")
+
+
+class PostBwdTensors(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in POST_BWD_TENSOR_FIELDS]
 
 
 def load(path: str | None = None):
@@ -131,6 +144,16 @@ def load(path: str | None = None):
                                         ctypes.POINTER(ctypes.c_int32)]
     lib.mhc_pre_backward.argtypes = [ctypes.POINTER(BwdParams), ctypes.POINTER(BwdTensors),
                                      ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    vp = ctypes.c_void_p
+    for name, argtypes in (
+            ("mhc_checkpoint", [ctypes.POINTER(CheckpointParams), vp, vp, vp, vp]),
+            ("mhc_checkpoint_restore", [ctypes.POINTER(CheckpointParams), vp, vp, vp, vp]),
+            ("mhc_post_checkpoint", [ctypes.POINTER(PostParams), ctypes.POINTER(PostTensors), vp, vp, vp]),
+            ("mhc_post_backward", [ctypes.POINTER(PostParams), ctypes.POINTER(PostBwdTensors), vp]),
+            ("mhc_pre_backward_checkpoint", [ctypes.POINTER(BwdParams), ctypes.POINTER(BwdTensors), vp, vp, vp,
+                                             ctypes.c_size_t, vp])):
+        getattr(lib, name).restype = ctypes.c_int32
+        getattr(lib, name).argtypes = argtypes
     if path is None:
         _lib = lib
     return lib
@@ -243,3 +266,32 @@ def raw_forward_noalloc(params: Params, ptrs: dict, stream) -> int:
     """mhc_pre_forward_noalloc: the forward with the library's per-GPU scratch array as workspace."""
     t = Tensors(*[ptrs.get(f) for f in TENSOR_FIELDS])
     return int(load().mhc_pre_forward_noalloc(ctypes.byref(params), ctypes.byref(t), stream))
+
+
+def raw_checkpoint(rows, D, x_f16, x_ptr, codes_ptr, scales_ptr, stream) -> int:
+    p = CheckpointParams(int(rows), int(D), int(bool(x_f16)))
+    return int(load().mhc_checkpoint(ctypes.byref(p), x_ptr, codes_ptr, scales_ptr, stream))
+
+
+def raw_checkpoint_restore(rows, D, x_f16, codes_ptr, scales_ptr, x_ptr, stream) -> int:
+    p = CheckpointParams(int(rows), int(D), int(bool(x_f16)))
+    return int(load().mhc_checkpoint_restore(ctypes.byref(p), codes_ptr, scales_ptr, x_ptr, stream))
+
+
+def raw_post_checkpoint(T, n, D, x_f16, x_ptr, residual_ptr, post_ptr, comb_ptr, out_ptr, codes_ptr, scales_ptr,
+                        stream) -> int:
+    p = PostParams(int(T), int(n), int(D), int(bool(x_f16)), 0)
+    t = PostTensors(x_ptr, residual_ptr, post_ptr, comb_ptr, out_ptr)
+    return int(load().mhc_post_checkpoint(ctypes.byref(p), ctypes.byref(t), codes_ptr, scales_ptr, stream))
+
+
+def raw_post_backward(T, n, D, x_f16, ptrs: dict, stream) -> int:
+    p = PostParams(int(T), int(n), int(D), int(bool(x_f16)), 0)
+    t = PostBwdTensors(*[ptrs.get(f) for f in POST_BWD_TENSOR_FIELDS])
+    return int(load().mhc_post_backward(ctypes.byref(p), ctypes.byref(t), stream))
+
+
+def raw_backward_checkpoint(params: BwdParams, ptrs: dict, codes_ptr, scales_ptr, ws_ptr, ws_bytes, stream) -> int:
+    t = BwdTensors(*[ptrs.get(f) for f in BWD_TENSOR_FIELDS])
+    return int(load().mhc_pre_backward_checkpoint(ctypes.byref(params), ctypes.byref(t), codes_ptr, scales_ptr,
+                                                  ws_ptr, ws_bytes, stream))

@@ -12,6 +12,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -20,7 +22,8 @@ LIB = os.path.join(HERE, "libmhc.so")
 ARCH = os.environ.get("MHC_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = [os.path.join(CSRC, "mhc_kernels.hip"), os.path.join(CSRC, "mhc_bwd.hip"), os.path.join(CSRC, "mhc_post.hip"),
-           os.path.join(CSRC, "mhc_scratch.hip"), os.path.join(CSRC, "mhc_api.cpp")]
+           os.path.join(CSRC, "mhc_scratch.hip"), os.path.join(CSRC, "mhc_ckpt.hip"), os.path.join(CSRC, "mhc_post_bwd.hip"),
+           os.path.join(CSRC, "mhc_api.cpp"), os.path.join(CSRC, "mhc_api_train.cpp")]
 # -amdgpu-mfma-vgpr-form=1 keeps matrix-core sources and accumulators in ordinary VGPRs.
 # With the default accumulation-register form, this toolchain's code for the projection
 # kernel produced wrong sums on gfx950 (deterministically, for every schedule tried); the
@@ -38,16 +41,26 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the ROCm toolchain is required to build libmhc.so")
 
 
-def build(verbose: bool = False) -> str:
-    """Compile the library (always recompiles). Returns the path of libmhc.so."""
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIP_FLAGS, "-shared", "-o", tmp, *SOURCES]
+def _run(cmd) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if verbose and err.strip():
+    return err
+
+
+def build(verbose: bool = False) -> str:
+    """Compile the library (always recompiles; one compiler process per source, a few at a
+    time). Returns the path of libmhc.so."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as objs:
+        out = [os.path.join(objs, os.path.basename(src) + ".o") for src in SOURCES]
+        with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as pool:
+            errs = list(pool.map(lambda so: _run([hipcc(), *HIP_FLAGS, "-c", "-o", so[1], so[0]]), zip(SOURCES, out)))
+        errs.append(_run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-o", tmp, *out]))
+    err = "\n".join(e for e in errs if e.strip())
+    if verbose and err:
         print(err, file=sys.stderr)
     os.replace(tmp, LIB)
     return LIB

@@ -254,8 +254,13 @@ mhc_status mhc_pre_backward_workspace_size(const mhc_pre_bwd_params* params, siz
     return MHC_OK;
 }
 
-mhc_status mhc_pre_backward(const mhc_pre_bwd_params* params, const mhc_pre_bwd_tensors* t,
-                            void* workspace, size_t workspace_bytes, void* stream)
+}  // extern "C"
+
+namespace {
+
+// The backward; x as t->x, or (codes non-NULL) as its 8-bit checkpoint.
+mhc_status backward_impl(const mhc_pre_bwd_params* params, const mhc_pre_bwd_tensors* t, const int8_t* codes,
+                         const uint8_t* scales, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (!params || !t) return MHC_ERR_NULLPTR;
     mhc::bwd::Geometry g;
@@ -265,19 +270,21 @@ mhc_status mhc_pre_backward(const mhc_pre_bwd_params* params, const mhc_pre_bwd_
     const bool tok = params->T > 0;
     if (!t->phi || !t->alpha || !t->grad_phi || !t->grad_alpha || !t->grad_bias || !workspace)
         return MHC_ERR_NULLPTR;
-    if (tok && (!t->x || !t->grad_h_in || !t->grad_h_post || !t->grad_h_res || !t->inv_rms ||
+    if (tok && ((!t->x && !codes) || !t->grad_h_in || !t->grad_h_post || !t->grad_h_res || !t->inv_rms ||
                 !t->h_mix || !t->h_pre || !t->h_post || !t->grad_x))
         return MHC_ERR_NULLPTR;
     if (tok && params->num_iters > 0 && (!t->sum_out || !t->norm_out)) return MHC_ERR_NULLPTR;
     if (t->gamma && !t->grad_gamma) return MHC_ERR_NULLPTR;
     const mhc::bwd::Plan plan = mhc::bwd::make_plan(g, params->T);
     if (workspace_bytes < plan.ws_bytes) return MHC_ERR_PARAM_INVALID;
-    if (!aligned(t->x, 16) || !aligned(t->grad_h_in, 16) || !aligned(t->grad_x, 16) ||
+    if ((codes ? !aligned(codes, 16) : !aligned(t->x, 16)) || !aligned(t->grad_h_in, 16) || !aligned(t->grad_x, 16) ||
         (t->grad_x_post && !aligned(t->grad_x_post, 16)) || !aligned(workspace, 256))
         return MHC_ERR_PARAM_INVALID;
 
     mhc::bwd::Args a;
-    a.x = t->x;
+    a.x = codes ? nullptr : t->x;
+    a.x_codes = codes;
+    a.x_scales = codes ? scales : nullptr;
     a.phi = t->phi;
     a.alpha = t->alpha;
     a.grad_h_in = t->grad_h_in;
@@ -307,6 +314,26 @@ mhc_status mhc_pre_backward(const mhc_pre_bwd_params* params, const mhc_pre_bwd_
     a.pgam = reinterpret_cast<float*>(ws + plan.off_pgam);
     a.glog = reinterpret_cast<double*>(ws + plan.off_glog);
     return mhc::bwd::launch_backward(plan, a, stream) == 0 ? MHC_OK : MHC_ERR_RUNTIME;
+}
+
+}  // namespace
+
+extern "C" {
+
+mhc_status mhc_pre_backward(const mhc_pre_bwd_params* params, const mhc_pre_bwd_tensors* t,
+                            void* workspace, size_t workspace_bytes, void* stream)
+{
+    return backward_impl(params, t, nullptr, nullptr, workspace, workspace_bytes, stream);
+}
+
+mhc_status mhc_pre_backward_checkpoint(const mhc_pre_bwd_params* params, const mhc_pre_bwd_tensors* t,
+                                       const int8_t* x_codes, const uint8_t* x_scales, void* workspace,
+                                       size_t workspace_bytes, void* stream)
+{
+    if (!params || !t) return MHC_ERR_NULLPTR;
+    if (params->T > 0 && (!x_codes || !x_scales)) return MHC_ERR_NULLPTR;
+    if (t->x) return MHC_ERR_PARAM_INVALID;   // x comes as its checkpoint
+    return backward_impl(params, t, x_codes, x_scales, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

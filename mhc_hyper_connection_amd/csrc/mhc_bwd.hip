@@ -25,13 +25,16 @@
 //   bwd_reduce_*        fixed-order fp64 sums of the partials (gradPhi, gradGamma) and
 //                       of the per-token terms (gradAlpha, gradBias)
 // x, gradHIn, gradXPost and gradX are bf16, or all fp16 (the guide's section 8.2: gradX
-// takes gradHIn's type); template flag H selects fp16.
+// takes gradHIn's type); template flag H selects fp16. x may also come as an 8-bit checkpoint
+// (template flag Q; mhc_ckpt_device.h): the token and main passes then read its codes and
+// block scales, 1.03 bytes a value instead of 2, and decode them in registers to the same
+// 16-bit octets. A d-block is one scale's block.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "mhc_bwd_plan.h"
-#include "mhc_device.h"
+#include "mhc_ckpt_device.h"
 
 namespace mhc {
 namespace bwd {
@@ -69,6 +72,16 @@ __device__ __forceinline__ void split_f16x8(u32x4 w, bf16x8& hi, bf16x8& lo)
     hi = __builtin_bit_cast(bf16x8, h);
     lo = __builtin_bit_cast(bf16x8, l);
 }
+// x as loaded: an octet of 16-bit values, or (Q) of codes with their block's scale byte.
+struct CodeOctet {
+    u32x2 c;
+    uint32_t s;
+};
+template <bool Q> struct XOctetOf { typedef u32x4 type; };
+template <> struct XOctetOf<true> { typedef CodeOctet type; };
+template <bool Q> using XOctet = typename XOctetOf<Q>::type;
+template <bool H> __device__ __forceinline__ u32x4 x_values(const u32x4& v) { return v; }
+template <bool H> __device__ __forceinline__ u32x4 x_values(const CodeOctet& v) { return ckpt_decode<H>(v.c, ckpt_step(v.s)); }
 // ------------------------------------------------------------------ weight pack
 
 // Unit u = (((((b * n + i) * 2 + h) * KS + ks) * 3 + p) * 64 + lane holds, for lane
@@ -238,7 +251,7 @@ __device__ __forceinline__ double wave_sum(double v)
 // One wave per token (4 per workgroup). Outputs: gMix [T][KS][3][32] (three bf16 terms
 // of each f32 value, zero past M), c3 [T], terms [3 + M][T] (fp64: the token's alpha
 // terms, then its bias terms).
-template <int N, bool H>
+template <int N, bool H, bool Q>
 __global__ void __launch_bounds__(256)
 bwd_token_kernel(Args a, int64_t T, int D)
 {
@@ -255,13 +268,23 @@ bwd_token_kernel(Args a, int64_t T, int D)
     double acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0;
-    const uint16_t* xt = a.x + t * K;
+    const uint16_t* xt = Q ? nullptr : a.x + t * K;
+    const int NB = (D + kDBlock - 1) / kDBlock;
+    const int8_t* ct = Q ? a.x_codes + t * K : nullptr;
+    const uint8_t* st = Q ? a.x_scales + t * (N * (int64_t)NB) : nullptr;
     const uint16_t* gt = a.grad_h_in + t * D;
     for (int o = lane; o < D / 8; o += 64) {
         const u32x4 gh = *reinterpret_cast<const u32x4*>(gt + 8 * o);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const u32x4 xv = *reinterpret_cast<const u32x4*>(xt + (int64_t)i * D + 8 * o);
+            XOctet<Q> xl;
+            if constexpr (Q) {
+                xl.c = *reinterpret_cast<const u32x2*>(ct + (int64_t)i * D + 8 * o);
+                xl.s = st[i * NB + (o >> 2)];
+            } else {
+                xl = *reinterpret_cast<const u32x4*>(xt + (int64_t)i * D + 8 * o);
+            }
+            const u32x4 xv = x_values<H>(xl);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 acc[i] += (double)(x16_lo<H>(gh[e]) * x16_lo<H>(xv[e]));
@@ -373,7 +396,7 @@ struct MainCfg {
 // GAMMA: gamma given (gradX scales xrsGrad, gradGamma is summed); XPOST: gradXPost given;
 // H: x, gradHIn, gradXPost and gradX in fp16 (x then enters gMix^T . x as two exact bf16
 // terms, six products instead of three).
-template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H>
+template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
 __global__ void __launch_bounds__(kThreads, GAMMA ? 2 : 3)
 bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, int64_t tasks)
 {
@@ -425,17 +448,26 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     // (where the registers allow it: no gamma, and not fp16 with gradXPost); the rest of a
     // tile's inputs after its predecessor's first phase, as with a single set
     constexpr bool DB = !GAMMA && !(XPOST && H);
-    u32x4 xv[SGN], xv2[DB ? SGN : 1], xp[SGN], gh, gh2, gmt[KS][3];
+    XOctet<Q> xv[SGN], xv2[DB ? SGN : 1];
+    u32x4 xp[SGN], gh, gh2, gmt[KS][3];
     float hp[SGN], c3;
-    auto load_xg = [&](int64_t tl, u32x4 (&xd)[SGN], u32x4& ghd) {
+    auto load_xg = [&](int64_t tl, XOctet<Q> (&xd)[SGN], u32x4& ghd) {
         const int64_t t0 = tl * kTile;
         const int ntile = (int)(T - t0 < kTile ? T - t0 : kTile);
-        const rsrc_t rx = make_rsrc(a.x + t0 * K, (int64_t)ntile * K * 2);
+        const rsrc_t rx = Q ? make_rsrc(a.x_codes + t0 * K, (int64_t)ntile * K)
+                            : make_rsrc(a.x + t0 * K, (int64_t)ntile * K * 2);
         const rsrc_t rgh = make_rsrc(a.grad_h_in + t0 * D, (int64_t)ntile * D * 2);
 #pragma unroll
         for (int s = 0; s < SGN; ++s) {
-            const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
-            xd[s] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)off, 0, 0);
+            if constexpr (Q) {   // rows past the tile and positions past D: codes 0 at a step of 0
+                const uint32_t off = dval ? (uint32_t)((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) : kOutOfRange;
+                const rsrc_t rs = make_rsrc(a.x_scales + t0 * N * nblk, (int64_t)ntile * N * nblk);
+                xd[s].c = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rx, (int)off, 0, 0));
+                xd[s].s = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (row * N + sg * SGN + s) * nblk + b, 0, 0);
+            } else {
+                const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
+                xd[s] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)off, 0, 0);
+            }
         }
         ghd = __builtin_amdgcn_raw_buffer_load_b128(rgh, dval ? (int)(((int64_t)row * D + d0) * 2) : (int)kOutOfRange, 0, 0);
     };
@@ -471,7 +503,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     const int64_t tile_end = (g + 1) * tpg < tiles ? (g + 1) * tpg : tiles;
     load_xg(g * tpg, xv, gh);
     load_rest(g * tpg);
-    auto step = [&](int64_t tile, u32x4 (&xc)[SGN], u32x4& ghc, u32x4 (&xn)[SGN], u32x4& ghn) __attribute__((always_inline)) {
+    auto step = [&](int64_t tile, XOctet<Q> (&xl)[SGN], u32x4& ghc, XOctet<Q> (&xn)[SGN], u32x4& ghn) __attribute__((always_inline)) {
         // the next tile's loads go out unconditionally (the last tile loads itself again), so
         // that every wait below has an exact count
         const int64_t nt = tile + 1 < tile_end ? tile + 1 : tile;
@@ -504,6 +536,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 for (int r = 0; r < 4; ++r) xg[4 * h + r] = acc[r];
             }
             // gradX = gradHIn hPre + xrsGrad gamma - c3 x (+ gradXPost), one RNE to x's format
+            const u32x4 xc = x_values<H>(xl[s]);
             u32x4 o;
 #pragma unroll
             for (int e2 = 0; e2 < 4; ++e2) {
@@ -511,7 +544,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
 #pragma unroll
                 for (int hl = 0; hl < 2; ++hl) {
                     const int e = 2 * e2 + hl;
-                    const float xe = hl ? x16_hi<H>(xc[s][e2]) : x16_lo<H>(xc[s][e2]);
+                    const float xe = hl ? x16_hi<H>(xc[e2]) : x16_lo<H>(xc[e2]);
                     const float ge = hl ? x16_hi<H>(ghc[e2]) : x16_lo<H>(ghc[e2]);
                     v[hl] = fmaf(ge, hp[s], GAMMA ? xg[e] * gam[GAMMA ? s : 0][e] : xg[e]);
                     v[hl] = fmaf(-c3, xe, v[hl]);
@@ -525,7 +558,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
             // x of this tile, transposed: xT[local column][token]
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                xT[tslot(s * kDBlock + 8 * grp + e, row)] = (uint16_t)((xc[s][e >> 1] >> (16 * (e & 1))) & 0xffffu);
+                xT[tslot(s * kDBlock + 8 * grp + e, row)] = (uint16_t)((xc[e >> 1] >> (16 * (e & 1))) & 0xffffu);
         }
         // gMix terms of this tile, transposed: gT[p][m][token]
 #pragma unroll
@@ -695,14 +728,14 @@ bwd_zero_kernel(Args a, int64_t MK, int64_t K, int M)
     if (idx < M) a.grad_bias[idx] = 0.f;
 }
 
-template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H>
+template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
 void launch_main(const Plan& p, const Args& a, hipStream_t st)
 {
-    hipLaunchKernelGGL((bwd_main_kernel<N, SGN, KS, GAMMA, XPOST, H>), dim3((unsigned)p.main_blocks),
+    hipLaunchKernelGGL((bwd_main_kernel<N, SGN, KS, GAMMA, XPOST, H, Q>), dim3((unsigned)p.main_blocks),
                        dim3(kThreads), 0, st, a, p.T, p.g.D, p.g.nblk, p.tpg, p.tiles, p.main_tasks);
 }
 
-template <int N, int SGN, int KS, bool H>
+template <int N, int SGN, int KS, bool H, bool Q>
 hipError_t launch_all(const Plan& p, const Args& a, hipStream_t st)
 {
     const Geometry& g = p.g;
@@ -718,15 +751,15 @@ hipError_t launch_all(const Plan& p, const Args& a, hipStream_t st)
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((bwd_token_kernel<N, H>), dim3((unsigned)p.token_blocks), dim3(256), 0, st, a, p.T, g.D);
+    hipLaunchKernelGGL((bwd_token_kernel<N, H, Q>), dim3((unsigned)p.token_blocks), dim3(256), 0, st, a, p.T, g.D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.gamma) {
-        if (a.grad_x_post) launch_main<N, SGN, KS, true, true, H>(p, a, st);
-        else launch_main<N, SGN, KS, true, false, H>(p, a, st);
+        if (a.grad_x_post) launch_main<N, SGN, KS, true, true, H, Q>(p, a, st);
+        else launch_main<N, SGN, KS, true, false, H, Q>(p, a, st);
     } else {
-        if (a.grad_x_post) launch_main<N, SGN, KS, false, true, H>(p, a, st);
-        else launch_main<N, SGN, KS, false, false, H>(p, a, st);
+        if (a.grad_x_post) launch_main<N, SGN, KS, false, true, H, Q>(p, a, st);
+        else launch_main<N, SGN, KS, false, false, H, Q>(p, a, st);
     }
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -751,12 +784,14 @@ int launch_backward(const Plan& p, const Args& a, void* stream)
         hipLaunchKernelGGL(bwd_zero_kernel, dim3((unsigned)((MK + 255) / 256)), dim3(256), 0, st, a, MK, g.K, g.M);
         return (int)hipGetLastError();
     }
-    if (g.n == 4 && g.SGN == 4 && g.KS == 1)
-        return (int)(g.x_f16 ? launch_all<4, 4, 1, true>(p, a, st) : launch_all<4, 4, 1, false>(p, a, st));
-    if (g.n == 6 && g.SGN == 2 && g.KS == 2)
-        return (int)(g.x_f16 ? launch_all<6, 2, 2, true>(p, a, st) : launch_all<6, 2, 2, false>(p, a, st));
-    if (g.n == 8 && g.SGN == 2 && g.KS == 3)
-        return (int)(g.x_f16 ? launch_all<8, 2, 3, true>(p, a, st) : launch_all<8, 2, 3, false>(p, a, st));
+    const bool q = a.x_codes != nullptr;
+#define MHC_BWD(NV, SV, KV)                                                                          \
+    (int)(q ? (g.x_f16 ? launch_all<NV, SV, KV, true, true>(p, a, st) : launch_all<NV, SV, KV, false, true>(p, a, st)) \
+            : (g.x_f16 ? launch_all<NV, SV, KV, true, false>(p, a, st) : launch_all<NV, SV, KV, false, false>(p, a, st)))
+    if (g.n == 4 && g.SGN == 4 && g.KS == 1) return MHC_BWD(4, 4, 1);
+    if (g.n == 6 && g.SGN == 2 && g.KS == 2) return MHC_BWD(6, 2, 2);
+    if (g.n == 8 && g.SGN == 2 && g.KS == 3) return MHC_BWD(8, 2, 3);
+#undef MHC_BWD
     return (int)hipErrorInvalidValue;
 }
 

@@ -160,7 +160,9 @@ inline Plan make_plan(const Geometry& g, int64_t T)
 
 // Device pointers of one backward call.
 struct Args {
-    const uint16_t* x;
+    const uint16_t* x;         // [T, n, D], or NULL: x_codes and x_scales
+    const int8_t* x_codes;     // [T, n, D] codes of x's 8-bit checkpoint, or NULL
+    const uint8_t* x_scales;   // [T, n, ceil(D / 32)] its scales
     const float* phi;
     const float* alpha;
     const uint16_t* grad_h_in;

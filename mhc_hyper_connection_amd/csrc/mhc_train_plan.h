@@ -1,0 +1,53 @@
+// mhc_train_plan.h -- geometry and launch interface of the sub-layer's training operators:
+// the 8-bit checkpoints, hc_post with a checkpoint, and hc_post's backward.
+//
+// Host-side and plain C++ (no HIP headers), like mhc_plan.h.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace mhc {
+
+constexpr int kCkptBlock = 32;       // values per scale
+
+// Scale bytes of a row of D values.
+inline int ckpt_blocks(int D) { return (D + kCkptBlock - 1) / kCkptBlock; }
+// Octets of a row with its last block padded to a whole one: what the kernels that work on
+// quads of lanes per block count in.
+inline int ckpt_octets(int D) { return 4 * ckpt_blocks(D); }
+
+// Workgroups of 256 threads over rows x padded octets, or -1 where that passes the grid's
+// 2^31 - 1.
+inline int64_t octet_blocks(int64_t rows, int D)
+{
+    const int64_t P = ckpt_octets(D);
+    if (rows > ((int64_t)0x7fffffff * 256) / P) return -1;
+    return (rows * P + 255) / 256;
+}
+
+struct PostBwdArgs {
+    const uint16_t* grad_out;      // [T, n, D]
+    const uint16_t* x;             // [T, D], or NULL: x_codes, x_scales
+    const int8_t* x_codes;
+    const uint8_t* x_scales;
+    const uint16_t* residual;      // [T, n, D], or NULL: r_codes, r_scales
+    const int8_t* r_codes;
+    const uint8_t* r_scales;
+    const float* post;             // [T, n]
+    const float* comb;             // [T, n, n]
+    uint16_t* grad_x;              // [T, D]
+    uint16_t* grad_residual;       // [T, n, D]
+    float* grad_post;              // [T, n]
+    float* grad_comb;              // [T, n, n]
+};
+
+// Implemented in mhc_ckpt.hip and mhc_post_bwd.hip. Each returns 0 or the HIP error code.
+int launch_checkpoint(int64_t rows, int D, const uint16_t* x, int8_t* codes, uint8_t* scales, int x_f16, void* stream);
+int launch_checkpoint_restore(int64_t rows, int D, const int8_t* codes, const uint8_t* scales, uint16_t* x, int x_f16,
+                              void* stream);
+int launch_post_checkpoint(int64_t T, int n, int D, const uint16_t* x, const uint16_t* residual, const float* post,
+                           const float* comb, uint16_t* out, int8_t* codes, uint8_t* scales, int x_f16, void* stream);
+int launch_post_backward(int64_t T, int n, int D, const PostBwdArgs& a, int x_f16, void* stream);
+
+}  // namespace mhc
