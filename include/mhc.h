@@ -481,8 +481,8 @@ mhc_status mhc_post(const mhc_post_params* params, const mhc_post_tensors* tenso
  *   scales    uint8   [rows, ceil(D / 32)]
  * Pointers may be NULL only when rows == 0 (nothing is launched). Asynchronous on `stream`,
  * no workspace, no allocation; outputs must not alias inputs. Errors: NULLPTR,
- * PARAM_INVALID (also where rows need more than 2^31 - 1 workgroups of 256 octets of
- * values), RUNTIME. */
+ * PARAM_INVALID (also where rows hold more than 2^32 - 256 octets of values, each row
+ * counted with its last block whole), RUNTIME. */
 typedef struct mhc_checkpoint_params {
     int64_t rows;       /* T * n for the streams, T for a [T, D] tensor */
     int32_t D;
@@ -554,6 +554,79 @@ typedef struct mhc_post_bwd_tensors {
 } mhc_post_bwd_tensors;
 
 mhc_status mhc_post_backward(const mhc_post_params* params, const mhc_post_bwd_tensors* tensors, void* stream);
+
+/* ------------------------------------------------------------------ gated projection
+ *
+ * The gated projection of a sub-layer's feed-forward block, between mhc_pre_forward (whose
+ * hIn it takes) and mhc_post (which takes the block's result, after the projection back to
+ * D, a plain matrix product of the caller's):
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) (.) u
+ *   act(g) = g sigmoid(g)                                          (MHC_ACT_SILU)
+ *            g sigmoid(2 sqrt(2/pi) (g + 0.044715 g^3))            (MHC_ACT_GELU_TANH: GELU's
+ *                                                                   tanh form)
+ * in one kernel: g and u stay in registers (fp32 sums of exact 16-bit products), one
+ * rounding to h's format. Few tokens are bound by reading the weights, many by the matrix cores.
+ *   T >= 0 tokens; D a multiple of 8 in [8, 16384]; F a multiple of 8 in [8, 65536];
+ *   ceil(T / 128) * ceil(F / 64) < 2^23
+ *   x      x_dtype [T, D]    w_gate, w_up x_dtype [F, D] (a row per result, as a linear
+ *   layer keeps its weight)  h x_dtype [T, F]            all 16-byte aligned
+ * With T == 0 nothing is launched, and x and h may be NULL. Asynchronous on `stream`, no
+ * workspace, no allocation; results are bitwise reproducible for the same sizes. h must not
+ * alias the inputs. Errors: NULLPTR, PARAM_INVALID, RUNTIME. */
+#define MHC_ACT_SILU 0
+#define MHC_ACT_GELU_TANH 1
+
+typedef struct mhc_glu_params {
+    int64_t T;
+    int32_t D;
+    int32_t F;
+    int32_t act;        /* MHC_ACT_SILU or MHC_ACT_GELU_TANH */
+    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16: every tensor's format */
+} mhc_glu_params;
+
+typedef struct mhc_glu_tensors {
+    const uint16_t* x;
+    const uint16_t* w_gate;
+    const uint16_t* w_up;
+    uint16_t* h;
+} mhc_glu_tensors;
+
+mhc_status mhc_glu(const mhc_glu_params* params, const mhc_glu_tensors* tensors, void* stream);
+
+/* Its backward, from x (or x's 8-bit checkpoint) and the weights alone: g and u are computed
+ * again and never stored. With dh = grad_h,
+ *   dg = dh (.) u (.) act'(g),  du = dh (.) act(g)         rounded once to x_dtype
+ *   grad_x = dg Wg + du Wu,  grad_w_gate = dg^T x,  grad_w_up = du^T x
+ * (fp32 sums, one rounding to x_dtype), and h again where asked for: the gradient of the
+ * projection behind it needs it, so a caller need not keep it.
+ *   grad_h x_dtype [T, F]; x x_dtype [T, D], or x_codes int8 [T, D] and x_scales uint8
+ *   [T, ceil(D / 32)] (then x NULL; the values are restored into the workspace);
+ *   w_gate, w_up x_dtype [F, D]; grad_x x_dtype [T, D]; grad_w_gate, grad_w_up x_dtype
+ *   [F, D] (overwritten, not added to); h x_dtype [T, F] or NULL. All but x_scales 16-byte
+ *   aligned; outputs must not alias inputs or each other.
+ * With T == 0 the weights' gradients are set to zero, and the per-token tensors may be NULL.
+ * The workspace (of mhc_glu_backward_workspace_size bytes, 256-byte aligned; from_checkpoint
+ * 1 where x comes as its checkpoint, else 0) holds [dg | du], the restored x and partial
+ * sums; it needs no initialisation, and calls that may overlap need distinct ones.
+ * Asynchronous on `stream`; every sum in a fixed order. Errors: NULLPTR, PARAM_INVALID,
+ * RUNTIME. */
+typedef struct mhc_glu_bwd_tensors {
+    const uint16_t* grad_h;
+    const uint16_t* x;
+    const int8_t* x_codes;
+    const uint8_t* x_scales;
+    const uint16_t* w_gate;
+    const uint16_t* w_up;
+    uint16_t* grad_x;
+    uint16_t* grad_w_gate;
+    uint16_t* grad_w_up;
+    uint16_t* h;
+} mhc_glu_bwd_tensors;
+
+mhc_status mhc_glu_backward_workspace_size(const mhc_glu_params* params, int32_t from_checkpoint, size_t* bytes);
+
+mhc_status mhc_glu_backward(const mhc_glu_params* params, const mhc_glu_bwd_tensors* tensors, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@ from collections import namedtuple
 from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        MHC_ERR_RUNTIME, MHC_OK, STAGES, MhcError, Params, bwd_workspace_size,
                        forward_path, raw_inv_rms, raw_post, raw_sinkhorn, raw_checkpoint,
+                       ACTS, glu_backward_workspace_size, make_glu_params, raw_glu, raw_glu_backward,
                        raw_checkpoint_restore, raw_post_checkpoint, raw_post_backward, raw_backward_checkpoint,
                        load, make_bwd_params, make_params, packed_size, raw_backward,
                        raw_forward, raw_forward_noalloc, raw_forward_timed, raw_prepack, raw_wait_status,
@@ -27,7 +28,7 @@ from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
 
 __all__ = ["PreForward", "PreBackward", "mhc_pre", "mhc_pre_backward", "mhc_post", "mhc_pre_inv_rms",
            "mhc_pre_sinkhorn", "prepack", "version", "Checkpoint", "mhc_checkpoint", "mhc_checkpoint_restore",
-           "mhc_post_checkpoint", "mhc_post_backward",
+           "mhc_post_checkpoint", "mhc_post_backward", "mhc_glu", "mhc_glu_backward",
            "status_string", "MhcError", "FORWARD_EVENTS", "STAGES",
            "make_params", "packed_size", "workspace_size", "load",
            "MHC_OK", "MHC_ERR_NULLPTR", "MHC_ERR_PARAM_INVALID", "MHC_ERR_RUNTIME"]
@@ -555,6 +556,86 @@ def mhc_post_backward(grad_out, x, residual, post, comb, *, out=None):
         st = raw_post_backward(T, n, D, xdt == torch.float16, ptrs, _stream(dev))
     if st != MHC_OK:
         raise MhcError(st, "mhc_post_backward")
+    return out
+
+
+def _glu_shapes(x_shape, w_gate, w_up, act):
+    if act not in ACTS:
+        raise ValueError(f"act: {act!r}, expected one of {sorted(ACTS)}")
+    if w_gate.dim() != 2:
+        raise ValueError(f"w_gate: shape {tuple(w_gate.shape)}, expected [F, D]")
+    F, D = w_gate.shape
+    if not x_shape or x_shape[-1] != D:
+        raise ValueError(f"x: shape {tuple(x_shape)}, expected [..., {D}]")
+    return math.prod(x_shape[:-1]), int(D), int(F)
+
+
+def mhc_glu(x, w_gate, w_up, *, act="silu", out=None):
+    """The gated projection of a feed-forward block, h = act(x w_gate^T) * (x w_up^T), in one
+    kernel: x [..., D] (mhc_pre's hIn), w_gate and w_up [F, D], all bf16 or all fp16; returns
+    (or fills) h [..., F] in that dtype. act: "silu" or "gelu_tanh". Products accumulate in
+    fp32, g and u are never stored, one rounding to h. The stream is torch's current stream on
+    x's device."""
+    torch = _torch()
+    xdt = _x_dtype(x, "x")
+    T, D, F = _glu_shapes(x.shape, w_gate, w_up, act)
+    lead, dev = tuple(x.shape[:-1]), x.device
+    _check(x, "x", xdt, (*lead, D), dev)
+    _check(w_gate, "w_gate", xdt, (F, D), dev)
+    _check(w_up, "w_up", xdt, (F, D), dev)
+    if out is None:
+        out = torch.empty((*lead, F), dtype=xdt, device=dev)
+    _check(out, "out", xdt, (*lead, F), dev)
+    with _on_gpu(dev):
+        st = raw_glu(make_glu_params(T, D, F, act, xdt == torch.float16),
+                     {"x": _ptr(x), "w_gate": _ptr(w_gate), "w_up": _ptr(w_up), "h": _ptr(out)}, _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_glu")
+    return out
+
+
+def mhc_glu_backward(grad_h, x, w_gate, w_up, *, act="silu", need_h=False, out=None):
+    """mhc_glu's gradients, from x (the tensor, or its Checkpoint) and the weights: the two
+    projections are computed again. grad_h [..., F] in x's dtype. Returns (or fills) dict
+    grad_x [..., D], grad_w_gate and grad_w_up [F, D] (overwritten), all in x's dtype, and
+    with need_h also h [..., F], which the gradient of the projection behind it needs. The
+    workspace is the call's own."""
+    torch = _torch()
+    xdt = _x_dtype(grad_h, "grad_h")
+    ck = x if isinstance(x, Checkpoint) else None
+    if x is None:
+        raise ValueError("x: a tensor or a Checkpoint expected")
+    shape = tuple((x if ck is None else ck.codes).shape)
+    T, D, F = _glu_shapes(shape, w_gate, w_up, act)
+    lead, dev = shape[:-1], grad_h.device
+    _check(grad_h, "grad_h", xdt, (*lead, F), dev)
+    if ck is None:
+        _check(x, "x", xdt, shape, dev)
+    else:
+        _check_checkpoint(ck, "x", xdt, shape, dev)
+    _check(w_gate, "w_gate", xdt, (F, D), dev)
+    _check(w_up, "w_up", xdt, (F, D), dev)
+    want = {"grad_x": shape, "grad_w_gate": (F, D), "grad_w_up": (F, D)}
+    if need_h:
+        want["h"] = (*lead, F)
+    if out is None:
+        out = {k: torch.empty(v, dtype=xdt, device=dev) for k, v in want.items()}
+    elif set(out) != set(want):
+        raise ValueError(f"out must hold exactly {sorted(want)}")
+    for k, v in want.items():
+        _check(out[k], k, xdt, v, dev)
+    ptrs = {"grad_h": _ptr(grad_h), "w_gate": _ptr(w_gate), "w_up": _ptr(w_up), **{k: _ptr(out[k]) for k in want}}
+    if ck is None:
+        ptrs["x"] = _ptr(x)
+    else:
+        ptrs["x_codes"], ptrs["x_scales"] = _ptr(ck.codes), _ptr(ck.scales)
+    with _on_gpu(dev):
+        params = make_glu_params(T, D, F, act, xdt == torch.float16)
+        ws_bytes = glu_backward_workspace_size(params, ck is not None)
+        ws = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
+        st = raw_glu_backward(params, ptrs, _ptr(ws), ws_bytes, _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_glu_backward")
     return out
 
 

@@ -59,7 +59,8 @@ EXPORTS = ("mhc_version", "mhc_status_string", "mhc_pre_packed_size",
            "mhc_pre_forward_timed", "mhc_pre_forward_path", "mhc_pre_backward_workspace_size",
            "mhc_pre_backward", "mhc_post", "mhc_pre_inv_rms", "mhc_pre_sinkhorn",
            "mhc_pre_wait_status", "mhc_pre_forward_noalloc", "mhc_checkpoint", "mhc_checkpoint_restore",
-           "mhc_post_checkpoint", "mhc_post_backward", "mhc_pre_backward_checkpoint")
+           "mhc_post_checkpoint", "mhc_post_backward", "mhc_pre_backward_checkpoint", "mhc_glu",
+           "mhc_glu_backward_workspace_size", "mhc_glu_backward")
 
 # MHC_FORWARD_EVENTS: events of mhc_pre_forward_timed (before the first kernel, then one
 # after each of pack, projection, epilogue, hIn)
@@ -96,6 +97,27 @@ POST_BWD_TENSOR_FIELDS = ("grad_out", "x", "residual", "x_codes", "x_scales", "r
 
 class PostBwdTensors(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in POST_BWD_TENSOR_FIELDS]
+
+
+ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+class GluParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int32), ("F", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32)]
+
+
+GLU_TENSOR_FIELDS = ("x", "w_gate", "w_up", "h")
+GLU_BWD_TENSOR_FIELDS = ("grad_h", "x", "x_codes", "x_scales", "w_gate", "w_up", "grad_x", "grad_w_gate",
+                         "grad_w_up", "h")
+
+
+class GluTensors(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in GLU_TENSOR_FIELDS]
+
+
+class GluBwdTensors(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in GLU_BWD_TENSOR_FIELDS]
 
 
 def load(path: str | None = None):
@@ -151,7 +173,11 @@ def load(path: str | None = None):
             ("mhc_post_checkpoint", [ctypes.POINTER(PostParams), ctypes.POINTER(PostTensors), vp, vp, vp]),
             ("mhc_post_backward", [ctypes.POINTER(PostParams), ctypes.POINTER(PostBwdTensors), vp]),
             ("mhc_pre_backward_checkpoint", [ctypes.POINTER(BwdParams), ctypes.POINTER(BwdTensors), vp, vp, vp,
-                                             ctypes.c_size_t, vp])):
+                                             ctypes.c_size_t, vp]),
+            ("mhc_glu", [ctypes.POINTER(GluParams), ctypes.POINTER(GluTensors), vp]),
+            ("mhc_glu_backward_workspace_size", [ctypes.POINTER(GluParams), ctypes.c_int32,
+                                                 ctypes.POINTER(ctypes.c_size_t)]),
+            ("mhc_glu_backward", [ctypes.POINTER(GluParams), ctypes.POINTER(GluBwdTensors), vp, ctypes.c_size_t, vp])):
         getattr(lib, name).restype = ctypes.c_int32
         getattr(lib, name).argtypes = argtypes
     if path is None:
@@ -295,3 +321,25 @@ def raw_backward_checkpoint(params: BwdParams, ptrs: dict, codes_ptr, scales_ptr
     t = BwdTensors(*[ptrs.get(f) for f in BWD_TENSOR_FIELDS])
     return int(load().mhc_pre_backward_checkpoint(ctypes.byref(params), ctypes.byref(t), codes_ptr, scales_ptr,
                                                   ws_ptr, ws_bytes, stream))
+
+
+def make_glu_params(T, D, F, act, x_f16) -> GluParams:
+    return GluParams(int(T), int(D), int(F), ACTS[act], int(bool(x_f16)))
+
+
+def raw_glu(params: GluParams, ptrs: dict, stream) -> int:
+    t = GluTensors(*[ptrs.get(f) for f in GLU_TENSOR_FIELDS])
+    return int(load().mhc_glu(ctypes.byref(params), ctypes.byref(t), stream))
+
+
+def glu_backward_workspace_size(params: GluParams, from_checkpoint) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().mhc_glu_backward_workspace_size(ctypes.byref(params), int(bool(from_checkpoint)), ctypes.byref(out))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_glu_backward_workspace_size")
+    return int(out.value)
+
+
+def raw_glu_backward(params: GluParams, ptrs: dict, ws_ptr, ws_bytes, stream) -> int:
+    t = GluBwdTensors(*[ptrs.get(f) for f in GLU_BWD_TENSOR_FIELDS])
+    return int(load().mhc_glu_backward(ctypes.byref(params), ctypes.byref(t), ws_ptr, ws_bytes, stream))

@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "../../include/mhc.h"
+#include "mhc_glu_plan.h"
 #include "mhc_plan.h"
 #include "mhc_train_plan.h"
 
@@ -31,6 +32,14 @@ mhc_status check_post(const mhc_post_params* p)
     if (p->T < 0 || (p->n != 4 && p->n != 6 && p->n != 8) || !is_row(p->D)) return MHC_ERR_PARAM_INVALID;
     if (!is_x_dtype(p->x_dtype) || p->reserved != 0) return MHC_ERR_PARAM_INVALID;
     return mhc::octet_blocks(p->T, p->D) < 0 ? MHC_ERR_PARAM_INVALID : MHC_OK;
+}
+
+mhc_status check_glu(const mhc_glu_params* p, mhc::glu::Geometry* g)
+{
+    if (!p) return MHC_ERR_NULLPTR;
+    if (!is_x_dtype(p->x_dtype)) return MHC_ERR_PARAM_INVALID;
+    if (!mhc::glu::make_geometry(p->T, p->D, p->F, p->act, p->x_dtype == MHC_DTYPE_F16, g)) return MHC_ERR_PARAM_INVALID;
+    return MHC_OK;
 }
 
 }  // namespace
@@ -91,6 +100,76 @@ mhc_status mhc_post_backward(const mhc_post_params* params, const mhc_post_bwd_t
                                 t->grad_comb};
     return status_of(mhc::launch_post_backward(params->T, params->n, params->D, a, params->x_dtype == MHC_DTYPE_F16,
                                                stream));
+}
+
+mhc_status mhc_glu(const mhc_glu_params* params, const mhc_glu_tensors* t, void* stream)
+{
+    if (!params || !t) return MHC_ERR_NULLPTR;
+    mhc::glu::Geometry g;
+    const mhc_status st = check_glu(params, &g);
+    if (st != MHC_OK) return st;
+    if (!t->w_gate || !t->w_up || (g.T > 0 && (!t->x || !t->h))) return MHC_ERR_NULLPTR;
+    if (!aligned(t->x, 16) || !aligned(t->w_gate, 16) || !aligned(t->w_up, 16) || !aligned(t->h, 16))
+        return MHC_ERR_PARAM_INVALID;
+    if (g.T == 0) return MHC_OK;
+    mhc::glu::Args a = {};
+    a.x = t->x;
+    a.w_gate = t->w_gate;
+    a.w_up = t->w_up;
+    a.h = t->h;
+    return status_of(mhc::glu::launch_glu(g, a, stream));
+}
+
+mhc_status mhc_glu_backward_workspace_size(const mhc_glu_params* params, int32_t from_checkpoint, size_t* bytes)
+{
+    if (!params || !bytes) return MHC_ERR_NULLPTR;
+    mhc::glu::Geometry g;
+    const mhc_status st = check_glu(params, &g);
+    if (st != MHC_OK) return st;
+    if (from_checkpoint != 0 && from_checkpoint != 1) return MHC_ERR_PARAM_INVALID;
+    *bytes = mhc::glu::make_backward_plan(g, from_checkpoint == 1).ws_bytes;
+    return MHC_OK;
+}
+
+mhc_status mhc_glu_backward(const mhc_glu_params* params, const mhc_glu_bwd_tensors* t, void* workspace,
+                            size_t workspace_bytes, void* stream)
+{
+    if (!params || !t) return MHC_ERR_NULLPTR;
+    mhc::glu::Geometry g;
+    const mhc_status st = check_glu(params, &g);
+    if (st != MHC_OK) return st;
+    if (!t->w_gate || !t->w_up || !t->grad_w_gate || !t->grad_w_up) return MHC_ERR_NULLPTR;
+    const bool tok = g.T > 0, ck = t->x_codes || t->x_scales;
+    if (tok && (!workspace || !t->grad_h || !t->grad_x)) return MHC_ERR_NULLPTR;
+    if (t->x && ck) return MHC_ERR_PARAM_INVALID;
+    if (tok && !t->x && (!t->x_codes || !t->x_scales)) return MHC_ERR_NULLPTR;
+    const void* wide[] = {t->grad_h, t->x, t->x_codes, t->w_gate, t->w_up, t->grad_x, t->grad_w_gate, t->grad_w_up, t->h};
+    for (const void* q : wide)
+        if (!aligned(q, 16)) return MHC_ERR_PARAM_INVALID;
+    const mhc::glu::BackwardPlan p = mhc::glu::make_backward_plan(g, ck);
+    if (tok && (!aligned(workspace, 256) || workspace_bytes < p.ws_bytes)) return MHC_ERR_PARAM_INVALID;
+    if (ck && mhc::octet_blocks(g.T, g.D) < 0) return MHC_ERR_PARAM_INVALID;
+    char* const ws = static_cast<char*>(workspace);
+    mhc::glu::Args a = {};
+    a.x = t->x;
+    a.w_gate = t->w_gate;
+    a.w_up = t->w_up;
+    a.h = t->h;
+    a.grad_h = t->grad_h;
+    a.grad_x = t->grad_x;
+    a.grad_w_gate = t->grad_w_gate;
+    a.grad_w_up = t->grad_w_up;
+    if (tok) {
+        a.dgu = reinterpret_cast<uint16_t*>(ws + p.off_dgu);
+        a.part = reinterpret_cast<float*>(ws + p.off_part);
+        if (ck) {
+            uint16_t* const x = reinterpret_cast<uint16_t*>(ws + p.off_x);
+            const int e = mhc::launch_checkpoint_restore(g.T, g.D, t->x_codes, t->x_scales, x, g.f16, stream);
+            if (e != 0) return MHC_ERR_RUNTIME;
+            a.x = x;
+        }
+    }
+    return status_of(mhc::glu::launch_glu_backward(g, p, a, stream));
 }
 
 }  // extern "C"

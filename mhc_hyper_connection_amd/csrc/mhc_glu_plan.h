@@ -1,0 +1,129 @@
+// mhc_glu_plan.h -- geometry, launch shapes and workspace layout of the gated projection
+// h = act(x Wg^T) (.) (x Wu^T) and its backward.
+//
+// Host-side and plain C++ (no HIP headers), like mhc_plan.h.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace mhc {
+namespace glu {
+
+constexpr int kMaxD = 16384;
+constexpr int kMaxF = 65536;
+constexpr int kBK = 32;              // reduction positions per LDS stage
+constexpr int kCUs = 256;
+
+struct Geometry {
+    int64_t T = 0;
+    int D = 0, F = 0;
+    int act = 0;       // 0 SiLU, 1 GELU (tanh form)
+    int f16 = 0;
+};
+
+inline bool make_geometry(int64_t T, int D, int F, int act, int f16, Geometry* g)
+{
+    if (T < 0 || T > (int64_t)1 << 31) return false;
+    if (D < 8 || D % 8 != 0 || D > kMaxD) return false;
+    if (F < 8 || F % 8 != 0 || F > kMaxF) return false;
+    if (act != 0 && act != 1) return false;
+    g->T = T;
+    g->D = D;
+    g->F = F;
+    g->act = act;
+    g->f16 = f16;
+    // tiles of 128 tokens x 64 f: workgroups within a grid's 2^32 - 1 threads
+    return ((T + 127) / 128) * ((F + 63) / 64) < (int64_t)1 << 23;
+}
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// A tiled product of `rows` x `cols` results over `steps` stages of kBK: with 256 x 256 tiles (one
+// workgroup of 8 waves per compute unit) or 128 x 128 tiles (4 waves, two workgroups per
+// compute unit), and split along the reduction into `split` parts whose fp32 sums a second
+// kernel joins.
+struct Tiling {
+    bool large = false;
+    int64_t na = 0, nb = 0;   // tiles along rows and columns
+    int split = 1;
+    int64_t steps = 0;        // stages in all
+    int64_t per = 0;          // stages of a part
+    int64_t blocks() const { return na * nb * split; }
+};
+// groups: independent products of this size in one launch (2 for the two weight gradients)
+inline Tiling make_tiling(int64_t rows, int64_t cols, int64_t steps, int groups, bool may_split)
+{
+    Tiling t;
+    t.steps = steps;
+    t.large = cdiv(rows, 256) * cdiv(cols, 256) * groups >= kCUs * 3 / 4;
+    const int64_t tile = t.large ? 256 : 128;
+    t.na = cdiv(rows, tile);
+    t.nb = cdiv(cols, tile) * groups;
+    // few tiles and a long reduction: parts of at least 8 stages, until two workgroups per
+    // compute unit are reached
+    int64_t s = 1;
+    if (may_split && !t.large && t.na * t.nb > 0) {
+        s = cdiv(2 * kCUs, t.na * t.nb);
+        if (s > steps / 8) s = steps / 8;
+        if (s > 64) s = 64;
+        if (s < 1) s = 1;
+    }
+    t.per = cdiv(steps, s);
+    if (t.per < 1) t.per = 1;
+    t.split = (int)cdiv(steps, t.per);
+    if (t.split < 1) t.split = 1;
+    return t;
+}
+
+struct BackwardPlan {
+    Tiling act, dx, dw;       // recomputed projections; x's gradient; the weights' gradients
+    size_t off_dgu = 0, off_x = 0, off_part = 0, ws_bytes = 0;
+};
+
+inline Tiling forward_tiling(const Geometry& g) { return make_tiling(2 * (int64_t)g.F, g.T, cdiv(g.D, kBK), 1, false); }
+
+inline BackwardPlan make_backward_plan(const Geometry& g, bool checkpoint)
+{
+    BackwardPlan p;
+    p.act = forward_tiling(g);
+    p.dx = make_tiling(g.D, g.T, 2 * cdiv(g.F, kBK), 1, true);
+    p.dw = make_tiling(g.D, g.F, cdiv(g.T, kBK), 2, true);
+    size_t off = 0;
+    p.off_dgu = off;
+    off = align_up(off + (size_t)g.T * 2 * (size_t)g.F * 2, 256);
+    p.off_x = off;
+    if (checkpoint) off = align_up(off + (size_t)g.T * (size_t)g.D * 2, 256);
+    p.off_part = off;
+    size_t part = 0;
+    if (p.dx.split > 1) part = (size_t)p.dx.split * (size_t)g.T * (size_t)g.D * 4;
+    if (p.dw.split > 1) {
+        const size_t w = (size_t)p.dw.split * 2 * (size_t)g.F * (size_t)g.D * 4;
+        if (w > part) part = w;
+    }
+    off = align_up(off + part, 256);
+    p.ws_bytes = off;
+    return p;
+}
+
+struct Args {
+    const uint16_t* x;        // [T, D]
+    const uint16_t* w_gate;   // [F, D]
+    const uint16_t* w_up;     // [F, D]
+    uint16_t* h;              // [T, F] (the backward: may be NULL)
+    // backward
+    const uint16_t* grad_h;   // [T, F]
+    uint16_t* grad_x;         // [T, D]
+    uint16_t* grad_w_gate;    // [F, D]
+    uint16_t* grad_w_up;      // [F, D]
+    uint16_t* dgu;            // [T, 2F] gradients of the two projections' results
+    float* part;
+};
+
+// Implemented in mhc_glu.hip. Each returns 0 or the HIP error code.
+int launch_glu(const Geometry& g, const Args& a, void* stream);
+int launch_glu_backward(const Geometry& g, const BackwardPlan& p, const Args& a, void* stream);
+
+}  // namespace glu
+}  // namespace mhc

@@ -17,12 +17,12 @@ inline int ckpt_blocks(int D) { return (D + kCkptBlock - 1) / kCkptBlock; }
 // quads of lanes per block count in.
 inline int ckpt_octets(int D) { return 4 * ckpt_blocks(D); }
 
-// Workgroups of 256 threads over rows x padded octets, or -1 where that passes the grid's
-// 2^31 - 1.
+// Workgroups of 256 threads over rows x padded octets, or -1 where that passes a grid's
+// 2^32 - 1 threads.
 inline int64_t octet_blocks(int64_t rows, int D)
 {
     const int64_t P = ckpt_octets(D);
-    if (rows > ((int64_t)0x7fffffff * 256) / P) return -1;
+    if (rows > (int64_t)0xffffff * 256 / P) return -1;
     return (rows * P + 255) / 256;
 }
 

@@ -138,3 +138,65 @@ def test_python_pre_backward_checks():
     raises("x: a tensor or a Checkpoint", r, None, *args())
     raises("GPU", r, zck(T, n, D), *args())
     raises("multiple of 8", mhc.mhc_pre_backward, zck(T, n, 60), *args())
+
+
+GLU = dict.fromkeys(("x", "w_gate", "w_up", "h"), FAKE)
+GLU_BWD = dict.fromkeys(("grad_h", "x", "w_gate", "w_up", "grad_x", "grad_w_gate", "grad_w_up", "h"), FAKE)
+
+
+def glu(T=4, D=64, F=128, act=0, dt=0, **over):
+    return B.raw_glu(B.GluParams(T, D, F, act, dt), {**GLU, **over}, None)
+
+
+def glu_b(T=4, D=64, F=128, act=0, dt=0, ws=FAKE, ws_bytes=1 << 50, **over):
+    return B.raw_glu_backward(B.GluParams(T, D, F, act, dt), {**GLU_BWD, **over}, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("fn", [glu, glu_b])
+def test_glu_refusals(fn):
+    for over in (dict(T=-1), dict(T=(1 << 31) + 1), dict(D=0), dict(D=12), dict(D=16392), dict(F=0), dict(F=20), dict(F=65544), dict(act=2),
+                 dict(act=-1), dict(dt=2), dict(T=1 << 30, F=65536)):
+        assert fn(**over) == BAD, over
+    for f in ("x", "w_gate", "w_up", *(("h",) if fn is glu else ("grad_h", "grad_x", "grad_w_gate", "grad_w_up"))):
+        assert fn(**{f: None}) == NULL, f
+        assert fn(**{f: FAKE + 8}) == BAD, f
+
+
+def test_glu_backward_forms_and_workspace():
+    assert glu_b(x_codes=FAKE) == glu_b(x_scales=FAKE) == BAD                                   # both forms of x
+    assert glu_b(x=None, x_codes=FAKE) == glu_b(x=None, x_scales=FAKE) == NULL
+    assert glu_b(x=None, x_codes=FAKE + 8, x_scales=FAKE) == glu_b(h=FAKE + 2) == BAD
+    assert glu_b(ws=None) == NULL and glu_b(ws=FAKE + 16) == BAD
+    p = B.make_glu_params(4, 64, 128, "silu", False)
+    need, need_ck = B.glu_backward_workspace_size(p, False), B.glu_backward_workspace_size(p, True)
+    assert need >= 4 * 2 * 128 * 2 and need_ck >= need + 4 * 64 * 2
+    assert glu_b(ws_bytes=need - 1) == BAD
+    assert B.glu_backward_workspace_size(B.make_glu_params(0, 64, 128, "silu", False), True) == 0
+    out = ctypes.c_size_t(0)
+    size = B.load().mhc_glu_backward_workspace_size
+    assert size(None, 0, ctypes.byref(out)) == size(ctypes.byref(p), 0, None) == NULL
+    assert size(ctypes.byref(p), 2, ctypes.byref(out)) == BAD
+    assert glu(T=0, x=None, h=None) == OK
+    assert B.load().mhc_glu(None, None, None) == B.load().mhc_glu_backward(None, None, None, 0, None) == NULL
+
+
+def test_python_glu_checks():
+    x, wg, wu, gh = z(3, 64, dt=bf), z(128, 64, dt=bf), z(128, 64, dt=bf), z(3, 128, dt=bf)
+    f, b = mhc.mhc_glu, mhc.mhc_glu_backward
+    raises("act", f, x, wg, wu, act="relu")
+    raises("x: dtype", f, x.float(), wg, wu)
+    raises("w_up: dtype", f, x, wg, wu.to(f16))
+    raises("w_up: shape", f, x, wg, wu[:64])
+    raises("x: shape", f, z(3, 72, dt=bf), wg, wu)
+    raises("w_gate: shape", f, x, wg[0], wu)
+    raises("contiguous", f, x, z(64, 128, dt=bf).t(), wu)
+    raises("out: shape", f, x, wg, wu, out=z(3, 64, dt=bf))
+    raises("GPU", f, x, wg, wu)
+    raises("act", b, gh, x, wg, wu, act="")
+    raises("grad_h: shape", b, gh[:, :64], x, wg, wu)
+    raises("x: dtype", b, gh, x.to(f16), wg, wu)
+    raises("x: a checkpoint of", b, gh, zck(3, 64, dt=f16), wg, wu)
+    raises("x: a tensor or a Checkpoint", b, gh, None, wg, wu)
+    raises("exactly", b, gh, x, wg, wu, out={"grad_x": x})
+    raises("exactly", b, gh, x, wg, wu, need_h=True, out={"grad_x": x, "grad_w_gate": wg, "grad_w_up": wu})
+    raises("GPU", b, gh, zck(3, 64), wg, wu)
