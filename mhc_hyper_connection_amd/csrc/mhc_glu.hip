@@ -9,7 +9,7 @@
 // registers; dg and du are rounded once to the 16-bit format (they are the operands of the next
 // products), and so is each result.
 //
-// Four products share one tiled kernel (tile_kernel): C = A B over a reduction of kBK = 32
+// Four products share one tiled kernel (tile_kernel): C = A B over a reduction of kBK = 64
 // positions per stage. The operand whose rows become C's rows is always the one whose
 // index is contiguous in the result, so that a lane of the matrix-core result (4 consecutive
 // rows of one column) holds consecutive results.
@@ -85,36 +85,76 @@ __device__ __forceinline__ void wait_loads_and_barrier()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
-// Workgroup -> tile. Workgroups b, b + 8, .. run on one XCD; each XCD takes a contiguous
-// run of the tile order, which walks the columns of kGroup rows of tiles before the next
-// rows: the tiles in flight on an XCD then share kGroup row operands and a few column
-// operands in its L2.
-constexpr int kGroup = 4;
-__device__ __forceinline__ bool tile_of(int64_t na, int64_t nb, int64_t* a, int64_t* b)
-{
-    const int64_t total = na * nb, per = (total + 7) / 8;
-    const int64_t t = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= per || t >= total) return false;
-    const int64_t group = t / (kGroup * nb), r = t - group * kGroup * nb;
-    const int64_t rows = na - group * kGroup < kGroup ? na - group * kGroup : kGroup;
-    *a = group * kGroup + r % rows;
-    *b = r / rows;
-    return true;
-}
-
 struct TileArgs {
     Args t;
     int64_t T;
     int D, F, act;
-    int64_t na, nb;
-    int64_t steps, per;   // stages in all, stages of a part
-    float* part;          // NULL, or the parts' sums [split][...] in fp32
+    int64_t na, nb;        // tiles along rows and columns
+    int64_t whole;         // tiles that one workgroup takes whole: the first of the tile order
+    int64_t steps, per;    // stages in all, stages of a part of the other tiles
+    int split;             // parts of each of those
+    float* part;           // their fp32 results, [tile][part][block of results][thread]
 };
 
-// WA x WB waves of IA x IB 16 x 16 results each. LDS: a ring of 4 stages of both operands.
-// At step k a wave waits for its own loads of stage k, meets the others (whose reads of
-// stage k - 1 are then done as well), sends off the loads of stage k + 3 into the slot of stage k - 1
-// and multiplies stage k. Loads past the end of the reduction bring zeros.
+// Workgroup -> tile and part. Workgroups b, b + 8, .. run on one XCD; each XCD takes a
+// contiguous run of the tile order, which walks the columns of kGroup rows of tiles before the
+// next rows: the tiles in flight on an XCD then share kGroup row operands and a few column
+// operands in its L2 (4 against 2, 8 and 16: within 2 % of the best for every product). The
+// split tiles follow, the same part of neighbouring tiles side by side.
+constexpr int kGroup = 4;
+struct Unit {
+    int64_t a, b, tile;
+    int part;
+};
+__device__ __forceinline__ void place(int64_t t, int64_t na, int64_t nb, Unit* u)
+{
+    const int64_t group = t / (kGroup * nb), r = t - group * kGroup * nb;
+    const int64_t rows = na - group * kGroup < kGroup ? na - group * kGroup : kGroup;
+    u->tile = t;
+    u->a = group * kGroup + r % rows;
+    u->b = r / rows;
+}
+__device__ __forceinline__ bool unit_of(const TileArgs& p, Unit* u)
+{
+    const int64_t first = (p.whole + 7) / 8;          // of the whole tiles, on each XCD
+    const int64_t xcd = blockIdx.x % 8, i = blockIdx.x / 8;
+    if (i < first) {
+        const int64_t t = xcd * first + i;
+        if (t >= p.whole) return false;
+        u->part = -1;
+        place(t, p.na, p.nb, u);
+        return true;
+    }
+    const int64_t rest = p.na * p.nb - p.whole, units = rest * p.split, per = (units + 7) / 8;
+    const int64_t v = xcd * per + (i - first);
+    if (i - first >= per || v >= units) return false;
+    u->part = (int)(v / rest);
+    place(p.whole + v % rest, p.na, p.nb, u);
+    return true;
+}
+
+// Four rows of one column of kGradX's or kGradW's result, at row d and column c of the tile's half
+// (`up`: Wu's gradient). [column][row], rows contiguous: grad_x [T][D], or a weight's
+// gradient [F][D].
+template <int MODE, bool H>
+__device__ __forceinline__ void store_rows(const TileArgs& p, int up, int64_t d, int64_t c, f32x4 v)
+{
+    uint16_t* const out = MODE == kGradX ? p.t.grad_x : (up ? p.t.grad_w_up : p.t.grad_w_gate);
+    if (c < (MODE == kGradX ? p.T : (int64_t)p.F) && d < p.D)
+        *reinterpret_cast<u32x2*>(out + c * p.D + d) = u32x2{pack_x16<H>(v[0], v[1]), pack_x16<H>(v[2], v[3])};
+}
+
+// WA x WB waves of IA x IB 16 x 16 results each. A stage of the reduction is kBK = 64 positions,
+// so that a direct load takes whole 128-byte lines of an operand contiguous along the
+// reduction (with 32 the L2 saw twice the requests, and they bound the loop). LDS holds
+// three stages of A and two of B. A wave's operands of half a stage (32 positions, the depth
+// of one matrix-core instruction) are read while it multiplies the half before:
+//   first half of stage m    read the second half of m, send off A's loads of stage m + 2
+//   wait for the loads of stage m + 1, meet the other waves (whose reads of stage m are then done)
+//   second half of stage m   read the first half of m + 1, send off B's loads of stage m + 2
+// The reads and loads are dealt out between the products (loads sent off together held up
+// every wave's next products: 6 % of the whole). Loads past the end of the reduction bring
+// zeros.
 template <int MODE, bool H, int WA, int WB, int IA, int IB>
 __global__ void __launch_bounds__(64 * WA * WB, 2)
 tile_kernel(TileArgs p)
@@ -122,17 +162,18 @@ tile_kernel(TileArgs p)
     constexpr int NW = WA * WB;
     constexpr int AR = 16 * WA * IA, BC = 16 * WB * IB;          // rows and columns of the tile
     constexpr int ASZ = AR * 2 * kBK, BSZ = BC * 2 * kBK;        // bytes of a stage
-    constexpr int QA = AR / 16 / NW, QB = BC / 16 / NW;          // direct loads of a wave per stage
-    constexpr int R = 4;
+    constexpr int QA = ASZ / 1024 / NW, QB = BSZ / 1024 / NW;    // direct loads of a wave per stage
+    constexpr int RA = 3, RB = 2;                                // stages in LDS
     constexpr bool A_ACROSS = MODE == kGradX || MODE == kGradW;  // A contiguous across the reduction
     constexpr bool B_ACROSS = MODE == kGradW;
     constexpr bool GATED = MODE == kForward || MODE == kRecompute;
-    static_assert(QA * 16 * NW == AR && QB * 16 * NW == BC, "whole direct loads");
+    static_assert(QA * 1024 * NW == ASZ && QB * 1024 * NW == BSZ, "whole direct loads");
     static_assert(!GATED || QA % 2 == 0, "a direct load is of one of the two weights");
-    __shared__ __attribute__((aligned(1024))) char lds[R * (ASZ + BSZ)];
+    __shared__ __attribute__((aligned(1024))) char lds[RA * ASZ + RB * BSZ];
 
-    int64_t ta, tb;
-    if (!tile_of(p.na, p.nb, &ta, &tb)) return;   // the padding of the last run of tiles
+    Unit unit;
+    if (!unit_of(p, &unit)) return;   // the padding of an XCD's run
+    const int64_t ta = unit.a, tb = unit.b;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wa = wave / WB, wb = wave % WB;
     const int j = lane & 15, kg = lane >> 4;
@@ -146,13 +187,14 @@ tile_kernel(TileArgs p)
     const int64_t b0 = (tb - up * nbh) * BC;                     // first token, or f
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds));
-    const uint32_t ldsb = lds0 + R * ASZ;
+    const uint32_t ldsb = lds0 + RA * ASZ;
 
-    // --- loads. Contiguous along the reduction: LDS rows of 64 bytes, a load is 16 rows; the 16-byte
-    // chunk c of row r sits at c ^ s(r), with s so that the 16 rows of an operand read meet
-    // all banks: s = (r / 4) % 4 for 16 rows in a run, (r / 8) % 4 for the gated rows, which
-    // are read 4 of every 8. Across: rows of one reduction position, chunk c of row k at
-    // c ^ 2 ((k % 4) + 4 ((k / 8) % 2)).
+    // --- loads, 1 KiB each. Contiguous along the reduction: 8 LDS rows of 128 bytes; the 16-byte
+    // chunk c of row r sits at c ^ s(r), s = (r / 2) % 8 for 16 rows in a run. The gated rows
+    // are read 4 of every 8, and s = 2 ((r / 8) % 4) + (r / 2) % 2 numbers those the same way. The
+    // LDS serves a 16-byte read in four turns of 16 lanes, the first of lanes 0-3, 12-15 and
+    // 20-27, and each turn then meets all 64 banks once. Across: 64 / C rows of C chunks,
+    // chunk c of position k at c ^ 2 ((k % 4) + 4 ((k / 8) % 2)). No conflicts are counted.
     constexpr int CA = AR / 8, CB = BC / 8;                      // chunks of an across row
     uint32_t va[QA], vb[QB];
     int ka[QA], kb[QB];                                          // the chunk's place in the stage (along)
@@ -164,7 +206,7 @@ tile_kernel(TileArgs p)
             va[q] = (uint32_t)((int64_t)k * D * 2) + (uint32_t)(a0 + 8 * c) * 2;
             ka[q] = 0;
         } else {
-            const int r = 16 * i + lane / 4, c = (lane & 3) ^ ((r >> 3) & 3);
+            const int r = 8 * i + lane / 8, c = (lane & 7) ^ (2 * ((r >> 3) & 3) + ((r >> 1) & 1));
             va[q] = (uint32_t)(r % (AR / 2)) * (uint32_t)D * 2 + 16 * c;
             ka[q] = 8 * c;
         }
@@ -177,7 +219,7 @@ tile_kernel(TileArgs p)
             vb[q] = (uint32_t)k * (uint32_t)F * 4 + (uint32_t)((int64_t)up * F + b0 + 8 * c) * 2;
             kb[q] = 0;
         } else {
-            const int r = 16 * i + lane / 4, c = (lane & 3) ^ ((r >> 2) & 3);
+            const int r = 8 * i + lane / 8, c = (lane & 7) ^ ((r >> 1) & 7);
             vb[q] = (uint32_t)r * (uint32_t)(MODE == kGradX ? 2 * F : D) * 2 + 16 * c;
             kb[q] = 8 * c;
         }
@@ -193,35 +235,33 @@ tile_kernel(TileArgs p)
         db = descriptor(p.t.dgu + b0 * 2 * F, (uint32_t)(brow * 2 * F * 2));
     }
     auto rows_left = [](int64_t n, int64_t k) { return (uint32_t)(n - k <= 0 ? 0 : (n - k < kBK ? n - k : kBK)); };
-    auto issue = [&](int64_t step, int slot) __attribute__((always_inline)) {
-        const uint32_t la = lds0 + slot * ASZ + wave * 1024, lb = ldsb + slot * BSZ + wave * 1024;
+    // load q of this wave's part of a stage of A, of B
+    auto issue_a = [&](int64_t step, int slot, int q) __attribute__((always_inline)) {
+        const uint32_t at = lds0 + slot * ASZ + (wave + q * NW) * 1024;
         if constexpr (GATED) {
             const int k = (int)(step * kBK);
-#pragma unroll
-            for (int q = 0; q < QA; ++q)
-                buffer_to_lds(q < QA / 2 ? dag : dau, k + ka[q] < D ? va[q] + 2 * k : kOutOfRange, la + q * NW * 1024);
-#pragma unroll
-            for (int q = 0; q < QB; ++q)
-                buffer_to_lds(db, k + kb[q] < D ? vb[q] + 2 * k : kOutOfRange, lb + q * NW * 1024);
+            buffer_to_lds(q < QA / 2 ? dag : dau, k + ka[q] < D ? va[q] + 2 * k : kOutOfRange, at);
         } else if constexpr (MODE == kGradX) {
             const int hf = step >= half_steps ? 1 : 0;
             const int64_t k = (step - (int64_t)hf * half_steps) * kBK;
-            const uint32_t left = rows_left(F, k);
-            const u32x4 da = descriptor((hf ? p.t.w_up : p.t.w_gate) + k * D, left * (uint32_t)D * 2);
-#pragma unroll
-            for (int q = 0; q < QA; ++q) buffer_to_lds(da, va[q], la + q * NW * 1024);
-#pragma unroll
-            for (int q = 0; q < QB; ++q)
-                buffer_to_lds(db, k + kb[q] < F ? vb[q] + (uint32_t)(2 * (k + (int64_t)hf * F)) : kOutOfRange, lb + q * NW * 1024);
+            buffer_to_lds(descriptor((hf ? p.t.w_up : p.t.w_gate) + k * D, rows_left(F, k) * (uint32_t)D * 2), va[q], at);
         } else {
-            const int64_t k = step * kBK;
-            const uint32_t left = rows_left(T, k);
-            const u32x4 da = descriptor(p.t.x + (left ? k : 0) * D, left * (uint32_t)D * 2);
-            const u32x4 dd = descriptor(p.t.dgu + (left ? k : 0) * 2 * F, left * (uint32_t)F * 4);
-#pragma unroll
-            for (int q = 0; q < QA; ++q) buffer_to_lds(da, va[q], la + q * NW * 1024);
-#pragma unroll
-            for (int q = 0; q < QB; ++q) buffer_to_lds(dd, vb[q], lb + q * NW * 1024);
+            const uint32_t left = rows_left(T, step * kBK);
+            buffer_to_lds(descriptor(p.t.x + (left ? step * kBK : 0) * D, left * (uint32_t)D * 2), va[q], at);
+        }
+    };
+    auto issue_b = [&](int64_t step, int slot, int q) __attribute__((always_inline)) {
+        const uint32_t at = ldsb + slot * BSZ + (wave + q * NW) * 1024;
+        if constexpr (GATED) {
+            const int k = (int)(step * kBK);
+            buffer_to_lds(db, k + kb[q] < D ? vb[q] + 2 * k : kOutOfRange, at);
+        } else if constexpr (MODE == kGradX) {
+            const int hf = step >= half_steps ? 1 : 0;
+            const int64_t k = (step - (int64_t)hf * half_steps) * kBK;
+            buffer_to_lds(db, k + kb[q] < F ? vb[q] + (uint32_t)(2 * (k + (int64_t)hf * F)) : kOutOfRange, at);
+        } else {
+            const uint32_t left = rows_left(T, step * kBK);
+            buffer_to_lds(descriptor(p.t.dgu + (left ? step * kBK : 0) * 2 * F, left * (uint32_t)F * 4), vb[q], at);
         }
     };
 
@@ -230,10 +270,10 @@ tile_kernel(TileArgs p)
     // are 8 consecutive f.
     const uint32_t aoff = A_ACROSS ? (uint32_t)((8 * kg + (j >> 2)) * (AR * 2) +
                                                 (((IA * 2 * wa + ((j & 3) >> 1)) ^ (2 * ((j >> 2) + 4 * (kg & 1)))) << 4) + (j & 1) * 8)
-                                   : (uint32_t)((16 * wa * IA / 2 + 8 * (j >> 2) + (j & 3)) * 64 + ((kg ^ (j >> 2)) << 4));
+                                   : (uint32_t)((16 * wa * IA / 2 + 8 * (j >> 2) + (j & 3)) * 128 + ((kg ^ (j >> 1)) << 4));
     const uint32_t boff = B_ACROSS ? (uint32_t)((8 * kg + (j >> 2)) * (BC * 2) +
                                                 (((IB * 2 * wb + ((j & 3) >> 1)) ^ (2 * ((j >> 2) + 4 * (kg & 1)))) << 4) + (j & 1) * 8)
-                                   : (uint32_t)((16 * wb * IB + j) * 64 + ((kg ^ (j >> 2)) << 4));
+                                   : (uint32_t)((16 * wb * IB + j) * 128 + ((kg ^ (j >> 1)) << 4));
     auto read_along = [](uint32_t at) { return *(const MHC_LDS s16x8*)(uintptr_t)at; };
     auto read_across = [](uint32_t at, int row_bytes) {
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MHC_LDS s16x4*)(uintptr_t)at);
@@ -247,72 +287,122 @@ tile_kernel(TileArgs p)
 #pragma unroll
         for (int q = 0; q < IB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto multiply = [&](int slot) __attribute__((always_inline)) {
-        const uint32_t la = lds0 + slot * ASZ, lb = ldsb + slot * BSZ;
-        s16x8 bf[IB];
-#pragma unroll
-        for (int q = 0; q < IB; ++q) {
-            if constexpr (B_ACROSS) bf[q] = read_across(lb + (boff ^ (q << 5)), BC * 2);
-            else bf[q] = read_along(lb + boff + q * 1024);
-        }
-#pragma unroll
-        for (int i = 0; i < IA; ++i) {
-            s16x8 af;
-            if constexpr (A_ACROSS) af = read_across(la + (aoff ^ (i << 5)), AR * 2);
-            else {   // gated: results 0 .. IA/2 - 1 are the gate's, the rest the up projection's
-                const int i2 = i % (IA / 2);
-                af = read_along(la + aoff + (i < IA / 2 ? 0 : AR / 2 * 64) + (i2 / 2) * 2048 + (i2 % 2) * 256);
-            }
-#pragma unroll
-            for (int q = 0; q < IB; ++q) acc[i][q] = mfma<H>(af, bf[q], acc[i][q]);
+    struct Operands {
+        s16x8 a[IA], b[IB];
+    };
+    // the across reads' addresses, one instruction each, are formed anew for every half stage:
+    // kept, all their sums with the slots would take more registers than there are
+    uint32_t anow = aoff, bnow = boff;
+    auto read_a = [&](int slot, int half, int i, Operands& o) __attribute__((always_inline)) {
+        const uint32_t la = lds0 + slot * ASZ;
+        if constexpr (A_ACROSS) o.a[i] = read_across((anow ^ (i << 5)) + (la + half * 32 * (AR * 2)), AR * 2);
+        else {   // gated: results 0 .. IA/2 - 1 are the gate's, the rest the up projection's
+            const int i2 = i % (IA / 2);
+            o.a[i] = read_along(la + (aoff ^ (half << 6)) + (i < IA / 2 ? 0 : AR / 2 * 128) + (i2 / 2) * 4096 + (i2 % 2) * 512);
         }
     };
+    auto read_b = [&](int slot, int half, int q, Operands& o) __attribute__((always_inline)) {
+        const uint32_t lb = ldsb + slot * BSZ;
+        if constexpr (B_ACROSS) o.b[q] = read_across((bnow ^ (q << 5)) + (lb + half * 32 * (BC * 2)), BC * 2);
+        else o.b[q] = read_along(lb + (boff ^ (half << 6)) + q * 2048);
+    };
 
-    const int64_t k0 = (int64_t)blockIdx.y * p.per, k1 = k0 + p.per < p.steps ? k0 + p.per : p.steps;
-    issue(k0, 0);
-    issue(k0 + 1, 1);
-    issue(k0 + 2, 2);
-    for (int64_t k = k0; k < k1; k += R) {
+    const int64_t m0 = unit.part < 0 ? 0 : unit.part * p.per;
+    const int64_t m1 = unit.part < 0 || m0 + p.per > p.steps ? p.steps : m0 + p.per;
+    Operands op[2];
 #pragma unroll
-        for (int s = 0; s < R; ++s) {
-            if (k + s < k1) {
-                wait_loads_and_barrier<2 * (QA + QB)>();
-                issue(k + s + 3, (s + 3) % R);
-                multiply(s);
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int q = 0; q < QA; ++q) issue_a(m0 + s, s, q);
+#pragma unroll
+        for (int q = 0; q < QB; ++q) issue_b(m0 + s, s, q);
+    }
+    wait_loads_and_barrier<QA + QB>();
+#pragma unroll
+    for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]);
+#pragma unroll
+    for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]);
+    // half of stage m (slot numbers s = m - m0): the products of `now` in IA parts, the reads of the next half
+    // and the loads dealt out over them in order
+    auto half = [&](int64_t m, int s, int h, const Operands& now, Operands& next) __attribute__((always_inline)) {
+        constexpr int READS = IA + IB;
+        const int rs = s + h;   // the stage whose half 1 - h is read
+        if constexpr (A_ACROSS) asm volatile("" : "+v"(anow));
+        if constexpr (B_ACROSS) asm volatile("" : "+v"(bnow));
+#pragma unroll
+        for (int i = 0; i < IA; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int r = i * READS / IA; r < (i + 1) * READS / IA; ++r) {
+                if (r < IB) read_b(rs % RB, 1 - h, r, next);
+                else read_a(rs % RA, 1 - h, r - IB, next);
+            }
+#pragma unroll
+            for (int q = 0; q < IB; ++q) acc[i][q] = mfma<H>(now.a[i], now.b[q], acc[i][q]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (h == 0) {
+#pragma unroll
+                for (int q = i * QA / IA; q < (i + 1) * QA / IA; ++q) issue_a(m + 2, (s + 2) % RA, q);
+            } else {
+#pragma unroll
+                for (int q = i * QB / IA; q < (i + 1) * QB / IA; ++q) issue_b(m + 2, s % RB, q);
+            }
+        }
+    };
+    for (int64_t m = m0; m < m1; m += RA * RB) {
+#pragma unroll
+        for (int s = 0; s < RA * RB; ++s) {
+            if (m + s < m1) {
+                half(m + s, s, 0, op[0], op[1]);
+                wait_loads_and_barrier<QA>();
+                half(m + s, s, 1, op[1], op[0]);
             }
         }
     }
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");   // no load is left behind in LDS at the end
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // no load is left behind in LDS at the end
 
     // --- results: lane (j, kg) holds rows 4 kg .. 4 kg + 3 of column j of each 16 x 16 block
     if constexpr (GATED) {
+        const int64_t f0 = a0 + 16 * wa * IA / 2 + 8 * kg, t0 = b0 + 16 * wb * IB + j;
+        u32x4 dh[IB][IA / 4];
+        if constexpr (MODE == kRecompute) {   // all of them on their way before the first is used
+#pragma unroll
+            for (int q = 0; q < IB; ++q)
+#pragma unroll
+                for (int i = 0; i < IA / 4; ++i) {
+                    const int64_t t = t0 + 16 * q < T ? t0 + 16 * q : T - 1, f = f0 + 32 * i < F ? f0 + 32 * i : 0;
+                    dh[q][i] = *reinterpret_cast<const u32x4*>(p.t.grad_h + t * F + f);
+                }
+        }
 #pragma unroll
         for (int q = 0; q < IB; ++q) {
-            const int64_t t = b0 + 16 * (wb * IB + q) + j;
+            const int64_t t = t0 + 16 * q;
 #pragma unroll
             for (int i = 0; i < IA / 4; ++i) {
-                const int64_t f = a0 + 16 * wa * IA / 2 + 32 * i + 8 * kg;
-                if (t < T && f < F) {
-                    u32x4 dh = {0u, 0u, 0u, 0u};
-                    if constexpr (MODE == kRecompute) dh = *reinterpret_cast<const u32x4*>(p.t.grad_h + t * F + f);
-                    u32x4 hv, gv, uv;
+                const int64_t f = f0 + 32 * i;
+                u32x4 hv, gv, uv;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float hh[2], dg[2], du[2];
+                for (int e = 0; e < 4; ++e) {
+                    float hh[2], dg[2], du[2];
 #pragma unroll
-                        for (int l = 0; l < 2; ++l) {
-                            const int r = 2 * e + l;                            // f + r
-                            const float gg = acc[2 * i + r / 4][q][r % 4], uu = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
-                            const Act ac = activation(gg, p.act);
-                            const float d = l ? x16_hi<H>(dh[e]) : x16_lo<H>(dh[e]);
-                            hh[l] = ac.a * uu;
+                    for (int l = 0; l < 2; ++l) {
+                        const int r = 2 * e + l;                            // f + r
+                        const float gg = acc[2 * i + r / 4][q][r % 4], uu = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
+                        const Act ac = activation(gg, p.act);
+                        hh[l] = ac.a * uu;
+                        if constexpr (MODE == kRecompute) {
+                            const float d = l ? x16_hi<H>(dh[q][i][e]) : x16_lo<H>(dh[q][i][e]);
                             dg[l] = d * uu * ac.da;
                             du[l] = d * ac.a;
                         }
-                        hv[e] = pack_x16<H>(hh[0], hh[1]);
+                    }
+                    hv[e] = pack_x16<H>(hh[0], hh[1]);
+                    if constexpr (MODE == kRecompute) {
                         gv[e] = pack_x16<H>(dg[0], dg[1]);
                         uv[e] = pack_x16<H>(du[0], du[1]);
                     }
+                }
+                if (t < T && f < F) {
                     if (MODE == kForward || p.t.h) *reinterpret_cast<u32x4*>(p.t.h + t * F + f) = hv;
                     if constexpr (MODE == kRecompute) {
                         *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + f) = gv;
@@ -321,38 +411,45 @@ tile_kernel(TileArgs p)
                 }
             }
         }
+    } else if (unit.part < 0) {
+#pragma unroll
+        for (int q = 0; q < IB; ++q)
+#pragma unroll
+            for (int i = 0; i < IA; ++i)
+                store_rows<MODE, H>(p, up, a0 + 16 * (wa * IA + i) + 4 * kg, b0 + 16 * (wb * IB + q) + j, acc[i][q]);
     } else {
-        // [column][row], rows contiguous: grad_x [T][D], or a weight's gradient [F][D]
-        const int64_t ncol = MODE == kGradX ? T : F;
-        uint16_t* const out = MODE == kGradX ? p.t.grad_x : (up ? p.t.grad_w_up : p.t.grad_w_gate);
-        float* const part = p.part ? p.part + ((int64_t)blockIdx.y * (MODE == kGradX ? T : 2 * (int64_t)F) + (int64_t)up * F) * D : nullptr;
+        f32x4* const part = reinterpret_cast<f32x4*>(p.part) +
+                            ((unit.tile - p.whole) * p.split + unit.part) * (IA * IB * 64 * NW) + tid;
 #pragma unroll
-        for (int q = 0; q < IB; ++q) {
-            const int64_t c = b0 + 16 * (wb * IB + q) + j;
+        for (int i = 0; i < IA; ++i)
 #pragma unroll
-            for (int i = 0; i < IA; ++i) {
-                const int64_t d = a0 + 16 * (wa * IA + i) + 4 * kg;
-                if (c < ncol && d < D) {
-                    if (part) *reinterpret_cast<f32x4*>(part + c * D + d) = acc[i][q];
-                    else *reinterpret_cast<u32x2*>(out + c * D + d) = u32x2{pack_x16<H>(acc[i][q][0], acc[i][q][1]), pack_x16<H>(acc[i][q][2], acc[i][q][3])};
-                }
-            }
-        }
+            for (int q = 0; q < IB; ++q) part[(i * IB + q) * 64 * NW] = acc[i][q];
     }
 }
 
-// out = the parts' sum in their order, rounded once; 4 results a thread. The second output
-// takes the results from `first` on.
-template <bool H>
-__global__ void __launch_bounds__(256)
-join_kernel(const float* __restrict__ part, int split, int64_t n, uint16_t* __restrict__ out0, uint16_t* __restrict__ out1, int64_t first)
+// The split tiles: a result is its parts' sum in their order, rounded once. Workgroup (tile,
+// i): block row i of the tile's waves, laid out as tile_kernel left it.
+template <int MODE, bool H, int WA, int WB, int IA, int IB>
+__global__ void __launch_bounds__(64 * WA * WB)
+join_kernel(TileArgs p)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
-    f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
-    for (int s = 1; s < split; ++s) v += *reinterpret_cast<const f32x4*>(part + s * n + i);
-    uint16_t* o = i < first ? out0 + i : out1 + (i - first);
-    *reinterpret_cast<u32x2*>(o) = u32x2{pack_x16<H>(v[0], v[1]), pack_x16<H>(v[2], v[3])};
+    constexpr int NW = WA * WB, AR = 16 * WA * IA, BC = 16 * WB * IB;
+    Unit u;
+    place(p.whole + blockIdx.x, p.na, p.nb, &u);
+    const int i = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wa = wave / WB, wb = wave % WB;
+    const int64_t nbh = MODE == kGradW ? p.nb / 2 : p.nb;
+    const int up = MODE == kGradW && u.b >= nbh ? 1 : 0;
+    const f32x4* part = reinterpret_cast<const f32x4*>(p.part) + (int64_t)blockIdx.x * p.split * (IA * IB * 64 * NW) + tid;
+    f32x4 v[IB];
+#pragma unroll
+    for (int q = 0; q < IB; ++q) v[q] = part[(i * IB + q) * 64 * NW];
+    for (int s = 1; s < p.split; ++s)
+#pragma unroll
+        for (int q = 0; q < IB; ++q) v[q] += part[(int64_t)s * (IA * IB * 64 * NW) + (i * IB + q) * 64 * NW];
+#pragma unroll
+    for (int q = 0; q < IB; ++q)
+        store_rows<MODE, H>(p, up, u.a * AR + 16 * (wa * IA + i) + 4 * (lane >> 4),
+                            (u.b - up * nbh) * BC + 16 * (wb * IB + q) + (lane & 15), v[q]);
 }
 
 // An empty sum over tokens: both weights' gradients are zero.
@@ -365,36 +462,34 @@ zero_kernel(uint16_t* __restrict__ a, uint16_t* __restrict__ b, int64_t n)
     *reinterpret_cast<u32x4*>(b + i) = u32x4{0u, 0u, 0u, 0u};
 }
 
+template <int MODE, bool H, int WA, int WB, int IA, int IB>
+hipError_t launch_shape(const Geometry& g, const Tiling& t, const Args& a, hipStream_t st)
+{
+    const TileArgs p = {a, g.T, g.D, g.F, g.act, t.na, t.nb, t.whole, t.steps, t.per, t.split, a.part};
+    hipLaunchKernelGGL((tile_kernel<MODE, H, WA, WB, IA, IB>), dim3((unsigned)t.blocks()), dim3(64 * WA * WB), 0, st, p);
+    hipError_t e = hipGetLastError();
+    if constexpr (MODE == kGradX || MODE == kGradW) {
+        if (e == hipSuccess && t.rest() > 0) {
+            hipLaunchKernelGGL((join_kernel<MODE, H, WA, WB, IA, IB>), dim3((unsigned)t.rest(), IA), dim3(64 * WA * WB), 0, st, p);
+            e = hipGetLastError();
+        }
+    }
+    return e;
+}
+
 template <int MODE, bool H>
 hipError_t launch_tiles(const Geometry& g, const Tiling& t, const Args& a, hipStream_t st)
 {
-    TileArgs p = {a, g.T, g.D, g.F, g.act, t.na, t.nb, t.steps, t.per, t.split > 1 ? a.part : nullptr};
-    const dim3 grid((unsigned)(cdiv(t.na * t.nb, 8) * 8), (unsigned)t.split);
-    if (t.large) hipLaunchKernelGGL((tile_kernel<MODE, H, 2, 4, 8, 4>), grid, dim3(512), 0, st, p);
-    else hipLaunchKernelGGL((tile_kernel<MODE, H, 2, 2, 4, 4>), grid, dim3(256), 0, st, p);
-    return hipGetLastError();
-}
-
-template <bool H>
-hipError_t join(const Tiling& t, const Args& a, int64_t n, uint16_t* out0, uint16_t* out1, int64_t first, hipStream_t st)
-{
-    if (t.split <= 1) return hipSuccess;
-    hipLaunchKernelGGL(join_kernel<H>, dim3((unsigned)cdiv(n, 1024)), dim3(256), 0, st, a.part, t.split, n, out0, out1, first);
-    return hipGetLastError();
+    return t.large ? launch_shape<MODE, H, 2, 4, 8, 4>(g, t, a, st) : launch_shape<MODE, H, 2, 2, 4, 4>(g, t, a, st);
 }
 
 template <bool H>
 hipError_t backward(const Geometry& g, const BackwardPlan& p, const Args& a, hipStream_t st)
 {
     hipError_t e = launch_tiles<kRecompute, H>(g, p.act, a, st);
-    if (e != hipSuccess) return e;
-    e = launch_tiles<kGradX, H>(g, p.dx, a, st);
-    if (e != hipSuccess) return e;
-    e = join<H>(p.dx, a, g.T * g.D, a.grad_x, a.grad_x, g.T * g.D, st);
-    if (e != hipSuccess) return e;
-    e = launch_tiles<kGradW, H>(g, p.dw, a, st);
-    if (e != hipSuccess) return e;
-    return join<H>(p.dw, a, 2 * (int64_t)g.F * g.D, a.grad_w_gate, a.grad_w_up, (int64_t)g.F * g.D, st);
+    if (e == hipSuccess) e = launch_tiles<kGradX, H>(g, p.dx, a, st);
+    if (e == hipSuccess) e = launch_tiles<kGradW, H>(g, p.dw, a, st);
+    return e;
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ namespace glu {
 
 constexpr int kMaxD = 16384;
 constexpr int kMaxF = 65536;
-constexpr int kBK = 32;              // reduction positions per LDS stage
+constexpr int kBK = 64;              // reduction positions per LDS stage
 constexpr int kCUs = 256;
 
 struct Geometry {
@@ -40,40 +40,48 @@ inline bool make_geometry(int64_t T, int D, int F, int act, int f16, Geometry* g
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// A tiled product of `rows` x `cols` results over `steps` stages of kBK: with 256 x 256 tiles (one
-// workgroup of 8 waves per compute unit) or 128 x 128 tiles (4 waves, two workgroups per
-// compute unit), and split along the reduction into `split` parts whose fp32 sums a second
-// kernel joins.
+// A tiled product of `rows` x `cols` results over `steps` stages of kBK, in 256 x 256 tiles
+// (one workgroup of 8 waves per compute unit) or 128 x 128 tiles (4 waves, two workgroups
+// per compute unit). Tiles run in rounds of one for each place on the chip; where the last
+// round would leave places empty and the product may be split (its results are plain sums),
+// each of its tiles is cut along the reduction into as many parts as fill it, whose fp32
+// results a second kernel joins.
 struct Tiling {
     bool large = false;
     int64_t na = 0, nb = 0;   // tiles along rows and columns
-    int split = 1;
+    int64_t whole = 0;        // tiles not cut: the first of the tile order
+    int split = 1;            // parts of each of the others
     int64_t steps = 0;        // stages in all
     int64_t per = 0;          // stages of a part
-    int64_t blocks() const { return na * nb * split; }
+    int64_t rest() const { return na * nb - whole; }
+    // workgroups: both runs padded to whole turns of the 8 XCDs
+    int64_t blocks() const { return (whole + 7) / 8 * 8 + (rest() * split + 7) / 8 * 8; }
+    size_t part_bytes() const { return (size_t)(rest() * split) * (large ? 256 * 256 : 128 * 128) * 4; }
 };
-// groups: independent products of this size in one launch (2 for the two weight gradients)
+// groups: independent products of this size in one launch (2 for the two weights' gradients)
 inline Tiling make_tiling(int64_t rows, int64_t cols, int64_t steps, int groups, bool may_split)
 {
     Tiling t;
     t.steps = steps;
-    t.large = cdiv(rows, 256) * cdiv(cols, 256) * groups >= kCUs * 3 / 4;
-    const int64_t tile = t.large ? 256 : 128;
+    // Rounds of large tiles against rounds of two small ones per compute unit, which take
+    // 2/3 of a large one's time; a product that may be split fills its last round, and is
+    // worth large tiles once every compute unit has 4 stages of one.
+    const int64_t nl = cdiv(rows, 256) * cdiv(cols, 256) * groups, ns = cdiv(rows, 128) * cdiv(cols, 128) * groups;
+    t.large = may_split ? nl * steps >= 4 * kCUs : 3 * cdiv(nl, kCUs) <= 2 * cdiv(ns, 2 * kCUs);
+    const int64_t tile = t.large ? 256 : 128, places = t.large ? kCUs : 2 * kCUs;
     t.na = cdiv(rows, tile);
     t.nb = cdiv(cols, tile) * groups;
-    // few tiles and a long reduction: parts of at least 8 stages, until two workgroups per
-    // compute unit are reached
-    int64_t s = 1;
-    if (may_split && !t.large && t.na * t.nb > 0) {
-        s = cdiv(2 * kCUs, t.na * t.nb);
-        if (s > steps / 8) s = steps / 8;
-        if (s > 64) s = 64;
-        if (s < 1) s = 1;
-    }
+    const int64_t tiles = t.na * t.nb;
+    t.whole = tiles;
+    t.per = steps;
+    if (!may_split || tiles == 0 || steps == 0) return t;
+    const int64_t rest = tiles % places;
+    int64_t s = rest ? places / rest : 1;
+    if (s > steps / 4) s = steps / 4;     // parts of at least 4 stages
+    if (s < 2) return t;
     t.per = cdiv(steps, s);
-    if (t.per < 1) t.per = 1;
     t.split = (int)cdiv(steps, t.per);
-    if (t.split < 1) t.split = 1;
+    t.whole = tiles - rest;
     return t;
 }
 
@@ -96,12 +104,7 @@ inline BackwardPlan make_backward_plan(const Geometry& g, bool checkpoint)
     p.off_x = off;
     if (checkpoint) off = align_up(off + (size_t)g.T * (size_t)g.D * 2, 256);
     p.off_part = off;
-    size_t part = 0;
-    if (p.dx.split > 1) part = (size_t)p.dx.split * (size_t)g.T * (size_t)g.D * 4;
-    if (p.dw.split > 1) {
-        const size_t w = (size_t)p.dw.split * 2 * (size_t)g.F * (size_t)g.D * 4;
-        if (w > part) part = w;
-    }
+    const size_t px = p.dx.part_bytes(), pw = p.dw.part_bytes(), part = px > pw ? px : pw;
     off = align_up(off + part, 256);
     p.ws_bytes = off;
     return p;
