@@ -4,7 +4,8 @@
 //   backward  with dh = dL/dh: g and u again, dg = dh u act'(g), du = dh act(g), h = act(g) u,
 //             dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x
 // x [T, D], Wg and Wu [F, D], h and dh [T, F], bf16 or fp16 (template flag H); act(g) =
-// g sigmoid(z) with z = g (SiLU) or 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU's tanh form).
+// g sigmoid(z) with z = g (SiLU, ACT 0) or 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU's tanh form,
+// ACT 1).
 // Products accumulate in fp32 on the matrix cores; g, u and the activation stay in fp32
 // registers; dg and du are rounded once to the 16-bit format (they are the operands of the next
 // products), and so is each result.
@@ -50,18 +51,20 @@ __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c)
 struct Act {
     float a, da;
 };
-__device__ __forceinline__ Act activation(float g, int act)
+template <int ACT>
+__device__ __forceinline__ Act activation(float g)
 {
+#pragma clang fp contract(off)   // the same steps wherever it is inlined: h again is h
     constexpr float c = 1.5957691216057308f, q = 0.044715f;   // 2 sqrt(2 / pi)
     float z = g, dz = 1.f;
-    if (act) {
-        const float gc = fminf(fmaxf(g, -64.f), 64.f);
-        z = c * (g + q * g * g * g);
-        dz = c * (1.f + 3.f * q * gc * gc);
+    if constexpr (ACT == 1) {
+        const float gc = __builtin_amdgcn_fmed3f(g, -64.f, 64.f);
+        z = c * fmaf(q * g * g, g, g);
+        dz = fmaf(3.f * q * c * gc, gc, c);
     }
     const float s = __builtin_amdgcn_rcpf(1.f + __expf(-z));
     const float a = g * s;
-    return {a, s + a * (1.f - s) * dz};
+    return {a, fmaf(a * (1.f - s), dz, s)};
 }
 
 // A raw buffer's descriptor as four words for the direct-to-LDS loads below: accesses at or
@@ -89,10 +92,10 @@ struct TileArgs {
     Args t;
     int64_t T;
     int D, F, act;
-    int64_t na, nb;        // tiles along rows and columns
-    int64_t whole;         // tiles that one workgroup takes whole: the first of the tile order
+    uint32_t na, nb;       // tiles along rows and columns
+    uint32_t whole;        // tiles that one workgroup takes whole: the first of the tile order
     int64_t steps, per;    // stages in all, stages of a part of the other tiles
-    int split;             // parts of each of those
+    uint32_t split;        // parts of each of those
     float* part;           // their fp32 results, [tile][part][block of results][thread]
 };
 
@@ -101,32 +104,32 @@ struct TileArgs {
 // next rows: the tiles in flight on an XCD then share kGroup row operands and a few column
 // operands in its L2 (4 against 2, 8 and 16: within 2 % of the best for every product). The
 // split tiles follow, the same part of neighbouring tiles side by side.
-constexpr int kGroup = 4;
+constexpr uint32_t kGroup = 4;
 struct Unit {
-    int64_t a, b, tile;
+    uint32_t a, b, tile;
     int part;
 };
-__device__ __forceinline__ void place(int64_t t, int64_t na, int64_t nb, Unit* u)
+__device__ __forceinline__ void place(uint32_t t, uint32_t na, uint32_t nb, Unit* u)
 {
-    const int64_t group = t / (kGroup * nb), r = t - group * kGroup * nb;
-    const int64_t rows = na - group * kGroup < kGroup ? na - group * kGroup : kGroup;
+    const uint32_t group = t / (kGroup * nb), r = t - group * kGroup * nb;
+    const uint32_t rows = na - group * kGroup < kGroup ? na - group * kGroup : kGroup;
     u->tile = t;
-    u->a = group * kGroup + r % rows;
     u->b = r / rows;
+    u->a = group * kGroup + (r - u->b * rows);
 }
 __device__ __forceinline__ bool unit_of(const TileArgs& p, Unit* u)
 {
-    const int64_t first = (p.whole + 7) / 8;          // of the whole tiles, on each XCD
-    const int64_t xcd = blockIdx.x % 8, i = blockIdx.x / 8;
+    const uint32_t first = (p.whole + 7) / 8;          // of the whole tiles, on each XCD
+    const uint32_t xcd = blockIdx.x % 8, i = blockIdx.x / 8;
     if (i < first) {
-        const int64_t t = xcd * first + i;
+        const uint32_t t = xcd * first + i;
         if (t >= p.whole) return false;
         u->part = -1;
         place(t, p.na, p.nb, u);
         return true;
     }
-    const int64_t rest = p.na * p.nb - p.whole, units = rest * p.split, per = (units + 7) / 8;
-    const int64_t v = xcd * per + (i - first);
+    const uint32_t rest = p.na * p.nb - p.whole, units = rest * p.split, per = (units + 7) / 8;
+    const uint32_t v = xcd * per + (i - first);
     if (i - first >= per || v >= units) return false;
     u->part = (int)(v / rest);
     place(p.whole + v % rest, p.na, p.nb, u);
@@ -142,6 +145,63 @@ __device__ __forceinline__ void store_rows(const TileArgs& p, int up, int64_t d,
     uint16_t* const out = MODE == kGradX ? p.t.grad_x : (up ? p.t.grad_w_up : p.t.grad_w_gate);
     if (c < (MODE == kGradX ? p.T : (int64_t)p.F) && d < p.D)
         *reinterpret_cast<u32x2*>(out + c * p.D + d) = u32x2{pack_x16<H>(v[0], v[1]), pack_x16<H>(v[2], v[3])};
+}
+
+// A wave's results of a gated tile, from f0 on and for tokens t0, t0 + 16, ..: lane values of g in
+// acc[0 .. IA/2), of u in the rest, 8 consecutive f in a pair of blocks.
+template <int MODE, bool H, int ACT, int IA, int IB>
+__device__ __forceinline__ void gated_results(const TileArgs& p, int64_t f0, int64_t t0, const f32x4 (&acc)[IA][IB])
+{
+    const int64_t T = p.T;
+    const int F = p.F;
+            u32x4 dh[IB][IA / 4];
+            if constexpr (MODE == kRecompute) {   // all of them on their way before the first is used
+    #pragma unroll
+                for (int q = 0; q < IB; ++q)
+    #pragma unroll
+                    for (int i = 0; i < IA / 4; ++i) {
+                        const int64_t t = t0 + 16 * q < T ? t0 + 16 * q : T - 1, f = f0 + 32 * i < F ? f0 + 32 * i : 0;
+                        dh[q][i] = *reinterpret_cast<const u32x4*>(p.t.grad_h + t * F + f);
+                    }
+            }
+    #pragma unroll
+            for (int q = 0; q < IB; ++q) {
+                const int64_t t = t0 + 16 * q;
+    #pragma unroll
+                for (int i = 0; i < IA / 4; ++i) {
+                    const int64_t f = f0 + 32 * i;
+                    u32x4 hv, gv, uv;
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float hh[2], dg[2], du[2];
+    #pragma unroll
+                        for (int l = 0; l < 2; ++l) {
+                            const int r = 2 * e + l;                            // f + r
+                            const float gg = acc[2 * i + r / 4][q][r % 4], uu = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
+                            const Act ac = activation<ACT>(gg);
+                            hh[l] = ac.a * uu;
+                    asm("" : "+v"(hh[l]));   // rounded to fp32 before fp16, in the forward as in the backward
+                            if constexpr (MODE == kRecompute) {
+                                const float d = l ? x16_hi<H>(dh[q][i][e]) : x16_lo<H>(dh[q][i][e]);
+                                dg[l] = d * uu * ac.da;
+                                du[l] = d * ac.a;
+                            }
+                        }
+                        hv[e] = pack_x16<H>(hh[0], hh[1]);
+                        if constexpr (MODE == kRecompute) {
+                            gv[e] = pack_x16<H>(dg[0], dg[1]);
+                            uv[e] = pack_x16<H>(du[0], du[1]);
+                        }
+                    }
+                    if (t < T && f < F) {
+                        if (MODE == kForward || p.t.h) *reinterpret_cast<u32x4*>(p.t.h + t * F + f) = hv;
+                        if constexpr (MODE == kRecompute) {
+                            *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + f) = gv;
+                            *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + F + f) = uv;
+                        }
+                    }
+                }
+            }
 }
 
 // WA x WB waves of IA x IB 16 x 16 results each. A stage of the reduction is kBK = 64 positions,
@@ -181,7 +241,7 @@ tile_kernel(TileArgs p)
     const int64_t T = p.T;
     const int half_steps = (F + kBK - 1) / kBK;                  // kGradX: stages of either weight
     // kGradW: the tiles of Wg's gradient, then those of Wu's
-    const int64_t nbh = MODE == kGradW ? p.nb / 2 : p.nb;
+    const int64_t nbh = p.nb / 2;
     const int up = MODE == kGradW && tb >= nbh ? 1 : 0;
     const int64_t a0 = ta * (GATED ? AR / 2 : AR);               // first f (gated) or d
     const int64_t b0 = (tb - up * nbh) * BC;                     // first token, or f
@@ -363,54 +423,8 @@ tile_kernel(TileArgs p)
 
     // --- results: lane (j, kg) holds rows 4 kg .. 4 kg + 3 of column j of each 16 x 16 block
     if constexpr (GATED) {
-        const int64_t f0 = a0 + 16 * wa * IA / 2 + 8 * kg, t0 = b0 + 16 * wb * IB + j;
-        u32x4 dh[IB][IA / 4];
-        if constexpr (MODE == kRecompute) {   // all of them on their way before the first is used
-#pragma unroll
-            for (int q = 0; q < IB; ++q)
-#pragma unroll
-                for (int i = 0; i < IA / 4; ++i) {
-                    const int64_t t = t0 + 16 * q < T ? t0 + 16 * q : T - 1, f = f0 + 32 * i < F ? f0 + 32 * i : 0;
-                    dh[q][i] = *reinterpret_cast<const u32x4*>(p.t.grad_h + t * F + f);
-                }
-        }
-#pragma unroll
-        for (int q = 0; q < IB; ++q) {
-            const int64_t t = t0 + 16 * q;
-#pragma unroll
-            for (int i = 0; i < IA / 4; ++i) {
-                const int64_t f = f0 + 32 * i;
-                u32x4 hv, gv, uv;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float hh[2], dg[2], du[2];
-#pragma unroll
-                    for (int l = 0; l < 2; ++l) {
-                        const int r = 2 * e + l;                            // f + r
-                        const float gg = acc[2 * i + r / 4][q][r % 4], uu = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
-                        const Act ac = activation(gg, p.act);
-                        hh[l] = ac.a * uu;
-                        if constexpr (MODE == kRecompute) {
-                            const float d = l ? x16_hi<H>(dh[q][i][e]) : x16_lo<H>(dh[q][i][e]);
-                            dg[l] = d * uu * ac.da;
-                            du[l] = d * ac.a;
-                        }
-                    }
-                    hv[e] = pack_x16<H>(hh[0], hh[1]);
-                    if constexpr (MODE == kRecompute) {
-                        gv[e] = pack_x16<H>(dg[0], dg[1]);
-                        uv[e] = pack_x16<H>(du[0], du[1]);
-                    }
-                }
-                if (t < T && f < F) {
-                    if (MODE == kForward || p.t.h) *reinterpret_cast<u32x4*>(p.t.h + t * F + f) = hv;
-                    if constexpr (MODE == kRecompute) {
-                        *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + f) = gv;
-                        *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + F + f) = uv;
-                    }
-                }
-            }
-        }
+        if (p.act) gated_results<MODE, H, 1, IA, IB>(p, a0 + 16 * wa * IA / 2 + 8 * kg, b0 + 16 * wb * IB + j, acc);
+        else gated_results<MODE, H, 0, IA, IB>(p, a0 + 16 * wa * IA / 2 + 8 * kg, b0 + 16 * wb * IB + j, acc);
     } else if (unit.part < 0) {
 #pragma unroll
         for (int q = 0; q < IB; ++q)
@@ -419,7 +433,7 @@ tile_kernel(TileArgs p)
                 store_rows<MODE, H>(p, up, a0 + 16 * (wa * IA + i) + 4 * kg, b0 + 16 * (wb * IB + q) + j, acc[i][q]);
     } else {
         f32x4* const part = reinterpret_cast<f32x4*>(p.part) +
-                            ((unit.tile - p.whole) * p.split + unit.part) * (IA * IB * 64 * NW) + tid;
+                            (int64_t)((unit.tile - p.whole) * p.split + unit.part) * (IA * IB * 64 * NW) + tid;
 #pragma unroll
         for (int i = 0; i < IA; ++i)
 #pragma unroll
@@ -437,19 +451,19 @@ join_kernel(TileArgs p)
     Unit u;
     place(p.whole + blockIdx.x, p.na, p.nb, &u);
     const int i = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wa = wave / WB, wb = wave % WB;
-    const int64_t nbh = MODE == kGradW ? p.nb / 2 : p.nb;
+    const uint32_t nbh = p.nb / 2;
     const int up = MODE == kGradW && u.b >= nbh ? 1 : 0;
     const f32x4* part = reinterpret_cast<const f32x4*>(p.part) + (int64_t)blockIdx.x * p.split * (IA * IB * 64 * NW) + tid;
     f32x4 v[IB];
 #pragma unroll
     for (int q = 0; q < IB; ++q) v[q] = part[(i * IB + q) * 64 * NW];
-    for (int s = 1; s < p.split; ++s)
+    for (uint32_t s = 1; s < p.split; ++s)
 #pragma unroll
         for (int q = 0; q < IB; ++q) v[q] += part[(int64_t)s * (IA * IB * 64 * NW) + (i * IB + q) * 64 * NW];
 #pragma unroll
     for (int q = 0; q < IB; ++q)
-        store_rows<MODE, H>(p, up, u.a * AR + 16 * (wa * IA + i) + 4 * (lane >> 4),
-                            (u.b - up * nbh) * BC + 16 * (wb * IB + q) + (lane & 15), v[q]);
+        store_rows<MODE, H>(p, up, (int64_t)u.a * AR + 16 * (wa * IA + i) + 4 * (lane >> 4),
+                            (int64_t)(u.b - up * nbh) * BC + 16 * (wb * IB + q) + (lane & 15), v[q]);
 }
 
 // An empty sum over tokens: both weights' gradients are zero.
@@ -465,7 +479,7 @@ zero_kernel(uint16_t* __restrict__ a, uint16_t* __restrict__ b, int64_t n)
 template <int MODE, bool H, int WA, int WB, int IA, int IB>
 hipError_t launch_shape(const Geometry& g, const Tiling& t, const Args& a, hipStream_t st)
 {
-    const TileArgs p = {a, g.T, g.D, g.F, g.act, t.na, t.nb, t.whole, t.steps, t.per, t.split, a.part};
+    const TileArgs p = {a, g.T, g.D, g.F, g.act, (uint32_t)t.na, (uint32_t)t.nb, (uint32_t)t.whole, t.steps, t.per, (uint32_t)t.split, a.part};
     hipLaunchKernelGGL((tile_kernel<MODE, H, WA, WB, IA, IB>), dim3((unsigned)t.blocks()), dim3(64 * WA * WB), 0, st, p);
     hipError_t e = hipGetLastError();
     if constexpr (MODE == kGradX || MODE == kGradW) {
