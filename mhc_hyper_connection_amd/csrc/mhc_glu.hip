@@ -426,11 +426,26 @@ tile_kernel(TileArgs p)
         if (p.act) gated_results<MODE, H, 1, IA, IB>(p, a0 + 16 * wa * IA / 2 + 8 * kg, b0 + 16 * wb * IB + j, acc);
         else gated_results<MODE, H, 0, IA, IB>(p, a0 + 16 * wa * IA / 2 + 8 * kg, b0 + 16 * wb * IB + j, acc);
     } else if (unit.part < 0) {
+        // through LDS, so that a wave stores whole rows of the tile ([column][row], rows
+        // contiguous: grad_x [T][D], or a weight's gradient [F][D]): 2 AR bytes of a column and
+        // 16 more, with which the 8-byte writes of 16 columns meet all banks
+        constexpr int CS = 2 * AR + 16, OCT = AR / 8;
+        static_assert(BC * CS <= RA * ASZ + RB * BSZ, "the tile fits in LDS");
+        __syncthreads();   // every wave's last reads and loads are done (waited for above)
 #pragma unroll
-        for (int q = 0; q < IB; ++q)
+        for (int i = 0; i < IA; ++i)
 #pragma unroll
-            for (int i = 0; i < IA; ++i)
-                store_rows<MODE, H>(p, up, a0 + 16 * (wa * IA + i) + 4 * kg, b0 + 16 * (wb * IB + q) + j, acc[i][q]);
+            for (int q = 0; q < IB; ++q)
+                *reinterpret_cast<u32x2*>(lds + (16 * (wb * IB + q) + j) * CS + (16 * (wa * IA + i) + 4 * kg) * 2) =
+                    u32x2{pack_x16<H>(acc[i][q][0], acc[i][q][1]), pack_x16<H>(acc[i][q][2], acc[i][q][3])};
+        __syncthreads();
+        uint16_t* const out = MODE == kGradX ? p.t.grad_x : (up ? p.t.grad_w_up : p.t.grad_w_gate);
+        const int o = tid % OCT;
+        const int64_t d = a0 + 8 * o, ncol = MODE == kGradX ? T : F;
+#pragma unroll
+        for (int c = tid / OCT; c < BC; c += 64 * NW / OCT)
+            if (d < D && b0 + c < ncol)
+                *reinterpret_cast<u32x4*>(out + (b0 + c) * D + d) = *reinterpret_cast<const u32x4*>(lds + c * CS + 16 * o);
     } else {
         f32x4* const part = reinterpret_cast<f32x4*>(p.part) +
                             (int64_t)((unit.tile - p.whole) * p.split + unit.part) * (IA * IB * 64 * NW) + tid;
@@ -466,6 +481,104 @@ join_kernel(TileArgs p)
                             (int64_t)(u.b - up * nbh) * BC + 16 * (wb * IB + q) + (lane & 15), v[q]);
 }
 
+// Few tokens (T <= 16 NT): reading the weights once is the whole cost. A workgroup takes 16 f of both
+// projections and all tokens, its W waves every W-th run of 64 positions; their sums meet in
+// LDS and are added in wave order. A wave keeps a ring of R stages of its own in LDS (32 weight
+// rows and the tokens' rows, 128 bytes each, by direct loads of whole lines), so that it waits
+// for its own loads only and meets the others once. (The same weights read straight into
+// operand registers, 64 bytes of a row an instruction: 86 us against 70 at D = 7168, F = 14336,
+// whatever the waves and loads in flight.) Rows past T or F and positions past D read as zeros.
+template <int MODE, bool H, int NT, int W>
+__global__ void __launch_bounds__(64 * W)
+skinny_kernel(TileArgs p)
+{
+    constexpr int R = 3, ROWS = 32 + 16 * NT, STAGE = ROWS * 128, LOADS = ROWS / 8;
+    static_assert(R * STAGE >= 2 * NT * 64 * 16, "a wave's sums fit where its stages were");
+    __shared__ __attribute__((aligned(1024))) char lds[W * R * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int j = lane & 15, kg = lane >> 4, D = p.D, F = p.F;
+    const int64_t f0 = (int64_t)blockIdx.x * 16;
+    const uint32_t rows = (uint32_t)(F - f0 < 16 ? F - f0 : 16), line = (uint32_t)D * 2;
+    const u32x4 dg_ = descriptor(p.t.w_gate + f0 * D, rows * line), du_ = descriptor(p.t.w_up + f0 * D, rows * line);
+    const u32x4 dx_ = descriptor(p.t.x, (uint32_t)p.T * line);
+    const uint32_t mine = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds)) + wave * (R * STAGE);
+    // load i of a stage: 8 rows; the 16-byte chunk c of row r sits at c ^ (r / 2) % 8, as in tile_kernel
+    const int lr = lane / 8, lc = (lane & 7);
+    auto issue = [&](int step, int slot) __attribute__((always_inline)) {
+        const int k = step * 64;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = 8 * (i < 4 ? i % 2 : i - 4) + lr, c = lc ^ ((r >> 1) & 7);
+            const uint32_t off = k + 8 * c < D ? (uint32_t)r * line + (uint32_t)(k + 8 * c) * 2 : kOutOfRange;
+            buffer_to_lds(i < 2 ? dg_ : (i < 4 ? du_ : dx_), off, mine + slot * STAGE + i * 1024);
+        }
+    };
+    const uint32_t at0 = mine + j * 128 + ((kg ^ (j >> 1)) << 4);
+    f32x4 acc[2][NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int steps = (D + 63) / 64;
+#pragma unroll
+    for (int s = 0; s < R - 1; ++s) issue(wave + s * W, s);
+    for (int k = wave; k < steps; k += R * W) {
+#pragma unroll
+        for (int s = 0; s < R; ++s) {
+            if (k + s * W < steps) {
+                issue(k + (s + R - 1) * W, (s + R - 1) % R);
+                asm volatile("s_waitcnt vmcnt(%0)" : : "n"((R - 1) * LOADS) : "memory");
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = (at0 ^ (h << 6)) + s * STAGE;
+                    const s16x8 g = *(const MHC_LDS s16x8*)(uintptr_t)at, u = *(const MHC_LDS s16x8*)(uintptr_t)(at + 2048);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const s16x8 x = *(const MHC_LDS s16x8*)(uintptr_t)(at + 4096 + n * 2048);
+                        acc[0][n] = mfma<H>(g, x, acc[0][n]);
+                        acc[1][n] = mfma<H>(u, x, acc[1][n]);
+                    }
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // read, before the slot is loaded again
+            }
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    // the sums, each wave's where its stages were
+    auto red = [&](int w, int i) { return reinterpret_cast<f32x4*>(lds + w * (R * STAGE)) + i * 64; };
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        red(wave, 2 * n)[lane] = acc[0][n];
+        red(wave, 2 * n + 1)[lane] = acc[1][n];
+    }
+    __syncthreads();
+    if (wave >= NT) return;
+    f32x4 g = red(0, 2 * wave)[lane], u = red(0, 2 * wave + 1)[lane];   // wave n: tokens 16 n ..
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+        g += red(w, 2 * wave)[lane];
+        u += red(w, 2 * wave + 1)[lane];
+    }
+    const int64_t t = 16 * wave + j, f = f0 + 4 * kg;
+    if (t >= p.T || f >= F) return;
+    u32x2 dh = {0u, 0u};
+    if constexpr (MODE == kRecompute) dh = *reinterpret_cast<const u32x2*>(p.t.grad_h + t * F + f);
+    float hh[4], dg[4], du[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const Act ac = p.act ? activation<1>(g[r]) : activation<0>(g[r]);
+        hh[r] = ac.a * u[r];
+        asm("" : "+v"(hh[r]));
+        const float d = (r & 1) ? x16_hi<H>(dh[r >> 1]) : x16_lo<H>(dh[r >> 1]);
+        dg[r] = d * u[r] * ac.da;
+        du[r] = d * ac.a;
+    }
+    if (MODE == kForward || p.t.h)
+        *reinterpret_cast<u32x2*>(p.t.h + t * F + f) = u32x2{pack_x16<H>(hh[0], hh[1]), pack_x16<H>(hh[2], hh[3])};
+    if constexpr (MODE == kRecompute) {
+        *reinterpret_cast<u32x2*>(p.t.dgu + t * 2 * F + f) = u32x2{pack_x16<H>(dg[0], dg[1]), pack_x16<H>(dg[2], dg[3])};
+        *reinterpret_cast<u32x2*>(p.t.dgu + t * 2 * F + F + f) = u32x2{pack_x16<H>(du[0], du[1]), pack_x16<H>(du[2], du[3])};
+    }
+}
+
 // An empty sum over tokens: both weights' gradients are zero.
 __global__ void __launch_bounds__(256)
 zero_kernel(uint16_t* __restrict__ a, uint16_t* __restrict__ b, int64_t n)
@@ -494,6 +607,16 @@ hipError_t launch_shape(const Geometry& g, const Tiling& t, const Args& a, hipSt
 template <int MODE, bool H>
 hipError_t launch_tiles(const Geometry& g, const Tiling& t, const Args& a, hipStream_t st)
 {
+    if constexpr (MODE == kForward || MODE == kRecompute) {
+        if (g.skinny()) {
+            const TileArgs p = {a, g.T, g.D, g.F, g.act};
+            const dim3 grid((unsigned)cdiv(g.F, 16)), block(256);
+            if (g.T <= 16) hipLaunchKernelGGL((skinny_kernel<MODE, H, 1, 4>), grid, block, 0, st, p);
+            else if (g.T <= 32) hipLaunchKernelGGL((skinny_kernel<MODE, H, 2, 4>), grid, block, 0, st, p);
+            else hipLaunchKernelGGL((skinny_kernel<MODE, H, 4, 4>), grid, block, 0, st, p);
+            return hipGetLastError();
+        }
+    }
     return t.large ? launch_shape<MODE, H, 2, 4, 8, 4>(g, t, a, st) : launch_shape<MODE, H, 2, 2, 4, 4>(g, t, a, st);
 }
 
