@@ -136,17 +136,6 @@ __device__ __forceinline__ bool unit_of(const TileArgs& p, Unit* u)
     return true;
 }
 
-// Four rows of one column of kGradX's or kGradW's result, at row d and column c of the tile's half
-// (`up`: Wu's gradient). [column][row], rows contiguous: grad_x [T][D], or a weight's
-// gradient [F][D].
-template <int MODE, bool H>
-__device__ __forceinline__ void store_rows(const TileArgs& p, int up, int64_t d, int64_t c, f32x4 v)
-{
-    uint16_t* const out = MODE == kGradX ? p.t.grad_x : (up ? p.t.grad_w_up : p.t.grad_w_gate);
-    if (c < (MODE == kGradX ? p.T : (int64_t)p.F) && d < p.D)
-        *reinterpret_cast<u32x2*>(out + c * p.D + d) = u32x2{pack_x16<H>(v[0], v[1]), pack_x16<H>(v[2], v[3])};
-}
-
 // A wave's results of a gated tile, from f0 on and for tokens t0, t0 + 16, ..: lane values of g in
 // acc[0 .. IA/2), of u in the rest, 8 consecutive f in a pair of blocks.
 template <int MODE, bool H, int ACT, int IA, int IB>
@@ -450,35 +439,44 @@ tile_kernel(TileArgs p)
         f32x4* const part = reinterpret_cast<f32x4*>(p.part) +
                             (int64_t)((unit.tile - p.whole) * p.split + unit.part) * (IA * IB * 64 * NW) + tid;
 #pragma unroll
-        for (int i = 0; i < IA; ++i)
+        for (int q = 0; q < IB; ++q) {
+            if (b0 + 16 * (wb * IB + q) >= (MODE == kGradX ? T : (int64_t)F)) break;   // no such columns
 #pragma unroll
-            for (int q = 0; q < IB; ++q) part[(i * IB + q) * 64 * NW] = acc[i][q];
+            for (int i = 0; i < IA; ++i) part[(i * IB + q) * 64 * NW] = acc[i][q];
+        }
     }
 }
 
 // The split tiles: a result is its parts' sum in their order, rounded once. Workgroup (tile,
-// i): block row i of the tile's waves, laid out as tile_kernel left it.
+// block): one 16 x 16 block of each of the tile's waves, laid out as tile_kernel left it;
+// four parts on their way at a time.
 template <int MODE, bool H, int WA, int WB, int IA, int IB>
 __global__ void __launch_bounds__(64 * WA * WB)
 join_kernel(TileArgs p)
 {
-    constexpr int NW = WA * WB, AR = 16 * WA * IA, BC = 16 * WB * IB;
+    constexpr int NW = WA * WB, AR = 16 * WA * IA, BC = 16 * WB * IB, STRIDE = IA * IB * 64 * NW;
     Unit u;
     place(p.whole + blockIdx.x, p.na, p.nb, &u);
-    const int i = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wa = wave / WB, wb = wave % WB;
+    const int i = blockIdx.y / IB, q = blockIdx.y % IB;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wa = wave / WB, wb = wave % WB;
     const uint32_t nbh = p.nb / 2;
     const int up = MODE == kGradW && u.b >= nbh ? 1 : 0;
-    const f32x4* part = reinterpret_cast<const f32x4*>(p.part) + (int64_t)blockIdx.x * p.split * (IA * IB * 64 * NW) + tid;
-    f32x4 v[IB];
+    const int64_t d = (int64_t)u.a * AR + 16 * (wa * IA + i) + 4 * (lane >> 4);
+    const int64_t c = (int64_t)(u.b - up * nbh) * BC + 16 * (wb * IB + q) + (lane & 15);
+    if (c >= (MODE == kGradX ? p.T : (int64_t)p.F) || d >= p.D) return;
+    const f32x4* part = reinterpret_cast<const f32x4*>(p.part) + (int64_t)blockIdx.x * p.split * STRIDE + blockIdx.y * (64 * NW) + tid;
+    f32x4 v = part[0];
+    uint32_t s = 1;
+    for (; s + 4 <= p.split; s += 4) {
+        f32x4 w[4];
 #pragma unroll
-    for (int q = 0; q < IB; ++q) v[q] = part[(i * IB + q) * 64 * NW];
-    for (uint32_t s = 1; s < p.split; ++s)
+        for (int e = 0; e < 4; ++e) w[e] = part[(int64_t)(s + e) * STRIDE];
 #pragma unroll
-        for (int q = 0; q < IB; ++q) v[q] += part[(int64_t)s * (IA * IB * 64 * NW) + (i * IB + q) * 64 * NW];
-#pragma unroll
-    for (int q = 0; q < IB; ++q)
-        store_rows<MODE, H>(p, up, (int64_t)u.a * AR + 16 * (wa * IA + i) + 4 * (lane >> 4),
-                            (int64_t)(u.b - up * nbh) * BC + 16 * (wb * IB + q) + (lane & 15), v[q]);
+        for (int e = 0; e < 4; ++e) v += w[e];
+    }
+    for (; s < p.split; ++s) v += part[(int64_t)s * STRIDE];
+    uint16_t* const out = MODE == kGradX ? p.t.grad_x : (up ? p.t.grad_w_up : p.t.grad_w_gate);
+    *reinterpret_cast<u32x2*>(out + c * p.D + d) = u32x2{pack_x16<H>(v[0], v[1]), pack_x16<H>(v[2], v[3])};
 }
 
 // Few tokens (T <= 16 NT): reading the weights once is the whole cost. A workgroup takes 16 f of both
@@ -597,7 +595,7 @@ hipError_t launch_shape(const Geometry& g, const Tiling& t, const Args& a, hipSt
     hipError_t e = hipGetLastError();
     if constexpr (MODE == kGradX || MODE == kGradW) {
         if (e == hipSuccess && t.rest() > 0) {
-            hipLaunchKernelGGL((join_kernel<MODE, H, WA, WB, IA, IB>), dim3((unsigned)t.rest(), IA), dim3(64 * WA * WB), 0, st, p);
+            hipLaunchKernelGGL((join_kernel<MODE, H, WA, WB, IA, IB>), dim3((unsigned)t.rest(), IA * IB), dim3(64 * WA * WB), 0, st, p);
             e = hipGetLastError();
         }
     }
