@@ -79,6 +79,12 @@ Checkpoint.__doc__ = """An activation tensor [..., D] kept in 8 bits (mhc_checkp
 is restored to."""
 
 
+def _new_checkpoint(shape, dtype, device):
+    torch = _torch()
+    return Checkpoint(torch.empty(shape, dtype=torch.int8, device=device),
+                      torch.empty((*shape[:-1], -(-shape[-1] // CHECKPOINT_BLOCK)), dtype=torch.uint8, device=device), dtype)
+
+
 def _check_checkpoint(ck, name, dtype, shape, device):
     if ck.dtype != dtype:
         raise ValueError(f"{name}: a checkpoint of {ck.dtype}, expected {dtype}")
@@ -457,9 +463,9 @@ def mhc_checkpoint(x, *, out=None):
     shape, D, dev = tuple(x.shape), int(x.shape[-1]), x.device
     _check(x, "x", xdt, shape, dev)
     if out is None:
-        out = Checkpoint(torch.empty(shape, dtype=torch.int8, device=dev),
-                         torch.empty((*shape[:-1], -(-D // CHECKPOINT_BLOCK)), dtype=torch.uint8, device=dev), xdt)
-    _check_checkpoint(out, "out", xdt, shape, dev)
+        out = _new_checkpoint(shape, xdt, dev)
+    else:
+        _check_checkpoint(out, "out", xdt, shape, dev)
     with _on_gpu(dev):
         st = raw_checkpoint(math.prod(shape[:-1]), D, xdt == torch.float16, _ptr(x), _ptr(out.codes),
                             _ptr(out.scales), _stream(dev))
@@ -480,7 +486,8 @@ def mhc_checkpoint_restore(checkpoint, *, out=None):
     _check_checkpoint(checkpoint, "checkpoint", xdt, shape, dev)
     if out is None:
         out = torch.empty(shape, dtype=xdt, device=dev)
-    _check(out, "out", xdt, shape, dev)
+    else:
+        _check(out, "out", xdt, shape, dev)
     with _on_gpu(dev):
         st = raw_checkpoint_restore(math.prod(shape[:-1]), shape[-1], xdt == torch.float16, _ptr(checkpoint.codes),
                                     _ptr(checkpoint.scales), _ptr(out), _stream(dev))
@@ -504,11 +511,12 @@ def mhc_post_checkpoint(x, residual, post, comb, *, out=None, checkpoint=None):
     _check(comb, "comb", torch.float32, (T, n, n), dev)
     if out is None:
         out = torch.empty((T, n, D), dtype=xdt, device=dev)
-    _check(out, "out", xdt, (T, n, D), dev)
+    else:
+        _check(out, "out", xdt, (T, n, D), dev)
     if checkpoint is None:
-        checkpoint = Checkpoint(torch.empty((T, n, D), dtype=torch.int8, device=dev),
-                                torch.empty((T, n, -(-D // CHECKPOINT_BLOCK)), dtype=torch.uint8, device=dev), xdt)
-    _check_checkpoint(checkpoint, "checkpoint", xdt, (T, n, D), dev)
+        checkpoint = _new_checkpoint((T, n, D), xdt, dev)
+    else:
+        _check_checkpoint(checkpoint, "checkpoint", xdt, (T, n, D), dev)
     with _on_gpu(dev):
         st = raw_post_checkpoint(T, n, D, xdt == torch.float16, _ptr(x), _ptr(residual), _ptr(post), _ptr(comb), _ptr(out),
                                  _ptr(checkpoint.codes), _ptr(checkpoint.scales), _stream(dev))
@@ -547,11 +555,13 @@ def mhc_post_backward(grad_out, x, residual, post, comb, *, out=None):
             "grad_comb": (torch.float32, (T, n, n))}
     if out is None:
         out = {k: torch.empty(shape, dtype=dt, device=dev) for k, (dt, shape) in want.items()}
-    elif set(out) != set(want):
-        raise ValueError(f"out must hold exactly {sorted(want)}")
-    for k, (dt, shape) in want.items():
-        _check(out[k], k, dt, shape, dev)
-        ptrs[k] = _ptr(out[k])
+    else:
+        if set(out) != set(want):
+            raise ValueError(f"out must hold exactly {sorted(want)}")
+        for k, (dt, shape) in want.items():
+            _check(out[k], k, dt, shape, dev)
+    for k, v in out.items():
+        ptrs[k] = _ptr(v)
     with _on_gpu(dev):
         st = raw_post_backward(T, n, D, xdt == torch.float16, ptrs, _stream(dev))
     if st != MHC_OK:
@@ -585,7 +595,8 @@ def mhc_glu(x, w_gate, w_up, *, act="silu", out=None):
     _check(w_up, "w_up", xdt, (F, D), dev)
     if out is None:
         out = torch.empty((*lead, F), dtype=xdt, device=dev)
-    _check(out, "out", xdt, (*lead, F), dev)
+    else:
+        _check(out, "out", xdt, (*lead, F), dev)
     with _on_gpu(dev):
         st = raw_glu(make_glu_params(T, D, F, act, xdt == torch.float16),
                      {"x": _ptr(x), "w_gate": _ptr(w_gate), "w_up": _ptr(w_up), "h": _ptr(out)}, _stream(dev))
@@ -620,10 +631,11 @@ def mhc_glu_backward(grad_h, x, w_gate, w_up, *, act="silu", need_h=False, out=N
         want["h"] = (*lead, F)
     if out is None:
         out = {k: torch.empty(v, dtype=xdt, device=dev) for k, v in want.items()}
-    elif set(out) != set(want):
-        raise ValueError(f"out must hold exactly {sorted(want)}")
-    for k, v in want.items():
-        _check(out[k], k, xdt, v, dev)
+    else:
+        if set(out) != set(want):
+            raise ValueError(f"out must hold exactly {sorted(want)}")
+        for k, v in want.items():
+            _check(out[k], k, xdt, v, dev)
     ptrs = {"grad_h": _ptr(grad_h), "w_gate": _ptr(w_gate), "w_up": _ptr(w_up), **{k: _ptr(out[k]) for k in want}}
     if ck is None:
         ptrs["x"] = _ptr(x)
