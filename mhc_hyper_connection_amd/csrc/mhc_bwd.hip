@@ -21,7 +21,8 @@
 //   bwd_main_kernel     one workgroup per (token group, d-block, stream group): per tile
 //                       of 64 tokens, xrsGrad on the matrix cores (phi terms x gMix terms,
 //                       six products), gradX, the gradGamma sums, and gMix^T . x on the
-//                       matrix cores with x transposed through LDS; group sums to partials
+//                       matrix cores, both transposed on their way out of LDS; group sums to
+//                       partials
 //   bwd_reduce_*        fixed-order fp64 sums of the partials (gradPhi, gradGamma) and
 //                       of the per-token terms (gradAlpha, gradBias)
 // x, gradHIn, gradXPost and gradX are bf16, or all fp16 (the guide's section 8.2: gradX
@@ -32,6 +33,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "mhc_bwd_plan.h"
 #include "mhc_ckpt_device.h"
@@ -72,16 +74,6 @@ __device__ __forceinline__ void split_f16x8(u32x4 w, bf16x8& hi, bf16x8& lo)
     hi = __builtin_bit_cast(bf16x8, h);
     lo = __builtin_bit_cast(bf16x8, l);
 }
-// x as loaded: an octet of 16-bit values, or (Q) of codes with their block's scale byte.
-struct CodeOctet {
-    u32x2 c;
-    uint32_t s;
-};
-template <bool Q> struct XOctetOf { typedef u32x4 type; };
-template <> struct XOctetOf<true> { typedef CodeOctet type; };
-template <bool Q> using XOctet = typename XOctetOf<Q>::type;
-template <bool H> __device__ __forceinline__ u32x4 x_values(const u32x4& v) { return v; }
-template <bool H> __device__ __forceinline__ u32x4 x_values(const CodeOctet& v) { return ckpt_decode<H>(v.c, ckpt_step(v.s)); }
 // ------------------------------------------------------------------ weight pack
 
 // Unit u = (((((b * n + i) * 2 + h) * KS + ks) * 3 + p) * 64 + lane holds, for lane
@@ -277,14 +269,10 @@ bwd_token_kernel(Args a, int64_t T, int D)
         const u32x4 gh = *reinterpret_cast<const u32x4*>(gt + 8 * o);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            XOctet<Q> xl;
-            if constexpr (Q) {
-                xl.c = *reinterpret_cast<const u32x2*>(ct + (int64_t)i * D + 8 * o);
-                xl.s = st[i * NB + (o >> 2)];
-            } else {
-                xl = *reinterpret_cast<const u32x4*>(xt + (int64_t)i * D + 8 * o);
-            }
-            const u32x4 xv = x_values<H>(xl);
+            u32x4 xv;
+            if constexpr (Q)
+                xv = ckpt_decode<H>(*reinterpret_cast<const u32x2*>(ct + (int64_t)i * D + 8 * o), ckpt_step(st[i * NB + (o >> 2)]));
+            else xv = *reinterpret_cast<const u32x4*>(xt + (int64_t)i * D + 8 * o);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 acc[i] += (double)(x16_lo<H>(gh[e]) * x16_lo<H>(xv[e]));
@@ -363,13 +351,20 @@ constexpr int kPairs = 6;
 constexpr int pair_a(int q) { return q == 0 ? 2 : (q == 1 ? 0 : (q == 2 ? 1 : (q == 3 ? 1 : 0))); }
 constexpr int pair_b(int q) { return q == 0 ? 0 : (q == 1 ? 2 : (q == 2 ? 1 : (q == 3 ? 0 : (q == 4 ? 1 : 0)))); }
 
-// Transposed LDS rows ([column or m][64 tokens], 128 bytes) hold their eight 8-token
-// chunks in a row-dependent order: chunk c of row r sits at c ^ swz(r). A 16-byte
-// operand read (8 consecutive tokens of 16 rows r0..r0+15) then spreads over all banks,
-// and so do the scattered 2-byte writes of one instruction (8 positions g*8 + e of a
-// token, for the four lane groups g).
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ (((r >> 3) & 3) << 1); }
-__device__ __forceinline__ int tslot(int r, int tok) { return r * kTile + (((tok >> 3) ^ swz(r)) << 3) + (tok & 7); }
+// The tile's x and gMix rows in LDS, by token as they came (16-byte writes), and the
+// transposing read that makes matrix-core operands of them: lane (j, g) gets column c0 + j of
+// the 8 tokens 8 g .. of a K-step (two ds_read_b64_tr_b16: each gives lane i of 16 the
+// column i of the 4 tokens x 16 columns that the 16 lanes address, lane i its token i / 4 and
+// columns 4 (i % 4) ..). A token's 16-byte chunks sit in a token-dependent order so that the 16
+// token rows of a read spread over the banks (32 bytes of each).
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+__device__ __forceinline__ bf16x8 read_tr(const char* at, int row_bytes)
+{
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at + 4 * row_bytes));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
 
 template <int N, int SGN, int KS>
 struct MainCfg {
@@ -380,16 +375,25 @@ struct MainCfg {
     static constexpr int CB = NCOL / 16;                  // gradPhi column blocks
     static constexpr int BPW = RB * CB / 4;               // gradPhi blocks per wave
     static constexpr int PACK_U = SGN * 2 * KS * 3 * 64;  // 16-byte units of packed phi
-    static constexpr int XS = kTile;                      // bf16 per transposed-x row
-    static constexpr int GXS = kTile;                     // bf16 per transposed-gMix row
+    static constexpr int XROW = NCOL * 2;                 // bytes of a token's x in LDS
+    // and of its gMix terms ([term][MP]): an odd number of 64-byte lines, so that four tokens'
+    // rows start on different quarters of the banks
+    static constexpr int GROW = 3 * MP * 2 % 128 ? 3 * MP * 2 : 3 * MP * 2 + 64;
+    // chunk order: chunk c of token k at c ^ swz (even: the 32 bytes of a read stay together)
+    __device__ static __forceinline__ int xswz(int k)
+    {
+        return NCOL == 128 ? 2 * ((k & 3) + 4 * ((k >> 3) & 1)) : 2 * (((k >> 1) & 1) + 2 * ((k >> 3) & 1));
+    }
+    __device__ static __forceinline__ int gswz(int k) { return 2 * ((k >> 3) & 1); }
     static constexpr int PACK_BYTES = PACK_U * 16;
-    static constexpr int XT_BYTES = NCOL * XS * 2;
-    static constexpr int GT_BYTES = 3 * MP * GXS * 2;     // three terms
+    static constexpr int XT_BYTES = kTile * XROW;
+    static constexpr int GT_BYTES = kTile * GROW;
     static constexpr int RED_BYTES = kTile * NCOL * 4;    // gradGamma reduction at the end
     static constexpr int MAIN_BYTES = PACK_BYTES + XT_BYTES + GT_BYTES;
     static constexpr int LDS_BYTES = MAIN_BYTES > RED_BYTES ? MAIN_BYTES : RED_BYTES;
     static_assert((RB * CB) % 4 == 0, "gradPhi blocks divide among the four waves");
     static_assert(CB % 4 == 0, "wave w's gradPhi blocks use column blocks w, w + 4, ..");
+    static_assert(NCOL == 64 || NCOL == 128, "xswz");
     static_assert(XT_BYTES % 16 == 0 && PACK_BYTES % 16 == 0, "LDS regions stay 16-byte aligned");
 };
 
@@ -405,8 +409,8 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     constexpr int NSG = N / SGN;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS_BYTES];
     u32x4* sp = reinterpret_cast<u32x4*>(lds);
-    uint16_t* xT = reinterpret_cast<uint16_t*>(lds + C::PACK_BYTES);
-    uint16_t* gT = reinterpret_cast<uint16_t*>(lds + C::PACK_BYTES + C::XT_BYTES);   // [term][m][token]
+    char* const xT = lds + C::PACK_BYTES;                 // [token][column]
+    char* const gT = lds + C::PACK_BYTES + C::XT_BYTES;   // [token][term][m]
 
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int j = lane & 15, grp = lane >> 4;
@@ -448,22 +452,29 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     // (where the registers allow it: no gamma, and not fp16 with gradXPost); the rest of a
     // tile's inputs after its predecessor's first phase, as with a single set
     constexpr bool DB = !GAMMA && !(XPOST && H);
-    XOctet<Q> xv[SGN], xv2[DB ? SGN : 1];
+    // the address unit is what bounds this kernel (some 65 cycles an instruction, 16 rows
+    // each), so small values come several to a load: a token's hPre of all SGN streams, and its
+    // streams' scale bytes, which lane (j, s) loads for stream s and hands to the others
+    typedef typename std::conditional<Q, u32x2, u32x4>::type XLoad;
+    XLoad xv[SGN], xv2[DB ? SGN : 1];
+    uint32_t xs = 0, xs2 = 0;
     u32x4 xp[SGN], gh, gh2, gmt[KS][3];
     float hp[SGN], c3;
-    auto load_xg = [&](int64_t tl, XOctet<Q> (&xd)[SGN], u32x4& ghd) {
+    auto load_xg = [&](int64_t tl, XLoad (&xd)[SGN], uint32_t& xsd, u32x4& ghd) {
         const int64_t t0 = tl * kTile;
         const int ntile = (int)(T - t0 < kTile ? T - t0 : kTile);
         const rsrc_t rx = Q ? make_rsrc(a.x_codes + t0 * K, (int64_t)ntile * K)
                             : make_rsrc(a.x + t0 * K, (int64_t)ntile * K * 2);
         const rsrc_t rgh = make_rsrc(a.grad_h_in + t0 * D, (int64_t)ntile * D * 2);
+        if constexpr (Q) {   // rows past the tile: a step of 0
+            const rsrc_t rs = make_rsrc(a.x_scales + t0 * N * nblk, (int64_t)ntile * N * nblk);
+            xsd = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (row * N + sg * SGN + grp % SGN) * nblk + b, 0, 0);
+        }
 #pragma unroll
         for (int s = 0; s < SGN; ++s) {
-            if constexpr (Q) {   // rows past the tile and positions past D: codes 0 at a step of 0
+            if constexpr (Q) {
                 const uint32_t off = dval ? (uint32_t)((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) : kOutOfRange;
-                const rsrc_t rs = make_rsrc(a.x_scales + t0 * N * nblk, (int64_t)ntile * N * nblk);
-                xd[s].c = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rx, (int)off, 0, 0));
-                xd[s].s = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (row * N + sg * SGN + s) * nblk + b, 0, 0);
+                xd[s] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rx, (int)off, 0, 0));
             } else {
                 const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
                 xd[s] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)off, 0, 0);
@@ -494,20 +505,26 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         // branch (a load under a branch leaves the compiler no exact wait count)
         const rsrc_t rhp = make_rsrc(a.h_pre + t0 * N, (int64_t)ntile * N * 4);
         const rsrc_t rc3 = make_rsrc(a.c3 + t0, (int64_t)ntile * 4);
+        if constexpr (SGN == 4) {
+            const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rhp, (row * N + sg * SGN) * 4, 0, 0));
 #pragma unroll
-        for (int s = 0; s < SGN; ++s)
-            hp[s] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rhp, (row * N + sg * SGN + s) * 4, 0, 0));
+            for (int s = 0; s < SGN; ++s) hp[s] = v[s];
+        } else {
+            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rhp, (row * N + sg * SGN) * 4, 0, 0));
+            hp[0] = __uint_as_float(v[0]);
+            hp[1] = __uint_as_float(v[1]);
+        }
         c3 = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rc3, row * 4, 0, 0));
     };
 
     const int64_t tile_end = (g + 1) * tpg < tiles ? (g + 1) * tpg : tiles;
-    load_xg(g * tpg, xv, gh);
+    load_xg(g * tpg, xv, xs, gh);
     load_rest(g * tpg);
-    auto step = [&](int64_t tile, XOctet<Q> (&xl)[SGN], u32x4& ghc, XOctet<Q> (&xn)[SGN], u32x4& ghn) __attribute__((always_inline)) {
+    auto step = [&](int64_t tile, XLoad (&xl)[SGN], uint32_t& xsc, u32x4& ghc, XLoad (&xn)[SGN], uint32_t& xsn, u32x4& ghn) __attribute__((always_inline)) {
         // the next tile's loads go out unconditionally (the last tile loads itself again), so
         // that every wait below has an exact count
         const int64_t nt = tile + 1 < tile_end ? tile + 1 : tile;
-        if constexpr (DB) load_xg(nt, xn, ghn);
+        if constexpr (DB) load_xg(nt, xn, xsn, ghn);
         const int64_t t0 = tile * kTile;
         const int ntile = (int)(T - t0 < kTile ? T - t0 : kTile);
 
@@ -536,7 +553,10 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 for (int r = 0; r < 4; ++r) xg[4 * h + r] = acc[r];
             }
             // gradX = gradHIn hPre + xrsGrad gamma - c3 x (+ gradXPost), one RNE to x's format
-            const u32x4 xc = x_values<H>(xl[s]);
+            u32x4 xc;
+            if constexpr (Q)
+                xc = ckpt_decode<H>(xl[s], ckpt_step((uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * s + j), (int)xsc)));
+            else xc = xl[s];
             u32x4 o;
 #pragma unroll
             for (int e2 = 0; e2 < 4; ++e2) {
@@ -555,21 +575,16 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
             }
             const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
             __builtin_amdgcn_raw_buffer_store_b128(o, rgx, (int)off, 0, 0);
-            // x of this tile, transposed: xT[local column][token]
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                xT[tslot(s * kDBlock + 8 * grp + e, row)] = (uint16_t)((xc[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+            // x of this tile for the gradPhi phase
+            *reinterpret_cast<u32x4*>(xT + row * C::XROW + 16 * ((4 * s + grp) ^ C::xswz(row))) = xc;
         }
-        // gMix terms of this tile, transposed: gT[p][m][token]
+        // and its gMix terms
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    gT[tslot(p * MP + 32 * ks + 8 * grp + e, row)] =
-                        (uint16_t)((gmt[ks][p][e >> 1] >> (16 * (e & 1))) & 0xffffu);
-        if constexpr (!DB) load_xg(nt, xn, ghn);
+                *reinterpret_cast<u32x4*>(gT + row * C::GROW + 16 * (((p * MP + 32 * ks) / 8 + grp) ^ C::gswz(row))) = gmt[ks][p];
+        if constexpr (!DB) load_xg(nt, xn, xsn, ghn);
         load_rest(nt);
         __syncthreads();
 
@@ -578,14 +593,20 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         // bi = wave + 4 q has column block (wave + 4 q) % CB = wave + 4 (q % NCW): fp16 x
         // is split into its two bf16 terms once per column block and K-step.
         constexpr int NCW = CB / 4;
+        const int tk = 8 * grp + (j >> 2);               // the lane's token of a K-step's reads
+        auto read_x = [&](int cb, int kt) {
+            return read_tr(xT + (32 * kt + tk) * C::XROW + 16 * ((2 * cb + ((j & 3) >> 1)) ^ C::xswz(tk)) + 8 * (j & 1), C::XROW);
+        };
+        auto read_g = [&](int p, int rb, int kt) {
+            return read_tr(gT + (32 * kt + tk) * C::GROW + 16 * (((p * MP + 16 * rb) / 8 + ((j & 3) >> 1)) ^ C::gswz(tk)) + 8 * (j & 1), C::GROW);
+        };
         bf16x8 bxh[H ? NCW : 1][2], bxl[H ? NCW : 1][2];
         if constexpr (H) {
 #pragma unroll
             for (int c = 0; c < NCW; ++c)
 #pragma unroll
                 for (int kt = 0; kt < 2; ++kt)
-                    split_f16x8(*reinterpret_cast<const u32x4*>(xT + tslot(16 * (wave + 4 * c) + j, 32 * kt + 8 * grp)),
-                                bxh[c][kt], bxl[c][kt]);
+                    split_f16x8(__builtin_bit_cast(u32x4, read_x(wave + 4 * c, kt)), bxh[c][kt], bxl[c][kt]);
         }
 #pragma unroll
         for (int q = 0; q < BPW; ++q) {
@@ -595,8 +616,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
             for (int kt = 0; kt < 2; ++kt) {
                 bf16x8 at[3];
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    at[p] = *reinterpret_cast<const bf16x8*>(gT + tslot(p * MP + 16 * rb + j, 32 * kt + 8 * grp));
+                for (int p = 0; p < 3; ++p) at[p] = read_g(p, rb, kt);
                 if constexpr (H) {
                     const int c = q % NCW;
 #pragma unroll
@@ -606,7 +626,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                     for (int p = 2; p >= 0; --p)
                         pacc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at[p], bxh[c][kt], pacc[q], 0, 0, 0);
                 } else {
-                    const bf16x8 bv = *reinterpret_cast<const bf16x8*>(xT + tslot(16 * cb + j, 32 * kt + 8 * grp));
+                    const bf16x8 bv = read_x(cb, kt);
 #pragma unroll
                     for (int p = 2; p >= 0; --p)
                         pacc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at[p], bv, pacc[q], 0, 0, 0);
@@ -617,11 +637,11 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     };
     if constexpr (DB) {
         for (int64_t tile = g * tpg; tile < tile_end; tile += 2) {
-            step(tile, xv, gh, xv2, gh2);
-            if (tile + 1 < tile_end) step(tile + 1, xv2, gh2, xv, gh);
+            step(tile, xv, xs, gh, xv2, xs2, gh2);
+            if (tile + 1 < tile_end) step(tile + 1, xv2, xs2, gh2, xv, xs, gh);
         }
     } else {
-        for (int64_t tile = g * tpg; tile < tile_end; ++tile) step(tile, xv, gh, xv, gh);
+        for (int64_t tile = g * tpg; tile < tile_end; ++tile) step(tile, xv, xs, gh, xv, xs, gh);
     }
 
     // gradPhi partial of the group: P[g][m][k], k = stream * D + d
