@@ -11,9 +11,14 @@
 // which the token's lanes join at the end. x and the residual streams only enter the sums,
 // so either may come as an 8-bit checkpoint, decoded in registers.
 //
-// Memory-bound: per token 2nD (G) + 2(n + 1)D (or 33/32 (n + 1)D) read, 2(n + 1)D written.
-// One wave per token where there are enough tokens to fill the chip (the sums then stay
-// within a wave), four where there are not (kManyTokens).
+// Memory-bound: per token 2nD (G) + 2(n + 1)D (or 33/32 (n + 1)D) read, 2(n + 1)D written. At
+// T = 16384, n = 4, D = 7168 from checkpoints 515 us, 5.3 TB/s (a large copy: 5.2).
+//
+// Four waves a token where each then still has a few octets a lane for the n + n*n sums
+// that it joins at the end (D >= 512 n), and for few tokens, which would leave the chip empty;
+// else one. Measured from checkpoints, T = 16384: n = 4, D = 7168 515 us against 535 with one
+// wave, D = 2048 133 against 148, D = 512 58 against 32; n = 6, D = 2048 214 against 212;
+// T = 512: n = 8, D = 7168 38 against 59.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -25,7 +30,7 @@ namespace mhc {
 namespace {
 
 constexpr int kThr = 256;
-constexpr int64_t kManyTokens = 4096;   // 4 waves for each of the chip's 1024 SIMDs
+constexpr int64_t kFewTokens = 512;
 
 // An octet of 16-bit values, or of codes with their step.
 template <bool H, bool Q> struct Octet;
@@ -63,7 +68,7 @@ __device__ __forceinline__ float wave_sum(float v)
 
 // W waves per token, 4 / W tokens per workgroup.
 template <int N, bool H, bool QX, bool QR>
-__global__ void __launch_bounds__(kThr)
+__global__ void __launch_bounds__(kThr, N == 8 ? (H ? 3 : 2) : 4 - N / 6)
 post_bwd_kernel(PostBwdArgs a, int64_t T, int D, int NB, int W)
 {
     constexpr int V = N + N * N;
@@ -120,6 +125,7 @@ post_bwd_kernel(PostBwdArgs a, int64_t T, int D, int NB, int W)
         __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(a.grad_x + tt * (int64_t)D + 8 * o));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            __builtin_amdgcn_sched_barrier(0);   // one stream's values decoded at a time, not all at once
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float re = rv[i].get(e);
@@ -166,7 +172,7 @@ post_bwd_kernel(PostBwdArgs a, int64_t T, int D, int NB, int W)
 template <int N, bool H>
 void launch(int64_t T, int D, const PostBwdArgs& a, hipStream_t st)
 {
-    const int W = T >= kManyTokens ? 1 : 4;
+    const int W = D >= 512 * N || T < kFewTokens ? 4 : 1;
     const dim3 grid((unsigned)(W == 1 ? (T + 3) / 4 : T));
     const int NB = ckpt_blocks(D);
     if (a.x && a.residual) hipLaunchKernelGGL((post_bwd_kernel<N, H, false, false>), grid, dim3(kThr), 0, st, a, T, D, NB, W);

@@ -46,7 +46,7 @@ def check(got, go, x, r, post, comb, f16):
 
 
 CASES = [(1, 4, 8), (3, 4, 40), (2, 6, 1000), (65, 8, 520), (130, 4, 2048), (7, 6, 16384), (5, 8, 16384), (4096, 4, 72), (4099, 6, 136),
-         (5001, 8, 64), (4097, 4, 1032)]
+         (5001, 8, 64), (4097, 4, 1032), (600, 4, 2056), (513, 8, 4104)]
 
 
 @pytest.mark.parametrize("f16", [False, True])
