@@ -399,15 +399,21 @@ struct MainCfg {
 
 // GAMMA: gamma given (gradX scales xrsGrad, gradGamma is summed); XPOST: gradXPost given;
 // H: x, gradHIn, gradXPost and gradX in fp16 (x then enters gMix^T . x as two exact bf16
-// terms, six products instead of three).
+// terms, six products instead of three). Q: x from its checkpoint; the workgroup's SGN blocks
+// of 32 columns are then a run of one stream's positions (run_task) instead of one d-block of
+// SGN streams. Every column's arithmetic is the same, so are the token groups, and the
+// results agree bit for bit; but a token row is read and written in stretches of 128 (codes)
+// and 256 bytes (gradHIn, gradX) at n = 4 instead of 32 and 64.
 template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
-__global__ void __launch_bounds__(kThreads, GAMMA ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, GAMMA || Q ? 2 : 3)
 bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, int64_t tasks)
 {
     using C = MainCfg<N, SGN, KS>;
     constexpr int M = C::M, MP = C::MP, NCOL = C::NCOL, CB = C::CB, BPW = C::BPW;
     constexpr int NSG = N / SGN;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS_BYTES];
+    // Q: a wave's gradX of a tile, its 16 tokens' runs as they lie in memory
+    __shared__ __attribute__((aligned(16))) char rows[Q ? C::XT_BYTES : 16];
     u32x4* sp = reinterpret_cast<u32x4*>(lds);
     char* const xT = lds + C::PACK_BYTES;                 // [token][column]
     char* const gT = lds + C::PACK_BYTES + C::XT_BYTES;   // [token][term][m]
@@ -416,13 +422,24 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     const int j = lane & 15, grp = lane >> 4;
     int64_t g;
     int b, sg;
-    if (!main_task(blockIdx.x, nblk, NSG, tasks, &g, &b, &sg)) return;   // padding workgroup
+    if (!(Q ? run_task(blockIdx.x, (nblk + SGN - 1) / SGN, N, tasks, &g, &b, &sg)   // b: the run, sg: the stream
+            : main_task(blockIdx.x, nblk, NSG, tasks, &g, &b, &sg)))
+        return;   // padding workgroup
     const int64_t K = (int64_t)N * D;
-    const int d0 = kDBlock * b + 8 * grp;          // the lane's 8 positions d0 .. d0+7
-    const bool dval = d0 < D;                        // D % 8 == 0: all 8 or none
+    // the lane's 8 positions of block s: stream st(s), positions d0(s) .. d0(s) + 7
+    auto st = [&](int s) { return Q ? sg : sg * SGN + s; };
+    auto d0 = [&](int s) { return kDBlock * (Q ? SGN * b + s : b) + 8 * grp; };
+    auto dval = [&](int s) { return d0(s) < D; };    // D % 8 == 0: all 8 or none
+    constexpr int GHN = Q ? SGN : 1;                 // octets of gradHIn a lane holds
 
     // the workgroup's packed phi (its d-block, its streams) into LDS
-    {
+    if constexpr (Q) {
+        constexpr int PER = C::PACK_U / SGN;
+        for (int u = tid; u < C::PACK_U; u += kThreads) {
+            const int db = SGN * b + u / PER < nblk ? SGN * b + u / PER : nblk - 1;   // past D: any
+            sp[u] = (static_cast<const u32x4*>(a.pack) + pack_at(db, sg, N, KS))[u % PER];
+        }
+    } else {
         const u32x4* src = static_cast<const u32x4*>(a.pack) + pack_at(b, sg * SGN, N, KS);
         for (int u = tid; u < C::PACK_U; u += kThreads) sp[u] = src[u];
     }
@@ -431,7 +448,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
 #pragma unroll
         for (int s = 0; s < SGN; ++s)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) gam[s][e] = dval ? a.gamma[(int64_t)(sg * SGN + s) * D + d0 + e] : 1.f;
+            for (int e = 0; e < 8; ++e) gam[s][e] = dval(s) ? a.gamma[(int64_t)st(s) * D + d0(s) + e] : 1.f;
     }
 
     float gg[GAMMA ? SGN : 1][8];
@@ -454,13 +471,13 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     constexpr bool DB = !GAMMA && !(XPOST && H);
     // the address unit is what bounds this kernel (some 65 cycles an instruction, 16 rows
     // each), so small values come several to a load: a token's hPre of all SGN streams, and its
-    // streams' scale bytes, which lane (j, s) loads for stream s and hands to the others
+    // blocks' scale bytes, which lane (j, s) loads for block s and hands to the others
     typedef typename std::conditional<Q, u32x2, u32x4>::type XLoad;
     XLoad xv[SGN], xv2[DB ? SGN : 1];
     uint32_t xs = 0, xs2 = 0;
-    u32x4 xp[SGN], gh, gh2, gmt[KS][3];
+    u32x4 xp[SGN], gh[GHN], gh2[DB ? GHN : 1], gmt[KS][3];
     float hp[SGN], c3;
-    auto load_xg = [&](int64_t tl, XLoad (&xd)[SGN], uint32_t& xsd, u32x4& ghd) {
+    auto load_xg = [&](int64_t tl, XLoad (&xd)[SGN], uint32_t& xsd, u32x4 (&ghd)[GHN]) {
         const int64_t t0 = tl * kTile;
         const int ntile = (int)(T - t0 < kTile ? T - t0 : kTile);
         const rsrc_t rx = Q ? make_rsrc(a.x_codes + t0 * K, (int64_t)ntile * K)
@@ -468,19 +485,22 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         const rsrc_t rgh = make_rsrc(a.grad_h_in + t0 * D, (int64_t)ntile * D * 2);
         if constexpr (Q) {   // rows past the tile: a step of 0
             const rsrc_t rs = make_rsrc(a.x_scales + t0 * N * nblk, (int64_t)ntile * N * nblk);
-            xsd = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (row * N + sg * SGN + grp % SGN) * nblk + b, 0, 0);
+            const int db = SGN * b + grp % SGN;
+            xsd = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, db < nblk ? (row * N + sg) * nblk + db : (int)kOutOfRange, 0, 0);
         }
 #pragma unroll
         for (int s = 0; s < SGN; ++s) {
             if constexpr (Q) {
-                const uint32_t off = dval ? (uint32_t)((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) : kOutOfRange;
+                const uint32_t off = dval(s) ? (uint32_t)((int64_t)row * K + (int64_t)st(s) * D + d0(s)) : kOutOfRange;
                 xd[s] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rx, (int)off, 0, 0));
             } else {
-                const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
+                const uint32_t off = dval(s) ? (uint32_t)(((int64_t)row * K + (int64_t)st(s) * D + d0(s)) * 2) : kOutOfRange;
                 xd[s] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)off, 0, 0);
             }
         }
-        ghd = __builtin_amdgcn_raw_buffer_load_b128(rgh, dval ? (int)(((int64_t)row * D + d0) * 2) : (int)kOutOfRange, 0, 0);
+#pragma unroll
+        for (int s = 0; s < GHN; ++s)
+            ghd[s] = __builtin_amdgcn_raw_buffer_load_b128(rgh, dval(s) ? (int)(((int64_t)row * D + d0(s)) * 2) : (int)kOutOfRange, 0, 0);
     };
     auto load_rest = [&](int64_t tl) {
         const int64_t t0 = tl * kTile;
@@ -490,7 +510,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
             const rsrc_t rxp = make_rsrc(a.grad_x_post + t0 * K, (int64_t)ntile * K * 2);
 #pragma unroll
             for (int s = 0; s < SGN; ++s) {
-                const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
+                const uint32_t off = dval(s) ? (uint32_t)(((int64_t)row * K + (int64_t)st(s) * D + d0(s)) * 2) : kOutOfRange;
                 xp[s] = __builtin_amdgcn_raw_buffer_load_b128(rxp, (int)off, 0, 0);
             }
         }
@@ -505,7 +525,11 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         // branch (a load under a branch leaves the compiler no exact wait count)
         const rsrc_t rhp = make_rsrc(a.h_pre + t0 * N, (int64_t)ntile * N * 4);
         const rsrc_t rc3 = make_rsrc(a.c3 + t0, (int64_t)ntile * 4);
-        if constexpr (SGN == 4) {
+        if constexpr (Q) {
+            const float v = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rhp, (row * N + sg) * 4, 0, 0));
+#pragma unroll
+            for (int s = 0; s < SGN; ++s) hp[s] = v;
+        } else if constexpr (SGN == 4) {
             const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rhp, (row * N + sg * SGN) * 4, 0, 0));
 #pragma unroll
             for (int s = 0; s < SGN; ++s) hp[s] = v[s];
@@ -520,7 +544,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     const int64_t tile_end = (g + 1) * tpg < tiles ? (g + 1) * tpg : tiles;
     load_xg(g * tpg, xv, xs, gh);
     load_rest(g * tpg);
-    auto step = [&](int64_t tile, XLoad (&xl)[SGN], uint32_t& xsc, u32x4& ghc, XLoad (&xn)[SGN], uint32_t& xsn, u32x4& ghn) __attribute__((always_inline)) {
+    auto step = [&](int64_t tile, XLoad (&xl)[SGN], uint32_t& xsc, u32x4 (&ghc)[GHN], XLoad (&xn)[SGN], uint32_t& xsn, u32x4 (&ghn)[GHN]) __attribute__((always_inline)) {
         // the next tile's loads go out unconditionally (the last tile loads itself again), so
         // that every wait below has an exact count
         const int64_t nt = tile + 1 < tile_end ? tile + 1 : tile;
@@ -565,7 +589,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 for (int hl = 0; hl < 2; ++hl) {
                     const int e = 2 * e2 + hl;
                     const float xe = hl ? x16_hi<H>(xc[e2]) : x16_lo<H>(xc[e2]);
-                    const float ge = hl ? x16_hi<H>(ghc[e2]) : x16_lo<H>(ghc[e2]);
+                    const float ge = hl ? x16_hi<H>(ghc[Q ? s : 0][e2]) : x16_lo<H>(ghc[Q ? s : 0][e2]);
                     v[hl] = fmaf(ge, hp[s], GAMMA ? xg[e] * gam[GAMMA ? s : 0][e] : xg[e]);
                     v[hl] = fmaf(-c3, xe, v[hl]);
                     if constexpr (XPOST) v[hl] += hl ? x16_hi<H>(xp[s][e2]) : x16_lo<H>(xp[s][e2]);
@@ -573,10 +597,26 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 }
                 o[e2] = pack_x16<H>(v[0], v[1]);
             }
-            const uint32_t off = dval ? (uint32_t)(((int64_t)row * K + (int64_t)(sg * SGN + s) * D + d0) * 2) : kOutOfRange;
-            __builtin_amdgcn_raw_buffer_store_b128(o, rgx, (int)off, 0, 0);
+            if constexpr (Q) {
+                *reinterpret_cast<u32x4*>(rows + row * C::XROW + 16 * ((4 * s + grp) ^ (j % (4 * SGN)))) = o;
+            } else {
+                const uint32_t off = dval(s) ? (uint32_t)(((int64_t)row * K + (int64_t)st(s) * D + d0(s)) * 2) : kOutOfRange;
+                __builtin_amdgcn_raw_buffer_store_b128(o, rgx, (int)off, 0, 0);
+            }
             // x of this tile for the gradPhi phase
             *reinterpret_cast<u32x4*>(xT + row * C::XROW + 16 * ((4 * s + grp) ^ C::xswz(row))) = xc;
+        }
+        if constexpr (Q) {   // gradX leaves in whole runs: 4 SGN lanes a token (the wave's own rows: no barrier)
+            constexpr int LPR = 4 * SGN, RPI = 64 / LPR;
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+                const int r = RPI * i + lane / LPR, c = lane % LPR, d = kDBlock * SGN * b + 8 * c;
+                const u32x4 v = *reinterpret_cast<const u32x4*>(rows + (16 * wave + r) * C::XROW + 16 * (c ^ (r % LPR)));
+                const uint32_t off = d < D ? (uint32_t)(((int64_t)(16 * wave + r) * K + (int64_t)sg * D + d) * 2) : kOutOfRange;
+                __builtin_amdgcn_raw_buffer_store_b128(v, rgx, (int)off, 0, 0);
+            }
+            __builtin_amdgcn_wave_barrier();
         }
         // and its gMix terms
 #pragma unroll
@@ -651,11 +691,11 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         const int bi = wave + 4 * q;
         const int rb = bi / CB, cb = bi % CB;
         const int col = 16 * cb + j;                 // local column
-        const int s = col / kDBlock, dd = kDBlock * b + col % kDBlock;
+        const int s = col / kDBlock, dd = kDBlock * (Q ? SGN * b + s : b) + col % kDBlock;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int m = 16 * rb + 4 * grp + r;
-            if (m < M && dd < D) P[(int64_t)m * K + (int64_t)(sg * SGN + s) * D + dd] = pacc[q][r];
+            if (m < M && dd < D) P[(int64_t)m * K + (int64_t)st(s) * D + dd] = pacc[q][r];
         }
     }
     // gradGamma partial of the group: sum the 64 token lanes of each column in a fixed order
@@ -669,8 +709,8 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         for (int col = tid; col < NCOL; col += kThreads) {
             float v = 0.f;
             for (int rr = 0; rr < kTile; ++rr) v += red[rr * NCOL + col];
-            const int s = col / kDBlock, dd = kDBlock * b + col % kDBlock;
-            if (dd < D) a.pgam[g * K + (int64_t)(sg * SGN + s) * D + dd] = v;
+            const int s = col / kDBlock, dd = kDBlock * (Q ? SGN * b + s : b) + col % kDBlock;
+            if (dd < D) a.pgam[g * K + (int64_t)st(s) * D + dd] = v;
         }
     }
 }
@@ -751,8 +791,10 @@ bwd_zero_kernel(Args a, int64_t MK, int64_t K, int M)
 template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
 void launch_main(const Plan& p, const Args& a, hipStream_t st)
 {
-    hipLaunchKernelGGL((bwd_main_kernel<N, SGN, KS, GAMMA, XPOST, H, Q>), dim3((unsigned)p.main_blocks),
-                       dim3(kThreads), 0, st, a, p.T, p.g.D, p.g.nblk, p.tpg, p.tiles, p.main_tasks);
+    const int64_t tasks = Q ? run_tasks_for(p.G, p.g.nblk, SGN, N) : p.main_tasks;
+    const int64_t blocks = Q ? run_blocks_for(tasks, N) : p.main_blocks;
+    hipLaunchKernelGGL((bwd_main_kernel<N, SGN, KS, GAMMA, XPOST, H, Q>), dim3((unsigned)blocks),
+                       dim3(kThreads), 0, st, a, p.T, p.g.D, p.g.nblk, p.tpg, p.tiles, tasks);
 }
 
 template <int N, int SGN, int KS, bool H, bool Q>

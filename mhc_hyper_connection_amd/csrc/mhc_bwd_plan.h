@@ -15,7 +15,7 @@
 //                SGN streams): for each tile of 64 tokens, xrsGrad = gMix . phi on the
 //                matrix cores (phi^T as the A operand, packed per d-block; gMix as B),
 //                gradX, and the tile's share of gradGamma (x * xrsGrad) and gradPhi
-//                (gMix^T . x on the matrix cores, x transposed through LDS); the group's
+//                (gMix^T . x on the matrix cores, x transposed on its way out of LDS); the group's
 //                sums go to partial buffers.
 //   reduction    gradPhi = gamma (.) sum over groups, gradGamma = sum over groups, gradAlpha
 //                and gradBias = sums over tokens; every sum in a fixed order in fp64.
@@ -108,6 +108,23 @@ MHC_BWD_HOST_DEVICE inline bool main_task(int64_t blk, int nblk, int NSG, int64_
     const int64_t gs = t / nblk;
     *sg = (int)(gs % NSG);
     *grp = gs / NSG;
+    return true;
+}
+
+// The same for x from its checkpoint: a task is (token group, run of SGN d-blocks, stream).
+// The n streams of a run share gradHIn and gMix, and their tasks go to workgroups b, b + 8, ..
+// of one XCD.
+MHC_BWD_HOST_DEVICE inline int64_t run_tasks_for(int64_t G, int nblk, int SGN, int n) { return G * ((nblk + SGN - 1) / SGN) * n; }
+MHC_BWD_HOST_DEVICE inline int64_t run_blocks_for(int64_t tasks, int n) { return (tasks + 8 * n - 1) / (8 * n) * (8 * n); }
+MHC_BWD_HOST_DEVICE inline bool run_task(int64_t blk, int runs, int n, int64_t tasks, int64_t* grp, int* run, int* stream)
+{
+    const int64_t q = blk % 8, r = blk / 8;
+    const int64_t t = ((r / n) * 8 + q) * n + r % n;
+    if (t >= tasks) return false;
+    *stream = (int)(t % n);
+    const int64_t gr = t / n;
+    *run = (int)(gr % runs);
+    *grp = gr / runs;
     return true;
 }
 

@@ -99,43 +99,6 @@ struct TileArgs {
     float* part;           // their fp32 results, [tile][part][block of results][thread]
 };
 
-// Workgroup -> tile and part. Workgroups b, b + 8, .. run on one XCD; each XCD takes a
-// contiguous run of the tile order, which walks the columns of kGroup rows of tiles before the
-// next rows: the tiles in flight on an XCD then share kGroup row operands and a few column
-// operands in its L2 (4 against 2, 8 and 16: within 2 % of the best for every product). The
-// split tiles follow, the same part of neighbouring tiles side by side.
-constexpr uint32_t kGroup = 4;
-struct Unit {
-    uint32_t a, b, tile;
-    int part;
-};
-__device__ __forceinline__ void place(uint32_t t, uint32_t na, uint32_t nb, Unit* u)
-{
-    const uint32_t group = t / (kGroup * nb), r = t - group * kGroup * nb;
-    const uint32_t rows = na - group * kGroup < kGroup ? na - group * kGroup : kGroup;
-    u->tile = t;
-    u->b = r / rows;
-    u->a = group * kGroup + (r - u->b * rows);
-}
-__device__ __forceinline__ bool unit_of(const TileArgs& p, Unit* u)
-{
-    const uint32_t first = (p.whole + 7) / 8;          // of the whole tiles, on each XCD
-    const uint32_t xcd = blockIdx.x % 8, i = blockIdx.x / 8;
-    if (i < first) {
-        const uint32_t t = xcd * first + i;
-        if (t >= p.whole) return false;
-        u->part = -1;
-        place(t, p.na, p.nb, u);
-        return true;
-    }
-    const uint32_t rest = p.na * p.nb - p.whole, units = rest * p.split, per = (units + 7) / 8;
-    const uint32_t v = xcd * per + (i - first);
-    if (i - first >= per || v >= units) return false;
-    u->part = (int)(v / rest);
-    place(p.whole + v % rest, p.na, p.nb, u);
-    return true;
-}
-
 // A wave's results of a gated tile, from f0 on and for tokens t0, t0 + 16, ..: lane values of g in
 // acc[0 .. IA/2), of u in the rest, 8 consecutive f in a pair of blocks.
 template <int MODE, bool H, int ACT, int IA, int IB>
@@ -221,7 +184,7 @@ tile_kernel(TileArgs p)
     __shared__ __attribute__((aligned(1024))) char lds[RA * ASZ + RB * BSZ];
 
     Unit unit;
-    if (!unit_of(p, &unit)) return;   // the padding of an XCD's run
+    if (!unit_of(blockIdx.x, p.na, p.nb, p.whole, p.split, &unit)) return;   // the padding of an XCD's run
     const int64_t ta = unit.a, tb = unit.b;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wa = wave / WB, wb = wave % WB;
