@@ -378,6 +378,95 @@ def main_post(args):
     print(json.dumps(line), flush=True)
 
 
+TRAIN_OPS = ("checkpoint", "post_checkpoint", "post_backward", "backward_checkpoint", "glu", "glu_backward")
+
+
+def train_work(op, T, n, D, F, iters=20):
+    """(bytes, flops) that one call cannot do without: each input read once, each output
+    written once. A checkpoint is 1 + 1/32 bytes a value."""
+    el, ck, gates = T * n * D, T * n * (D + (D + 31) // 32), 4 * T * (n + n * n)
+    ckx = T * (D + (D + 31) // 32)
+    if op == "checkpoint":
+        return 2 * el + ck, 0
+    if op == "post_checkpoint":
+        return 2 * T * D + 4 * el + ck + gates, 2 * el * (n + 1)
+    if op == "post_backward":
+        return 4 * el + 2 * T * D + ck + ckx + 2 * gates, 4 * el * (n + 1)
+    if op == "backward_checkpoint":
+        return bwd_algorithmic_bytes(T, n, D, num_iters=iters) - 2 * el + ck, 4 * el * (n * n + 2 * n)
+    w = 4 * F * D
+    if op == "glu":
+        return 2 * T * D + w + 2 * T * F, 4 * T * D * F
+    return ckx + 2 * w + 2 * T * D + 4 * T * F, 12 * T * D * F
+
+
+def main_train(args):
+    """--op checkpoint, post_checkpoint, post_backward, backward_checkpoint (T = 16384, n = 4,
+    D = 7168), glu and glu_backward (T = 8192, D = 7168, F = 14336): one step = one call of
+    mhc_checkpoint, mhc_post_checkpoint, mhc_post_backward and mhc_pre_backward (activations
+    from their checkpoints), mhc_glu, mhc_glu_backward (x from its checkpoint, with h)."""
+    import torch
+
+    import mhc_hyper_connection_amd as mhc
+
+    op, n, D, F = args.op, 4, 7168, 14336
+    T = 8192 if op.startswith("glu") else 16384
+    dev = torch.device("cuda", 0)
+    g = torch.Generator(device=dev).manual_seed(1005)
+    f32 = lambda *s: torch.randn(*s, generator=g, device=dev)
+    b16 = lambda *s, std=1.0: (std * f32(*s)).to(torch.bfloat16)
+    if op.startswith("glu"):
+        x, wg, wu = b16(T, D), b16(F, D, std=D ** -0.5), b16(F, D, std=D ** -0.5)
+        if op == "glu":
+            out = torch.empty((T, F), dtype=torch.bfloat16, device=dev)
+            step = lambda: mhc.mhc_glu(x, wg, wu, out=out)
+        else:
+            gh, ck = b16(T, F), mhc.mhc_checkpoint(x)
+            step = lambda: mhc.mhc_glu_backward(gh, ck, wg, wu, need_h=True)
+    else:
+        streams, x = b16(T, n, D), b16(T, D)
+        post, comb = torch.rand((T, n), generator=g, device=dev), torch.softmax(f32(T, n, n), -1)
+        ck, ckx = mhc.mhc_checkpoint(streams), mhc.mhc_checkpoint(x)
+        if op == "checkpoint":
+            step = lambda: mhc.mhc_checkpoint(streams, out=ck)
+        elif op == "post_checkpoint":
+            out = torch.empty_like(streams)
+            step = lambda: mhc.mhc_post_checkpoint(x, streams, post, comb, out=out, checkpoint=ck)
+        elif op == "post_backward":
+            step = lambda: mhc.mhc_post_backward(streams, ckx, ck, post, comb)
+        else:
+            M = n * n + 2 * n
+            phi, alpha, bias = f32(M, n * D) * (n * D) ** -0.5, torch.ones(3, device=dev), torch.zeros(M, device=dev)
+            _, h_post, h_res, s = mhc.mhc_pre(streams, phi, alpha, bias, need_backward=True)
+            step = lambda: mhc.mhc_pre_backward(ck, phi, alpha, x, h_post, h_res, s["inv_rms"], s["h_mix"], s["h_pre"], h_post,
+                                                num_iters=20, sum_out=s["sum_out"], norm_out=s["norm_out"])
+    stream = torch.cuda.current_stream(dev)
+    print(f"[bench] {op}: warmup {args.warmup}, then {args.steps} steps", file=sys.stderr, flush=True)
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize(dev)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t0 = time.perf_counter()
+    a.record(stream)
+    for _ in range(args.steps):
+        step()
+    b.record(stream)
+    torch.cuda.synchronize(dev)
+    ms_step = (time.perf_counter() - t0) * 1e3 / args.steps
+    call_us = a.elapsed_time(b) * 1e3 / args.steps
+    nbytes, flops = train_work(op, T, n, D, F)
+    compute = op.startswith("glu")
+    achieved, peak = (flops / call_us / 1e6, 2500.0) if compute else (nbytes / call_us / 1e3, HBM_PEAK_GBS)
+    print(json.dumps({
+        "metric": f"tokens/s of {op}", "value": T / (ms_step * 1e-3), "unit": "tokens/s", "n_gpus": 1,
+        "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms_step, "higher_is_better": True, "scaling": "weak",
+        "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": op, "T": T, "D": D, **({"F": F} if compute else {"n": n}), "step": "one call (all of its kernels)"},
+        "roofline": {"bound": "mfma" if compute else "hbm", "achieved": achieved, "peak": peak,
+                     "unit": "TFLOP/s" if compute else "GB/s", "frac": achieved / peak, "kernel": "whole call",
+                     "algorithmic_bytes": nbytes, "algorithmic_flops": flops, "avg_launch_us": call_us}}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -400,9 +489,10 @@ def main():
                          "per-kernel pass (0: none; decode never flushes)")
     ap.add_argument("--calib-copy-mib", type=int, default=0,
                     help="run a plain copy of this size first (for counter calibration)")
-    ap.add_argument("--op", choices=("forward", "backward", "post"), default="forward",
+    ap.add_argument("--op", choices=("forward", "backward", "post", *TRAIN_OPS), default="forward",
                     help="forward (default): the pre-mapping forward line; backward: the "
-                         "MhcPre backward at the large prefill shape; post: hc_post at that shape")
+                         "MhcPre backward at the large prefill shape; post: hc_post at that shape; "
+                         "the others: the sub-layer's training operators (main_train)")
     ap.add_argument("--bwd-iters", type=int, default=20,
                     help="Sinkhorn iterations of the backward (0: the MhcPre backward)")
     ap.add_argument("--bwd-f16", action="store_true",
@@ -419,6 +509,9 @@ def main():
         return
     if args.op == "post":
         main_post(args)
+        return
+    if args.op in TRAIN_OPS:
+        main_train(args)
         return
 
     import torch

@@ -200,3 +200,15 @@ def test_python_glu_checks():
     raises("exactly", b, gh, x, wg, wu, out={"grad_x": x})
     raises("exactly", b, gh, x, wg, wu, need_h=True, out={"grad_x": x, "grad_w_gate": wg, "grad_w_up": wu})
     raises("GPU", b, gh, zck(3, 64), wg, wu)
+
+
+def test_bench_work_matches_the_hand_count():
+    import bench
+    T, n, D, F = 16384, 4, 7168, 14336
+    ck = T * n * (D + 224)
+    assert bench.train_work("checkpoint", T, n, D, F) == (2 * T * n * D + ck, 0)
+    assert bench.train_work("post_checkpoint", T, n, D, F)[0] == T * (2 * D + 4 * n * D + 4 * n + 4 * n * n) + ck
+    assert bench.train_work("post_backward", T, n, D, F)[0] == T * (4 * n * D + 2 * D + D + 224 + 8 * n + 8 * n * n) + ck
+    assert bench.train_work("backward_checkpoint", T, n, D, F)[0] == bench.bwd_algorithmic_bytes(T, n, D, num_iters=20) - 2 * T * n * D + ck
+    assert bench.train_work("glu", T, n, D, F) == (2 * (T * D + 2 * F * D + T * F), 4 * T * D * F)
+    assert bench.train_work("glu_backward", T, n, D, F) == (T * (D + 224) + 8 * F * D + 2 * T * D + 4 * T * F, 12 * T * D * F)
