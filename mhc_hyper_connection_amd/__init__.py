@@ -400,6 +400,8 @@ def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms,
     dict grad_x, grad_phi, grad_alpha, grad_bias (and grad_gamma when gamma is given)."""
     ck = x if isinstance(x, Checkpoint) else None
     xt = x if ck is None else ck.codes
+    if ck is not None and xt.dim() < 2:
+        raise ValueError(f"x: codes of shape {tuple(xt.shape)}, expected [..., n, D]")
     lead = tuple(xt.shape[:-2])
     n, D = int(xt.shape[-2]), int(xt.shape[-1])
     T = math.prod(lead) if lead else 1
@@ -407,6 +409,7 @@ def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms,
     if ck is not None:
         if D % 8:
             raise ValueError(f"x: D = {D}, expected a multiple of 8")
+        _check_checkpoint(ck, "x", ck.dtype, tuple(xt.shape), xt.device)
         r = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters, x_f16=f16, device=xt.device)
         x2 = Checkpoint(ck.codes.reshape(T, n, D), ck.scales.reshape(T, n, -(-D // CHECKPOINT_BLOCK)), ck.dtype)
     else:

@@ -411,15 +411,17 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     using C = MainCfg<N, SGN, KS>;
     constexpr int M = C::M, MP = C::MP, NCOL = C::NCOL, CB = C::CB, BPW = C::BPW;
     constexpr int NSG = N / SGN;
-    __shared__ __attribute__((aligned(16))) char lds[C::LDS_BYTES];
-    // Q: a wave's gradX of a tile, its 16 tokens' runs as they lie in memory
-    __shared__ __attribute__((aligned(16))) char rows[Q ? C::XT_BYTES : 16];
+    // Q: a wave's gradX of a tile passes through LDS, its 16 tokens' runs as they lie in memory:
+    // where its own gMix rows go next, if they are long enough (they are written after it)
+    constexpr bool OWN = Q && C::GROW < C::XROW;
+    __shared__ __attribute__((aligned(16))) char lds[C::LDS_BYTES + (OWN ? C::XT_BYTES : 0)];
     u32x4* sp = reinterpret_cast<u32x4*>(lds);
     char* const xT = lds + C::PACK_BYTES;                 // [token][column]
     char* const gT = lds + C::PACK_BYTES + C::XT_BYTES;   // [token][term][m]
 
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int j = lane & 15, grp = lane >> 4;
+    char* const rows = OWN ? lds + C::LDS_BYTES + 16 * wave * C::XROW : gT + 16 * wave * C::GROW;
     int64_t g;
     int b, sg;
     if (!(Q ? run_task(blockIdx.x, (nblk + SGN - 1) / SGN, N, tasks, &g, &b, &sg)   // b: the run, sg: the stream
@@ -598,7 +600,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 o[e2] = pack_x16<H>(v[0], v[1]);
             }
             if constexpr (Q) {
-                *reinterpret_cast<u32x4*>(rows + row * C::XROW + 16 * ((4 * s + grp) ^ (j % (4 * SGN)))) = o;
+                *reinterpret_cast<u32x4*>(rows + j * C::XROW + 16 * ((4 * s + grp) ^ (j % (4 * SGN)))) = o;
             } else {
                 const uint32_t off = dval(s) ? (uint32_t)(((int64_t)row * K + (int64_t)st(s) * D + d0(s)) * 2) : kOutOfRange;
                 __builtin_amdgcn_raw_buffer_store_b128(o, rgx, (int)off, 0, 0);
@@ -612,7 +614,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
 #pragma unroll
             for (int i = 0; i < 16 / RPI; ++i) {
                 const int r = RPI * i + lane / LPR, c = lane % LPR, d = kDBlock * SGN * b + 8 * c;
-                const u32x4 v = *reinterpret_cast<const u32x4*>(rows + (16 * wave + r) * C::XROW + 16 * (c ^ (r % LPR)));
+                const u32x4 v = *reinterpret_cast<const u32x4*>(rows + r * C::XROW + 16 * (c ^ (r % LPR)));
                 const uint32_t off = d < D ? (uint32_t)(((int64_t)(16 * wave + r) * K + (int64_t)sg * D + d) * 2) : kOutOfRange;
                 __builtin_amdgcn_raw_buffer_store_b128(v, rgx, (int)off, 0, 0);
             }

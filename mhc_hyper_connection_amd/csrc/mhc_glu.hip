@@ -106,54 +106,54 @@ __device__ __forceinline__ void gated_results(const TileArgs& p, int64_t f0, int
 {
     const int64_t T = p.T;
     const int F = p.F;
-            u32x4 dh[IB][IA / 4];
-            if constexpr (MODE == kRecompute) {   // all of them on their way before the first is used
-    #pragma unroll
-                for (int q = 0; q < IB; ++q)
-    #pragma unroll
-                    for (int i = 0; i < IA / 4; ++i) {
-                        const int64_t t = t0 + 16 * q < T ? t0 + 16 * q : T - 1, f = f0 + 32 * i < F ? f0 + 32 * i : 0;
-                        dh[q][i] = *reinterpret_cast<const u32x4*>(p.t.grad_h + t * F + f);
-                    }
+    u32x4 dh[IB][IA / 4];
+    if constexpr (MODE == kRecompute) {   // all of them on their way before the first is used
+#pragma unroll
+        for (int q = 0; q < IB; ++q)
+#pragma unroll
+            for (int i = 0; i < IA / 4; ++i) {
+                const int64_t t = t0 + 16 * q < T ? t0 + 16 * q : T - 1, f = f0 + 32 * i < F ? f0 + 32 * i : 0;
+                dh[q][i] = *reinterpret_cast<const u32x4*>(p.t.grad_h + t * F + f);
             }
-    #pragma unroll
-            for (int q = 0; q < IB; ++q) {
-                const int64_t t = t0 + 16 * q;
-    #pragma unroll
-                for (int i = 0; i < IA / 4; ++i) {
-                    const int64_t f = f0 + 32 * i;
-                    u32x4 hv, gv, uv;
-    #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float hh[2], dg[2], du[2];
-    #pragma unroll
-                        for (int l = 0; l < 2; ++l) {
-                            const int r = 2 * e + l;                            // f + r
-                            const float gg = acc[2 * i + r / 4][q][r % 4], uu = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
-                            const Act ac = activation<ACT>(gg);
-                            hh[l] = ac.a * uu;
+    }
+#pragma unroll
+    for (int q = 0; q < IB; ++q) {
+        const int64_t t = t0 + 16 * q;
+#pragma unroll
+        for (int i = 0; i < IA / 4; ++i) {
+            const int64_t f = f0 + 32 * i;
+            u32x4 hv, gv, uv;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float hh[2], dg[2], du[2];
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    const int r = 2 * e + l;                            // f + r
+                    const float gg = acc[2 * i + r / 4][q][r % 4], uu = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
+                    const Act ac = activation<ACT>(gg);
+                    hh[l] = ac.a * uu;
                     asm("" : "+v"(hh[l]));   // rounded to fp32 before fp16, in the forward as in the backward
-                            if constexpr (MODE == kRecompute) {
-                                const float d = l ? x16_hi<H>(dh[q][i][e]) : x16_lo<H>(dh[q][i][e]);
-                                dg[l] = d * uu * ac.da;
-                                du[l] = d * ac.a;
-                            }
-                        }
-                        hv[e] = pack_x16<H>(hh[0], hh[1]);
-                        if constexpr (MODE == kRecompute) {
-                            gv[e] = pack_x16<H>(dg[0], dg[1]);
-                            uv[e] = pack_x16<H>(du[0], du[1]);
-                        }
-                    }
-                    if (t < T && f < F) {
-                        if (MODE == kForward || p.t.h) *reinterpret_cast<u32x4*>(p.t.h + t * F + f) = hv;
-                        if constexpr (MODE == kRecompute) {
-                            *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + f) = gv;
-                            *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + F + f) = uv;
-                        }
+                    if constexpr (MODE == kRecompute) {
+                        const float d = l ? x16_hi<H>(dh[q][i][e]) : x16_lo<H>(dh[q][i][e]);
+                        dg[l] = d * uu * ac.da;
+                        du[l] = d * ac.a;
                     }
                 }
+                hv[e] = pack_x16<H>(hh[0], hh[1]);
+                if constexpr (MODE == kRecompute) {
+                    gv[e] = pack_x16<H>(dg[0], dg[1]);
+                    uv[e] = pack_x16<H>(du[0], du[1]);
+                }
             }
+            if (t < T && f < F) {
+                if (MODE == kForward || p.t.h) *reinterpret_cast<u32x4*>(p.t.h + t * F + f) = hv;
+                if constexpr (MODE == kRecompute) {
+                    *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + f) = gv;
+                    *reinterpret_cast<u32x4*>(p.t.dgu + t * 2 * F + F + f) = uv;
+                }
+            }
+        }
+    }
 }
 
 // WA x WB waves of IA x IB 16 x 16 results each. A stage of the reduction is kBK = 64 positions,

@@ -212,3 +212,12 @@ def test_bench_work_matches_the_hand_count():
     assert bench.train_work("backward_checkpoint", T, n, D, F)[0] == bench.bwd_algorithmic_bytes(T, n, D, num_iters=20) - 2 * T * n * D + ck
     assert bench.train_work("glu", T, n, D, F) == (2 * (T * D + 2 * F * D + T * F), 4 * T * D * F)
     assert bench.train_work("glu_backward", T, n, D, F) == (T * (D + 224) + 8 * F * D + 2 * T * D + 4 * T * F, 12 * T * D * F)
+
+
+def test_python_pre_backward_checks_the_checkpoint_before_it_reshapes():
+    n, D, T = 4, 64, 3
+    M = n * n + 2 * n
+    args = lambda: [z(M, n * D), z(3), z(T, D, dt=bf), z(T, n), z(T, n, n), z(T), z(T, M), z(T, n), z(T, n)]
+    raises("scales: shape", mhc.mhc_pre_backward, mhc.Checkpoint(z(T, n, D, dt=torch.int8), z(T, n, 3, dt=torch.uint8), bf), *args())
+    raises("contiguous", mhc.mhc_pre_backward, mhc.Checkpoint(z(T, D, n, dt=torch.int8).transpose(1, 2), z(T, n, 2, dt=torch.uint8), bf), *args())
+    raises(r"\[..., n, D\]", mhc.mhc_pre_backward, mhc.Checkpoint(z(D, dt=torch.int8), z(2, dt=torch.uint8), bf), *args())
