@@ -18,8 +18,8 @@
 //                       = phi^T . gMix^T per (d-block, stream, half, K-step, term)
 //   bwd_token_kernel    one wave per token: the hPre gradient in fp64, the gate backward,
 //                       gMix, c3 = gInv invRms^3 / (n D), and the token's alpha/bias terms
-//   bwd_main_kernel     one workgroup per (token group, d-block, stream group): per tile
-//                       of 64 tokens, xrsGrad on the matrix cores (phi terms x gMix terms,
+//   bwd_main_kernel     one workgroup per (token group, d-block, stream group), or per (token
+//                       group, run of d-blocks, stream) for large x: per tile of 64 tokens, xrsGrad on the matrix cores (phi terms x gMix terms,
 //                       six products), gradX, the gradGamma sums, and gMix^T . x on the
 //                       matrix cores, both transposed on their way out of LDS; group sums to
 //                       partials
@@ -399,21 +399,23 @@ struct MainCfg {
 
 // GAMMA: gamma given (gradX scales xrsGrad, gradGamma is summed); XPOST: gradXPost given;
 // H: x, gradHIn, gradXPost and gradX in fp16 (x then enters gMix^T . x as two exact bf16
-// terms, six products instead of three). Q: x from its checkpoint; the workgroup's SGN blocks
-// of 32 columns are then a run of one stream's positions (run_task) instead of one d-block of
-// SGN streams. Every column's arithmetic is the same, so are the token groups, and the
-// results agree bit for bit; but a token row is read and written in stretches of 128 (codes)
-// and 256 bytes (gradHIn, gradX) at n = 4 instead of 32 and 64.
-template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
-__global__ void __launch_bounds__(kThreads, GAMMA || Q ? 2 : 3)
+// terms, six products instead of three). Q: x from its checkpoint. RUN: the workgroup's SGN
+// blocks of 32 columns are a run of one stream's positions (run_task), not one d-block of SGN
+// streams (main_task). Every column's arithmetic is the same, and so are the token groups: the
+// results agree bit for bit; but a token row is read and written in stretches of 256 bytes (128
+// of codes) at n = 4 instead of 64 (32). (T = 16384, n = 4, D = 7168: 738 us against 852 from a
+// checkpoint, 800 against 915 from bf16 x, whole call.)
+template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q, bool RUN>
+__global__ void __launch_bounds__(kThreads, GAMMA || RUN ? 2 : 3)
 bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, int64_t tasks)
 {
     using C = MainCfg<N, SGN, KS>;
     constexpr int M = C::M, MP = C::MP, NCOL = C::NCOL, CB = C::CB, BPW = C::BPW;
     constexpr int NSG = N / SGN;
-    // Q: a wave's gradX of a tile passes through LDS, its 16 tokens' runs as they lie in memory:
+    static_assert(RUN || !Q, "a checkpoint's scale bytes are loaded by the run");
+    // RUN: a wave's gradX of a tile passes through LDS, its 16 tokens' runs as they lie in memory:
     // where its own gMix rows go next, if they are long enough (they are written after it)
-    constexpr bool OWN = Q && C::GROW < C::XROW;
+    constexpr bool OWN = RUN && C::GROW < C::XROW;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS_BYTES + (OWN ? C::XT_BYTES : 0)];
     u32x4* sp = reinterpret_cast<u32x4*>(lds);
     char* const xT = lds + C::PACK_BYTES;                 // [token][column]
@@ -424,18 +426,18 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     char* const rows = OWN ? lds + C::LDS_BYTES + 16 * wave * C::XROW : gT + 16 * wave * C::GROW;
     int64_t g;
     int b, sg;
-    if (!(Q ? run_task(blockIdx.x, (nblk + SGN - 1) / SGN, N, tasks, &g, &b, &sg)   // b: the run, sg: the stream
-            : main_task(blockIdx.x, nblk, NSG, tasks, &g, &b, &sg)))
+    if (!(RUN ? run_task(blockIdx.x, (nblk + SGN - 1) / SGN, N, tasks, &g, &b, &sg)   // b: the run, sg: the stream
+              : main_task(blockIdx.x, nblk, NSG, tasks, &g, &b, &sg)))
         return;   // padding workgroup
     const int64_t K = (int64_t)N * D;
     // the lane's 8 positions of block s: stream st(s), positions d0(s) .. d0(s) + 7
-    auto st = [&](int s) { return Q ? sg : sg * SGN + s; };
-    auto d0 = [&](int s) { return kDBlock * (Q ? SGN * b + s : b) + 8 * grp; };
+    auto st = [&](int s) { return RUN ? sg : sg * SGN + s; };
+    auto d0 = [&](int s) { return kDBlock * (RUN ? SGN * b + s : b) + 8 * grp; };
     auto dval = [&](int s) { return d0(s) < D; };    // D % 8 == 0: all 8 or none
-    constexpr int GHN = Q ? SGN : 1;                 // octets of gradHIn a lane holds
+    constexpr int GHN = RUN ? SGN : 1;                 // octets of gradHIn a lane holds
 
     // the workgroup's packed phi (its d-block, its streams) into LDS
-    if constexpr (Q) {
+    if constexpr (RUN) {
         constexpr int PER = C::PACK_U / SGN;
         for (int u = tid; u < C::PACK_U; u += kThreads) {
             const int db = SGN * b + u / PER < nblk ? SGN * b + u / PER : nblk - 1;   // past D: any
@@ -527,7 +529,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         // branch (a load under a branch leaves the compiler no exact wait count)
         const rsrc_t rhp = make_rsrc(a.h_pre + t0 * N, (int64_t)ntile * N * 4);
         const rsrc_t rc3 = make_rsrc(a.c3 + t0, (int64_t)ntile * 4);
-        if constexpr (Q) {
+        if constexpr (RUN) {
             const float v = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rhp, (row * N + sg) * 4, 0, 0));
 #pragma unroll
             for (int s = 0; s < SGN; ++s) hp[s] = v;
@@ -591,7 +593,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 for (int hl = 0; hl < 2; ++hl) {
                     const int e = 2 * e2 + hl;
                     const float xe = hl ? x16_hi<H>(xc[e2]) : x16_lo<H>(xc[e2]);
-                    const float ge = hl ? x16_hi<H>(ghc[Q ? s : 0][e2]) : x16_lo<H>(ghc[Q ? s : 0][e2]);
+                    const float ge = hl ? x16_hi<H>(ghc[RUN ? s : 0][e2]) : x16_lo<H>(ghc[RUN ? s : 0][e2]);
                     v[hl] = fmaf(ge, hp[s], GAMMA ? xg[e] * gam[GAMMA ? s : 0][e] : xg[e]);
                     v[hl] = fmaf(-c3, xe, v[hl]);
                     if constexpr (XPOST) v[hl] += hl ? x16_hi<H>(xp[s][e2]) : x16_lo<H>(xp[s][e2]);
@@ -599,7 +601,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
                 }
                 o[e2] = pack_x16<H>(v[0], v[1]);
             }
-            if constexpr (Q) {
+            if constexpr (RUN) {
                 *reinterpret_cast<u32x4*>(rows + j * C::XROW + 16 * ((4 * s + grp) ^ (j % (4 * SGN)))) = o;
             } else {
                 const uint32_t off = dval(s) ? (uint32_t)(((int64_t)row * K + (int64_t)st(s) * D + d0(s)) * 2) : kOutOfRange;
@@ -608,7 +610,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
             // x of this tile for the gradPhi phase
             *reinterpret_cast<u32x4*>(xT + row * C::XROW + 16 * ((4 * s + grp) ^ C::xswz(row))) = xc;
         }
-        if constexpr (Q) {   // gradX leaves in whole runs: 4 SGN lanes a token (the wave's own rows: no barrier)
+        if constexpr (RUN) {   // gradX leaves in whole runs: 4 SGN lanes a token (the wave's own rows: no barrier)
             constexpr int LPR = 4 * SGN, RPI = 64 / LPR;
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -693,7 +695,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         const int bi = wave + 4 * q;
         const int rb = bi / CB, cb = bi % CB;
         const int col = 16 * cb + j;                 // local column
-        const int s = col / kDBlock, dd = kDBlock * (Q ? SGN * b + s : b) + col % kDBlock;
+        const int s = col / kDBlock, dd = kDBlock * (RUN ? SGN * b + s : b) + col % kDBlock;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int m = 16 * rb + 4 * grp + r;
@@ -711,7 +713,7 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
         for (int col = tid; col < NCOL; col += kThreads) {
             float v = 0.f;
             for (int rr = 0; rr < kTile; ++rr) v += red[rr * NCOL + col];
-            const int s = col / kDBlock, dd = kDBlock * (Q ? SGN * b + s : b) + col % kDBlock;
+            const int s = col / kDBlock, dd = kDBlock * (RUN ? SGN * b + s : b) + col % kDBlock;
             if (dd < D) a.pgam[g * K + (int64_t)st(s) * D + dd] = v;
         }
     }
@@ -790,13 +792,22 @@ bwd_zero_kernel(Args a, int64_t MK, int64_t K, int M)
     if (idx < M) a.grad_bias[idx] = 0.f;
 }
 
+template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q, bool RUN>
+void launch_run(const Plan& p, const Args& a, hipStream_t st)
+{
+    const int64_t tasks = RUN ? run_tasks_for(p.G, p.g.nblk, SGN, N) : p.main_tasks;
+    const int64_t blocks = RUN ? run_blocks_for(tasks, N) : p.main_blocks;
+    hipLaunchKernelGGL((bwd_main_kernel<N, SGN, KS, GAMMA, XPOST, H, Q, RUN>), dim3((unsigned)blocks),
+                       dim3(kThreads), 0, st, a, p.T, p.g.D, p.g.nblk, p.tpg, p.tiles, tasks);
+}
+
 template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
 void launch_main(const Plan& p, const Args& a, hipStream_t st)
 {
-    const int64_t tasks = Q ? run_tasks_for(p.G, p.g.nblk, SGN, N) : p.main_tasks;
-    const int64_t blocks = Q ? run_blocks_for(tasks, N) : p.main_blocks;
-    hipLaunchKernelGGL((bwd_main_kernel<N, SGN, KS, GAMMA, XPOST, H, Q>), dim3((unsigned)blocks),
-                       dim3(kThreads), 0, st, a, p.T, p.g.D, p.g.nblk, p.tpg, p.tiles, tasks);
+    // 16-bit x by the run where the rows hold one and x is far larger than the caches: measured 5 to
+    // 16 % faster there (n = 4, 6, 8), and up to 5 % slower at T = 2048, D = 1024
+    if (Q || (p.g.D >= kDBlock * SGN && p.T * p.g.K >= (int64_t)1 << 25)) launch_run<N, SGN, KS, GAMMA, XPOST, H, Q, true>(p, a, st);
+    else launch_run<N, SGN, KS, GAMMA, XPOST, H, Q, Q>(p, a, st);
 }
 
 template <int N, int SGN, int KS, bool H, bool Q>

@@ -111,7 +111,8 @@ MHC_BWD_HOST_DEVICE inline bool main_task(int64_t blk, int nblk, int NSG, int64_
     return true;
 }
 
-// The same for x from its checkpoint: a task is (token group, run of SGN d-blocks, stream).
+// The same by runs (x from its checkpoint, and large 16-bit x): a task is (token group, run of
+// SGN d-blocks, stream).
 // The n streams of a run share gradHIn and gMix, and their tasks go to workgroups b, b + 8, ..
 // of one XCD.
 MHC_BWD_HOST_DEVICE inline int64_t run_tasks_for(int64_t G, int nblk, int SGN, int n) { return G * ((nblk + SGN - 1) / SGN) * n; }
