@@ -470,9 +470,12 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     // gradPhi phase. Rows past the tile and positions past D read as zero.
     const int row = 16 * wave + j;                   // the lane's token in a tile
     // DB: x and gradHIn are loaded a whole tile ahead, into the other of two register sets
-    // (where the registers allow it: no gamma, and not fp16 with gradXPost); the rest of a
-    // tile's inputs after its predecessor's first phase, as with a single set
-    constexpr bool DB = !GAMMA && !(XPOST && H);
+    // where the registers allow it; the rest of a tile's inputs after its predecessor's first
+    // phase, as with a single set. Without gamma that is always but for fp16 with gradXPost at
+    // three workgroups a compute unit; gamma's own 16 SGN registers leave room at two streams
+    // (n = 6, D = 4096, T = 8192: 526 -> 493 us a call; n = 8, D = 2048, T = 16384: 795 -> 720; 0 to 5 %
+    // at T = 2048, D = 1024), not at four (spills: 40 % slower).
+    constexpr bool DB = GAMMA ? SGN == 2 : RUN || !(XPOST && H);
     // the address unit is what bounds this kernel (some 65 cycles an instruction, 16 rows
     // each), so small values come several to a load: a token's hPre of all SGN streams, and its
     // blocks' scale bytes, which lane (j, s) loads for block s and hands to the others
