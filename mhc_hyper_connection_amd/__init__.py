@@ -385,9 +385,6 @@ class PreBackward:
         return out
 
 
-_BWD_RUNNERS: dict = {}
-
-
 def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms, h_mix, h_pre,
                      h_post, gamma=None, grad_x_post=None, *, hc_eps=1e-6, num_iters=0,
                      sum_out=None, norm_out=None):
@@ -395,8 +392,8 @@ def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms,
     the forward's sum_out [2it, ..., n] and norm_out [2it, ..., n, n]). x: bf16 or fp16
     [T, n, D] or [B, S, n, D] (grad_h_in, grad_x_post and the returned grad_x in the same
     format); the other per-token tensors follow x's leading dimensions. x may also be the
-    Checkpoint of that tensor: bit for bit the gradients of the restored x, in a workspace of
-    the call's own (calls on several streams, or captured ones, then share nothing). Returns
+    Checkpoint of that tensor: bit for bit the gradients of the restored x. The workspace is the
+    call's own: calls on several streams, or captured ones, share nothing. Returns
     dict grad_x, grad_phi, grad_alpha, grad_bias (and grad_gamma when gamma is given)."""
     ck = x if isinstance(x, Checkpoint) else None
     xt = x if ck is None else ck.codes
@@ -410,15 +407,11 @@ def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms,
         if D % 8:
             raise ValueError(f"x: D = {D}, expected a multiple of 8")
         _check_checkpoint(ck, "x", ck.dtype, tuple(xt.shape), xt.device)
-        r = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters, x_f16=f16, device=xt.device)
         x2 = Checkpoint(ck.codes.reshape(T, n, D), ck.scales.reshape(T, n, -(-D // CHECKPOINT_BLOCK)), ck.dtype)
     else:
-        key = (T, n, D, hc_eps, num_iters, f16, str(x.device))
-        r = _BWD_RUNNERS.get(key)
-        if r is None:
-            r = _BWD_RUNNERS[key] = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters,
-                                                x_f16=f16, device=x.device)
         x2 = x.reshape(T, n, D)
+    # a workspace for this call alone: it returns to torch's allocator, which orders its next use behind this stream
+    r = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters, x_f16=f16, device=xt.device)
     M = n * n + 2 * n
     rs = lambda t, *shape: None if t is None else t.reshape(*shape)
     out = r(x2, phi, alpha, rs(grad_h_in, T, D), rs(grad_h_post, T, n),
