@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import math
-from collections import namedtuple
+from collections import OrderedDict, namedtuple
 
 from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        MHC_ERR_RUNTIME, MHC_OK, STAGES, MhcError, Params, bwd_workspace_size,
@@ -244,16 +244,32 @@ class PreForward:
         return out
 
 
-_RUNNERS: dict = {}
+_RUNNERS: OrderedDict = OrderedDict()   # mhc_pre's launchers, the last used at the end
+_MAX_RUNNERS = 64
+
+
+def _capturing(device):
+    return device.type == "cuda" and _torch().cuda.is_current_stream_capturing()
 
 
 def _runner(T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, device, x_f16=False):
-    key = (T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, str(device), x_f16)
+    """The launcher of a size on the current stream: calls on one stream are ordered and share
+    its workspace, calls on different streams share none. A captured call has one of its own,
+    which the graph fills with zeros at each replay: the graph may be replayed on any stream."""
+    make = lambda: PreForward(T, n, D, n_alpha, num_iters=num_iters, norm_eps=norm_eps, hc_eps=hc_eps,
+                              need_backward=need_backward, device=device, x_f16=x_f16)
+    if _capturing(device):
+        return make()
+    stream = _stream(device) if device.type == "cuda" else None
+    key = (T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, str(device), x_f16,
+           stream.value if stream else 0)
     r = _RUNNERS.get(key)
     if r is None:
-        r = PreForward(T, n, D, n_alpha, num_iters=num_iters, norm_eps=norm_eps, hc_eps=hc_eps,
-                       need_backward=need_backward, device=device, x_f16=x_f16)
-        _RUNNERS[key] = r
+        r = _RUNNERS[key] = make()
+        if len(_RUNNERS) > _MAX_RUNNERS:
+            _RUNNERS.popitem(last=False)
+    else:
+        _RUNNERS.move_to_end(key)
     return r
 
 

@@ -78,3 +78,61 @@ def test_graphs_beside_eager_calls():
             eager = pre_backward(layers[2], grads[2])
         torch.cuda.synchronize()
         assert all(same(o, w) for o, w in zip((*outs, eager), want)), rep
+
+
+def forward_inputs(T, D, seed):
+    import synth
+    from gpu_helpers import to_dev
+    inp = synth.custom(T, 4, D, need_backward=True, seed=seed)
+    return [to_dev(a, device()) for a in (inp.x, inp.phi, inp.alpha, inp.bias)]
+
+
+def forward(args):
+    import mhc_hyper_connection_amd as mhc
+    h_in, h_post, h_res, extras = mhc.mhc_pre(*args, need_backward=True)
+    return {"h_in": h_in, "h_post": h_post, "h_res": h_res, **extras}
+
+
+@pytest.mark.parametrize("T,D", [(1400, 264), (4096, 1024)])
+def test_forward_on_streams(T, D):
+    # sizes of the classic and the streaming path: workgroups that do not wait on each other
+    import torch
+    print(f"[case] forward on streams T={T} D={D}", file=sys.stderr, flush=True)
+    args = [forward_inputs(T, D, seed) for seed in (1, 2, 3)]
+    want = [bits(forward(a)) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(device()) for _ in args]
+    for _ in range(3):
+        got = []
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                got.append(forward(a))
+        torch.cuda.synchronize()
+        assert all(same(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("T,D", [(60, 1056), (1300, 264), (4100, 1024)])
+def test_forward_first_called_under_capture(T, D):
+    # of sizes that no call had before: the captured calls' workspaces serve them alone
+    import torch
+    print(f"[case] forward under capture T={T} D={D}", file=sys.stderr, flush=True)
+    args = [forward_inputs(T, D, seed) for seed in (1, 2)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a in args:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(forward(a))
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    want = [bits(forward(a)) for a in args]
+    for rep in range(4):
+        for o in outs:
+            for v in o.values():
+                v.view(torch.uint8).fill_(0x7F)
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        eager = [forward(a) for a in args]
+        torch.cuda.synchronize()
+        assert all(same(o, w) for o, w in zip(outs + eager, want + want)), rep

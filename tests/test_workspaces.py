@@ -1,5 +1,8 @@
 """The workspaces of calls that may run at the same time, on the host: the library call is replaced by one that notes its
 arguments, so nothing is launched."""
+import contextlib
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -30,7 +33,6 @@ def test_backward_calls_in_flight_share_no_workspace(monkeypatch, checkpoint):
             mhc.mhc_pre_backward(*backward_inputs(checkpoint))
         return mhc.MHC_OK
 
-    import contextlib
     monkeypatch.setattr(mhc, "raw_backward", launch)
     monkeypatch.setattr(mhc, "raw_backward_checkpoint", launch)
     monkeypatch.setattr(mhc, "_stream", lambda device: None)
@@ -41,3 +43,58 @@ def test_backward_calls_in_flight_share_no_workspace(monkeypatch, checkpoint):
         assert size > 0 and a % 64 == 0
         for b, other in seen[:i]:
             assert a + size <= b or b + other <= a, "two calls in flight write to one workspace"
+
+
+@pytest.fixture
+def forward(monkeypatch):
+    """mhc_pre on tensors of a size, on a stream of that handle or under capture: the workspace it took."""
+    where = {"stream": None, "capturing": False}
+    seen = []
+
+    class Device:           # a GPU's name over host memory
+        type, index = "cuda", None
+        __str__ = lambda self: "cuda:0"
+
+    def make(*a, device, **k):
+        return real(*a, device="cpu", **k)
+
+    def launch(params, ptrs, ws, ws_bytes, stream):
+        seen.append((ws, ws_bytes))
+        return mhc.MHC_OK
+
+    real = mhc.PreForward
+    monkeypatch.setattr(mhc, "PreForward", make)
+    monkeypatch.setattr(mhc, "raw_forward", launch)
+    monkeypatch.setattr(mhc, "_stream", lambda device: where["stream"])
+    monkeypatch.setattr(mhc, "_capturing", lambda device: where["capturing"], raising=False)
+    monkeypatch.setattr(mhc, "_RUNNERS", type(mhc._RUNNERS)())
+    keep = []
+
+    def call(tokens, stream, capturing=False):
+        where.update(stream=ctypes.c_void_p(stream) if stream else None, capturing=capturing)
+        r = mhc._runner(tokens, N, D, 3, 20, 1e-6, 1e-6, False, Device())
+        keep.append(r)
+        z = torch.zeros
+        r(z((tokens, N, D), dtype=torch.bfloat16), z((M, N * D)), z(3), z(M))
+        return seen[-1]
+
+    return call
+
+
+def test_forward_calls_on_different_streams_share_no_workspace(forward):
+    first, second, default = forward(T, 16), forward(T, 32), forward(T, 0)
+    assert len({first, second, default}) == 3
+    assert forward(T, 16) == first and forward(T, 32) == second and forward(T, 0) == default
+
+
+def test_captured_forward_calls_have_workspaces_of_their_own(forward):
+    eager = forward(T, 16)
+    a, b = forward(T, 16, capturing=True), forward(T, 16, capturing=True)
+    assert len({eager, a, b}) == 3
+    assert forward(T, 16) == eager          # and nothing of a capture serves a later eager call
+
+
+def test_forward_keeps_few_launchers(forward):
+    for tokens in range(1, 2 * mhc._MAX_RUNNERS):
+        forward(tokens, 0)
+    assert len(mhc._RUNNERS) <= mhc._MAX_RUNNERS
