@@ -499,7 +499,9 @@ mhc_status mhc_checkpoint_restore(const mhc_checkpoint_params* params, const int
 
 /* mhc_post, bit for bit, and the checkpoint of its out (codes int8 [T, n, D], 16-byte
  * aligned; scales uint8 [T, n, ceil(D / 32)]) written from the same registers: what
- * mhc_checkpoint of out gives, without reading out again. Rules and errors as mhc_post's. */
+ * mhc_checkpoint of out gives, without reading out again. Rules and errors as mhc_post's,
+ * and PARAM_INVALID where a stream's T rows hold more than 2^32 - 256 octets, each row counted
+ * with its last block whole (T = 2^30 - 64 is the most at D = 8). */
 mhc_status mhc_post_checkpoint(const mhc_post_params* params, const mhc_post_tensors* tensors, int8_t* codes,
                                uint8_t* scales, void* stream);
 
@@ -522,8 +524,9 @@ mhc_status mhc_pre_backward_checkpoint(const mhc_pre_bwd_params* params, const m
  *   grad_comb[t][i][j]     = sum_d residual[t][i][d] grad_out[t][j][d]
  * fp32 fused multiply-adds and sums in a fixed order (results are bitwise reproducible),
  * one rounding to the 16-bit format. grad_residual is what mhc_pre_backward takes as
- * grad_x_post, grad_post and grad_comb what it takes as grad_h_post and grad_h_res. x and residual, each by itself, come as 16-bit tensors or as
- * 8-bit checkpoints (the pointers of the other form NULL).
+ * grad_x_post, grad_post and grad_comb what it takes as grad_h_post and grad_h_res. x and
+ * residual, each by itself, come as 16-bit tensors or as 8-bit checkpoints (the pointers of
+ * the other form NULL).
  *   params as for mhc_post
  *   grad_out x_dtype [T, n, D]  16-byte aligned
  *   x        x_dtype [T, D]     16-byte aligned, or x_codes [T, D] (16-byte aligned) and
@@ -536,7 +539,8 @@ mhc_status mhc_pre_backward_checkpoint(const mhc_pre_bwd_params* params, const m
  *   each other
  * Pointers may be NULL only when T == 0 (nothing is launched). Asynchronous on `stream`, no
  * workspace, no allocation. Errors: NULLPTR (neither form of x or of residual given, or a
- * checkpoint without its scales), PARAM_INVALID (both forms given), RUNTIME. */
+ * checkpoint without its scales), PARAM_INVALID (both forms given, or more tokens than
+ * mhc_post_checkpoint takes), RUNTIME. */
 typedef struct mhc_post_bwd_tensors {
     const uint16_t* grad_out;
     const uint16_t* x;

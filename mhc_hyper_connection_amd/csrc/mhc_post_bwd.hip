@@ -30,7 +30,6 @@ namespace mhc {
 namespace {
 
 constexpr int kThr = 256;
-constexpr int64_t kFewTokens = 512;
 
 // An octet of 16-bit values, or of codes with their step.
 template <bool H, bool Q> struct Octet;
@@ -170,15 +169,22 @@ post_bwd_kernel(PostBwdArgs a, int64_t T, int D, int NB, int W)
 }
 
 template <int N, bool H>
-void launch(int64_t T, int D, const PostBwdArgs& a, hipStream_t st)
+hipError_t launch(int64_t T, int D, PostBwdArgs a, hipStream_t st)
 {
-    const int W = D >= 512 * N || T < kFewTokens ? 4 : 1;
-    const dim3 grid((unsigned)(W == 1 ? (T + 3) / 4 : T));
-    const int NB = ckpt_blocks(D);
-    if (a.x && a.residual) hipLaunchKernelGGL((post_bwd_kernel<N, H, false, false>), grid, dim3(kThr), 0, st, a, T, D, NB, W);
-    else if (a.residual) hipLaunchKernelGGL((post_bwd_kernel<N, H, true, false>), grid, dim3(kThr), 0, st, a, T, D, NB, W);
-    else if (a.x) hipLaunchKernelGGL((post_bwd_kernel<N, H, false, true>), grid, dim3(kThr), 0, st, a, T, D, NB, W);
-    else hipLaunchKernelGGL((post_bwd_kernel<N, H, true, true>), grid, dim3(kThr), 0, st, a, T, D, NB, W);
+    const int W = post_bwd_waves(T, N, D), NB = ckpt_blocks(D);
+    const int64_t most = post_bwd_launch_tokens(W);
+    for (; T > 0; T -= most) {
+        const int64_t Tc = T < most ? T : most;
+        const dim3 grid((unsigned)post_bwd_blocks(Tc, W));
+        if (a.x && a.residual) hipLaunchKernelGGL((post_bwd_kernel<N, H, false, false>), grid, dim3(kThr), 0, st, a, Tc, D, NB, W);
+        else if (a.residual) hipLaunchKernelGGL((post_bwd_kernel<N, H, true, false>), grid, dim3(kThr), 0, st, a, Tc, D, NB, W);
+        else if (a.x) hipLaunchKernelGGL((post_bwd_kernel<N, H, false, true>), grid, dim3(kThr), 0, st, a, Tc, D, NB, W);
+        else hipLaunchKernelGGL((post_bwd_kernel<N, H, true, true>), grid, dim3(kThr), 0, st, a, Tc, D, NB, W);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        if (T > most) a = post_bwd_after(a, Tc, N, D);
+    }
+    return hipSuccess;
 }
 
 }  // namespace
@@ -187,11 +193,10 @@ int launch_post_backward(int64_t T, int n, int D, const PostBwdArgs& a, int x_f1
 {
     clear_pending_error();
     hipStream_t st = (hipStream_t)stream;
-    if (n == 4) x_f16 ? launch<4, true>(T, D, a, st) : launch<4, false>(T, D, a, st);
-    else if (n == 6) x_f16 ? launch<6, true>(T, D, a, st) : launch<6, false>(T, D, a, st);
-    else if (n == 8) x_f16 ? launch<8, true>(T, D, a, st) : launch<8, false>(T, D, a, st);
-    else return (int)hipErrorInvalidValue;
-    return (int)hipGetLastError();
+    if (n == 4) return (int)(x_f16 ? launch<4, true>(T, D, a, st) : launch<4, false>(T, D, a, st));
+    if (n == 6) return (int)(x_f16 ? launch<6, true>(T, D, a, st) : launch<6, false>(T, D, a, st));
+    if (n == 8) return (int)(x_f16 ? launch<8, true>(T, D, a, st) : launch<8, false>(T, D, a, st));
+    return (int)hipErrorInvalidValue;
 }
 
 }  // namespace mhc

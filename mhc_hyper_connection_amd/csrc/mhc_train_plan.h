@@ -26,6 +26,14 @@ inline int64_t octet_blocks(int64_t rows, int D)
     return (rows * P + 255) / 256;
 }
 
+// hc_post's backward: waves per token (4 or 1; mhc_post_bwd.hip has the rule's measurements),
+// and the tokens of one launch, whose workgroups of 256 threads (a token, or four of one wave
+// each) stay within a grid's 2^32 - 1 threads. More tokens go in several launches.
+constexpr int64_t kPostBwdFewTokens = 512;
+inline int post_bwd_waves(int64_t T, int n, int D) { return D >= 512 * n || T < kPostBwdFewTokens ? 4 : 1; }
+inline int64_t post_bwd_launch_tokens(int waves) { return (int64_t)0xffffff * (4 / waves); }
+inline int64_t post_bwd_blocks(int64_t tokens, int waves) { return waves == 1 ? (tokens + 3) / 4 : tokens; }
+
 struct PostBwdArgs {
     const uint16_t* grad_out;      // [T, n, D]
     const uint16_t* x;             // [T, D], or NULL: x_codes, x_scales
@@ -41,6 +49,30 @@ struct PostBwdArgs {
     float* grad_post;              // [T, n]
     float* grad_comb;              // [T, n, n]
 };
+
+// The arguments of the tokens behind the first t.
+inline PostBwdArgs post_bwd_after(PostBwdArgs a, int64_t t, int n, int D)
+{
+    const int64_t row = t * D, rows = row * n, nb = t * ckpt_blocks(D);
+    a.grad_out += rows;
+    if (a.x) a.x += row;
+    else {
+        a.x_codes += row;
+        a.x_scales += nb;
+    }
+    if (a.residual) a.residual += rows;
+    else {
+        a.r_codes += rows;
+        a.r_scales += nb * n;
+    }
+    a.post += t * n;
+    a.comb += t * n * n;
+    a.grad_x += row;
+    a.grad_residual += rows;
+    a.grad_post += t * n;
+    a.grad_comb += t * n * n;
+    return a;
+}
 
 // Implemented in mhc_ckpt.hip and mhc_post_bwd.hip. Each returns 0 or the HIP error code.
 int launch_checkpoint(int64_t rows, int D, const uint16_t* x, int8_t* codes, uint8_t* scales, int x_f16, void* stream);
