@@ -296,7 +296,7 @@ mhc_status mhc_pre_forward_timed(const mhc_pre_params* params, const mhc_pre_ten
  * P = norm_out[0] - hcEps. That logit gradient takes gradHRes's place above.
  *
  * Problem description (host memory):
- *   T          tokens, >= 0
+ *   T          tokens, 0 .. 67108860 (a wave of 64 threads each, in one grid)
  *   n          4, 6 or 8;  D  a multiple of 8 in [8, 16384]
  *   hc_eps     >= 0: the hcEps the forward used (hPre = sigmoid(...) + hcEps)
  *   num_iters  0: MhcPre backward (affine hRes); 1 .. 1000: MhcPreSinkhorn backward with

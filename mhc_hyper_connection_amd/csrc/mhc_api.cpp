@@ -235,7 +235,7 @@ mhc_status check_bwd_params(const mhc_pre_bwd_params* p, mhc::bwd::Geometry* g)
     if (p->x_f16 != 0 && p->x_f16 != 1) return MHC_ERR_PARAM_INVALID;
     if (p->num_iters < 0 || p->num_iters > 1000) return MHC_ERR_PARAM_INVALID;
     if (!(p->hc_eps >= 0.0)) return MHC_ERR_PARAM_INVALID;    // also rejects NaN
-    if (p->T < 0) return MHC_ERR_PARAM_INVALID;
+    if (p->T < 0 || p->T > mhc::bwd::kMaxT) return MHC_ERR_PARAM_INVALID;
     if (!mhc::bwd::make_geometry(p->n, p->D, g, p->x_f16 == 1)) return MHC_ERR_PARAM_INVALID;
     return MHC_OK;
 }

@@ -41,6 +41,7 @@ constexpr int kTile = 64;            // tokens per tile (4 waves x 16)
 constexpr int kDBlock = 32;          // positions per d-block
 constexpr int kMaxD = 16384;
 constexpr int kTargetBlocks = 2048;  // main-pass workgroups aimed for (token groups x blocks)
+constexpr int64_t kMaxT = 4 * (int64_t)0xffffff;   // one wave a token: a grid's 2^32 - 1 threads
 
 struct Geometry {
     int n = 0;
