@@ -145,3 +145,18 @@ def test_results_from_the_dg_and_du_that_are_held(T, D, F, f16, act, grad, kept)
     product("grad_x", ((dg, wg), (du, wu)), 2 * F)
     product("grad_w_gate", ((dg.t(), x),), T)
     product("grad_w_up", ((du.t(), x),), T)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("f16", [False, True])
+@pytest.mark.parametrize("T,D,F", [(1, 264, 1000), (16, 512, 136), (17, 96, 2048), (32, 72, 4104), (33, 2056, 264), (64, 128, 1032), (65, 72, 40), (300, 2048, 544),
+                                   (1003, 2048, 5464)])
+def test_h_again_is_the_forwards_h(T, D, F, f16, act):
+    # one kernel computes h in both directions, for few tokens as for many: the same bits
+    import mhc_hyper_connection_amd as mhc
+    import torch
+    print(f"[case] glu h again T={T} D={D} F={F} f16={f16} {act}", file=sys.stderr, flush=True)
+    d = random_inputs(T, D, F, torch_dtype(f16), seed=T, grad=1.0)
+    h = mhc.mhc_glu(d["x"], d["w_gate"], d["w_up"], act=act)
+    got = mhc.mhc_glu_backward(d["grad_h"], d["x"], d["w_gate"], d["w_up"], act=act, need_h=True)
+    assert torch.equal(got["h"].view(torch.int16), h.view(torch.int16))
