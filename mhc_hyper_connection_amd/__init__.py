@@ -622,7 +622,10 @@ def mhc_glu_backward(grad_h, x, w_gate, w_up, *, act="silu", need_h=False, out=N
     projections are computed again. grad_h [..., F] in x's dtype. Returns (or fills) dict
     grad_x [..., D], grad_w_gate and grad_w_up [F, D] (overwritten), all in x's dtype, and
     with need_h also h [..., F], which the gradient of the projection behind it needs. The
-    workspace is the call's own."""
+    gradients of the two projections' results, from which these are made, are held in x's
+    dtype: in fp16 keep the loss scale so that grad_h times the activation stays within
+    65504 and, for what matters, above 6e-5 (include/mhc.h has the rounding and the range).
+    The workspace is the call's own."""
     torch = _torch()
     xdt = _x_dtype(grad_h, "grad_h")
     ck = x if isinstance(x, Checkpoint) else None

@@ -107,8 +107,11 @@ def half(ref, f16):
     return (eps * ref.abs()).clamp(min=least)
 
 
-CASES = [(1003, 2048, 5464, True, "gelu_tanh", 1.0, True), (1030, 2560, 4104, False, "gelu_tanh", 1.0, True), (4099, 1032, 2056, True, "silu", 1.0, False),
-         (513, 4104, 1032, False, "silu", 1.0, True), (300, 2048, 544, True, "silu", 1.0, True), (20, 2048, 544, True, "gelu_tanh", 1.0, False)]
+CASES = [(1003, 2048, 5464, True, "gelu_tanh", 1.0, True), (1003, 2048, 5464, True, "silu", 1e-4, False), (1003, 2048, 5464, True, "silu", 1e3, True),
+         (1030, 2560, 4104, False, "gelu_tanh", 1.0, True), (4099, 1032, 2056, True, "gelu_tanh", 1e-4, False), (513, 4104, 1032, False, "silu", 1e-4, True),
+         (300, 2048, 544, True, "silu", 1e-4, True), (20, 2048, 544, True, "gelu_tanh", 1e-4, False), (20, 2048, 544, True, "silu", 1e3, False),
+         (4099, 1032, 2056, True, "silu", 1.0, False), (513, 4104, 1032, False, "silu", 1.0, True), (300, 2048, 544, True, "silu", 1.0, True),
+         (20, 2048, 544, True, "gelu_tanh", 1.0, False)]
 
 
 @pytest.mark.parametrize("T,D,F,f16,act,grad,kept", CASES)
@@ -160,3 +163,24 @@ def test_h_again_is_the_forwards_h(T, D, F, f16, act):
     h = mhc.mhc_glu(d["x"], d["w_gate"], d["w_up"], act=act)
     got = mhc.mhc_glu_backward(d["grad_h"], d["x"], d["w_gate"], d["w_up"], act=act, need_h=True)
     assert torch.equal(got["h"].view(torch.int16), h.view(torch.int16))
+
+
+@pytest.mark.parametrize("T,D,F", [(20, 264, 136), (300, 264, 136), (1003, 2048, 5464)])
+def test_fp16_range_of_dg_and_du(T, D, F):
+    # dg and du are fp16 tensors. A grad_h of 60000 leaves their range wherever act(g) or u act'(g) passes 1.1, as it does for some f
+    # of any token here: that token's grad_x is not finite, and no other token's changes. The same gradients 2^-14
+    # times the size (a smaller loss scale) are in range.
+    import mhc_hyper_connection_amd as mhc
+    import torch
+    print(f"[case] glu fp16 range T={T} D={D} F={F}", file=sys.stderr, flush=True)
+    d = random_inputs(T, D, F, torch.float16, seed=7, grad=1.0)
+    t = T // 2
+    keep = [k for k in range(T) if k != t]
+    base = mhc.mhc_glu_backward(d["grad_h"], d["x"], d["w_gate"], d["w_up"])
+    d["grad_h"][t] = 60000.0
+    big = mhc.mhc_glu_backward(d["grad_h"], d["x"], d["w_gate"], d["w_up"])
+    assert torch.equal(big["grad_x"][keep], base["grad_x"][keep])
+    assert not torch.isfinite(big["grad_x"][t]).all()
+    d["grad_h"][t] *= 2.0 ** -14
+    small = mhc.mhc_glu_backward(d["grad_h"], d["x"], d["w_gate"], d["w_up"])
+    assert all(torch.isfinite(v).all() for v in small.values())
