@@ -467,11 +467,12 @@ mhc_status mhc_post(const mhc_post_params* params, const mhc_post_tensors* tenso
  * Activations kept from the forward to the backward pass in 8 bits: the n streams are the
  * largest tensors that an mHC layer keeps, n times a plain residual network's. A row of D
  * values is cut into blocks of 32 along D (the last may be shorter). With a = the largest
- * magnitude in a block, its step is 2^e, e = floor(log2 a) - 6, but not below the least
- * value of the format (fp16: e >= -24; bf16: e >= -126); a value's code is its nearest
- * multiple of the step (ties to even) within +-127, as a signed byte; the block's scale
- * byte is e + 127. A value is off by at most half a step, a/128 (those above 127.5 steps by
- * less than a step), and code * step is exact in the 16-bit format it came from. A block
+ * magnitude in a block, its step is 2^e, e = floor(log2 a) - 6, but not below -24 for fp16
+ * (its least value) nor -126 for bf16 (its least normal value); a value's code is its
+ * nearest multiple of the step (ties to even) within +-127, as a signed byte; the block's
+ * scale byte is e + 127. A value is off by at most half a step (those above 127.5 steps by
+ * less than a step): in all by at most a/128, or 2^-127 where that is more, as in bf16
+ * blocks of a < 2^-120. code * step is exact in the 16-bit format it came from. A block
  * that holds a NaN or an infinity has the scale byte 255, and all its values come back
  * NaN. Scale bytes are 1 .. 248 and 255; a byte that the library did not write scales by
  * 2^(byte - 127) too (0 by zero), never out of bounds.

@@ -465,8 +465,8 @@ def mhc_post(x, residual, post, comb, *, out=None):
 def mhc_checkpoint(x, *, out=None):
     """x (bf16 or fp16 [..., D], D a multiple of 8) as its 8-bit Checkpoint: a signed byte per
     value and, per run of 32 values along D, a power of two (mhc_checkpoint in include/mhc.h
-    has the format: half a step of error, 1/128 of the run's largest magnitude at most; a run with a NaN
-    or an infinity comes back as NaN). out: a Checkpoint to fill. The stream is torch's
+    has the format: an error of 1/128 of the run's largest magnitude at most, or of 2^-127 where
+    that is more; a run with a NaN or an infinity comes back as NaN). out: a Checkpoint to fill. The stream is torch's
     current stream on x's device."""
     torch = _torch()
     xdt = _x_dtype(x, "x")

@@ -5,8 +5,9 @@
 // a = the largest magnitude in it, its step is 2^e, e = floor(log2 a) - 6 (at least -24 for
 // fp16, whose least value is 2^-24, and -126 for bf16, the least exponent of a normal
 // float), and a value's code is its nearest multiple of the step, ties to even, within
-// +-127. So a falls on 64 .. 127 steps, every value is off by half a step at most (those
-// above 127.5 steps by less than one), and code * step is exact in the 16-bit format the
+// +-127. So a falls on 64 .. 127 steps (on fewer at the least step), every value is off by
+// half a step at most (those above 127.5 steps by less than one): by a/128, or by 2^-127 where bf16's
+// least step makes that more; and code * step is exact in the 16-bit format the
 // value came from: at most 7 significant bits, no larger than a, no finer than the format's
 // least value (bf16: than 2^-126). The power of two makes the scaling exact in both
 // directions, so codes do not depend on how they are computed. The scale byte is e + 127;
