@@ -807,10 +807,10 @@ void launch_run(const Plan& p, const Args& a, hipStream_t st)
 template <int N, int SGN, int KS, bool GAMMA, bool XPOST, bool H, bool Q>
 void launch_main(const Plan& p, const Args& a, hipStream_t st)
 {
-    // 16-bit x by the run where the rows hold one and x is far larger than the caches: measured 5 to
-    // 16 % faster there (n = 4, 6, 8), and up to 5 % slower at T = 2048, D = 1024
-    if (Q || (p.g.D >= kDBlock * SGN && p.T * p.g.K >= (int64_t)1 << 25)) launch_run<N, SGN, KS, GAMMA, XPOST, H, Q, true>(p, a, st);
-    else launch_run<N, SGN, KS, GAMMA, XPOST, H, Q, Q>(p, a, st);
+    if constexpr (Q) launch_run<N, SGN, KS, GAMMA, XPOST, H, true, true>(p, a, st);
+    else if constexpr (N == 8 && !XPOST) launch_run<N, SGN, KS, GAMMA, XPOST, H, false, false>(p, a, st);   // never by runs (by_runs)
+    else if (by_runs(p.g, p.T, GAMMA, XPOST)) launch_run<N, SGN, KS, GAMMA, XPOST, H, false, true>(p, a, st);
+    else launch_run<N, SGN, KS, GAMMA, XPOST, H, false, false>(p, a, st);
 }
 
 template <int N, int SGN, int KS, bool H, bool Q>

@@ -112,10 +112,9 @@ MHC_BWD_HOST_DEVICE inline bool main_task(int64_t blk, int nblk, int NSG, int64_
     return true;
 }
 
-// The same by runs (x from its checkpoint, and large 16-bit x): a task is (token group, run of
-// SGN d-blocks, stream).
-// The n streams of a run share gradHIn and gMix, and their tasks go to workgroups b, b + 8, ..
-// of one XCD.
+// The same by runs (x from its checkpoint, and large 16-bit x: by_runs): a task is (token
+// group, run of SGN d-blocks, stream). The n streams of a run share gradHIn and gMix, and
+// their tasks go to workgroups b, b + 8, .. of one XCD.
 MHC_BWD_HOST_DEVICE inline int64_t run_tasks_for(int64_t G, int nblk, int SGN, int n) { return G * ((nblk + SGN - 1) / SGN) * n; }
 MHC_BWD_HOST_DEVICE inline int64_t run_blocks_for(int64_t tasks, int n) { return (tasks + 8 * n - 1) / (8 * n) * (8 * n); }
 MHC_BWD_HOST_DEVICE inline bool run_task(int64_t blk, int runs, int n, int64_t tasks, int64_t* grp, int* run, int* stream)
@@ -128,6 +127,33 @@ MHC_BWD_HOST_DEVICE inline bool run_task(int64_t blk, int runs, int n, int64_t t
     *run = (int)(gr % runs);
     *grp = gr / runs;
     return true;
+}
+
+// Whether 16-bit x goes by runs. A run stores gradX in whole rows of 256 (n = 4) or 128 bytes
+// instead of 64, which pays where x is far larger than the caches, and sooner where the rows
+// are no whole 128-byte lines, which 64-byte pieces then straddle; a last run that is partly
+// empty costs its share. Time by runs over time by d-blocks, the whole call, bf16 and fp16, at
+// 2^25 values of x, at 2^26 and at 2^28:
+//   n = 4  D = 1024, no gradXPost   1.01 - 1.10, 0.94 - 0.99, 0.90 - 0.91; with it 1.02 - 1.05, 0.90 - 0.96, 0.85 - 0.90
+//          D = 4104                 0.83 - 0.97, 0.85 - 0.93, 0.84 - 0.88; gamma and no gradXPost 0.99 - 1.02, 0.93 - 0.97, 0.90
+//          D = 192, 448 (whole lines; a quarter, an eighth of the runs empty)  1.08 - 1.18, 1.04 - 1.11, 1.02 - 1.10
+//   n = 6  D = 1024, no gradXPost   1.01 - 1.03, 1.00 - 1.01, 0.95 - 0.97; with it 0.97 - 1.02, 0.93 - 0.96, 0.90 - 0.93
+//          D = 520                  0.97 - 1.04, 0.93 - 0.99, 0.93 - 0.99 (2^27: 0.97 - 1.02)
+//   n = 8  D = 1024, no gradXPost   1.02 - 1.03, 1.01 - 1.02, 0.98 - 1.00; with it 0.94 - 1.06, 0.91 - 1.00, 0.91 - 0.97
+//          D = 520                  0.96 - 1.08, 0.93 - 1.01, 0.97 - 1.04
+// The lowest of each at n = 6 and 8 is fp16 with gradXPost and no gamma, where only the runs
+// have room for a second register set. fp16 splits x and gains from its size on a little later.
+inline bool by_runs(const Geometry& g, int64_t T, bool gamma, bool xpost)
+{
+    constexpr int64_t kMi = 1 << 20;
+    const int64_t values = T * g.K, most = (g.x_f16 ? 96 : 64) * kMi;
+    const bool lines = g.D % 64 == 0;
+    if (g.n == 4) {
+        if (lines) return g.D % 128 == 0 && values >= (xpost ? 48 * kMi : most);
+        return g.nblk >= 8 && values >= (gamma && !xpost ? most : 32 * kMi);
+    }
+    if (xpost && !gamma && g.x_f16) return g.nblk >= 8 && values >= 48 * kMi;
+    return lines && values >= 96 * kMi && (xpost || (g.n == 6 && g.D >= 1024));
 }
 
 struct Plan {
