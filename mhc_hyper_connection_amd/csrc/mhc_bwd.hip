@@ -19,8 +19,8 @@
 //   bwd_token_kernel    one wave per token: the hPre gradient in fp64, the gate backward,
 //                       gMix, c3 = gInv invRms^3 / (n D), and the token's alpha/bias terms
 //   bwd_main_kernel     one workgroup per (token group, d-block, stream group), or per (token
-//                       group, run of d-blocks, stream) for large x: per tile of 64 tokens, xrsGrad on the matrix cores (phi terms x gMix terms,
-//                       six products), gradX, the gradGamma sums, and gMix^T . x on the
+//                       group, run of d-blocks, stream) for large x: per tile of 64 tokens, xrsGrad on
+//                       the matrix cores (phi terms x gMix terms, six products), gradX, the gradGamma sums, and gMix^T . x on the
 //                       matrix cores, both transposed on their way out of LDS; group sums to
 //                       partials
 //   bwd_reduce_*        fixed-order fp64 sums of the partials (gradPhi, gradGamma) and
@@ -474,7 +474,11 @@ bwd_main_kernel(Args a, int64_t T, int D, int nblk, int64_t tpg, int64_t tiles, 
     // phase, as with a single set. Without gamma that is always but for fp16 with gradXPost at
     // three workgroups a compute unit; gamma's own 16 SGN registers leave room at two streams
     // (n = 6, D = 4096, T = 8192: 526 -> 493 us a call; n = 8, D = 2048, T = 16384: 795 -> 720; 0 to 5 %
-    // at T = 2048, D = 1024), not at four (spills: 40 % slower).
+    // at T = 2048, D = 1024; a group of one tile has nothing to load ahead: n = 6, D = 7168, T = 64 57 -> 61),
+    // not at four (spills: 40 % slower). One form just passes the 256 registers: n = 8 with gamma,
+    // gradXPost and fp16 x from its checkpoint spills three values that its loop over the tiles
+    // does not touch, and gains (T = 16384, D = 2048: 834 us with the second set, 878 without;
+    // T = 1003, D = 1000: 86 and 85).
     constexpr bool DB = GAMMA ? SGN == 2 : RUN || !(XPOST && H);
     // the address unit is what bounds this kernel (some 65 cycles an instruction, 16 rows
     // each), so small values come several to a load: a token's hPre of all SGN streams, and its
