@@ -13,8 +13,9 @@ the library's kernels, and nothing here falls back to another implementation.
 from __future__ import annotations
 
 import contextlib
+import functools
 import math
-from collections import OrderedDict, namedtuple
+from collections import namedtuple
 
 from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        MHC_ERR_RUNTIME, MHC_OK, STAGES, MhcError, Params, bwd_workspace_size,
@@ -43,14 +44,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(device):
+def _raw_stream(device):
     # torch's current stream on `device` as a raw handle (the direct getter: a fraction of
     # the cost of building a torch.cuda.Stream object on every call)
     torch = _torch()
     getter = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if getter is not None and device.index is not None:
-        return ctypes_void(getter(device.index))
-    return ctypes_void(torch.cuda.current_stream(device).cuda_stream)
+        return getter(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _stream(device):
+    return ctypes_void(_raw_stream(device))
 
 
 def ctypes_void(handle):
@@ -244,32 +249,31 @@ class PreForward:
         return out
 
 
-_RUNNERS: OrderedDict = OrderedDict()   # mhc_pre's launchers, the last used at the end
+_RUNNERS: dict = {}   # mhc_pre's launchers
 _MAX_RUNNERS = 64
 
 
 def _capturing(device):
-    return device.type == "cuda" and _torch().cuda.is_current_stream_capturing()
+    return device.type == "cuda" and _torch()._C._cuda_isCurrentStreamCapturing()
 
 
 def _runner(T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, device, x_f16=False):
     """The launcher of a size on the current stream: calls on one stream are ordered and share
     its workspace, calls on different streams share none. A captured call has one of its own,
     which the graph fills with zeros at each replay: the graph may be replayed on any stream."""
-    make = lambda: PreForward(T, n, D, n_alpha, num_iters=num_iters, norm_eps=norm_eps, hc_eps=hc_eps,
-                              need_backward=need_backward, device=device, x_f16=x_f16)
-    if _capturing(device):
-        return make()
-    stream = _stream(device) if device.type == "cuda" else None
-    key = (T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, str(device), x_f16,
-           stream.value if stream else 0)
-    r = _RUNNERS.get(key)
-    if r is None:
-        r = _RUNNERS[key] = make()
-        if len(_RUNNERS) > _MAX_RUNNERS:
-            _RUNNERS.popitem(last=False)
-    else:
-        _RUNNERS.move_to_end(key)
+    cached = not _capturing(device)
+    if cached:
+        key = (T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, device, x_f16,
+               _raw_stream(device) if device.type == "cuda" else 0)
+        r = _RUNNERS.get(key)
+        if r is not None:
+            return r
+    r = PreForward(T, n, D, n_alpha, num_iters=num_iters, norm_eps=norm_eps, hc_eps=hc_eps,
+                   need_backward=need_backward, device=device, x_f16=x_f16)
+    if cached:
+        _RUNNERS[key] = r
+        if len(_RUNNERS) > _MAX_RUNNERS:      # the oldest; its memory is freed in its stream's order
+            _RUNNERS.pop(next(iter(_RUNNERS)))
     return r
 
 
@@ -313,10 +317,11 @@ class PreBackward:
     """Launcher of the MhcPre backward for one problem size (MhcPreBackward guide,
     0539edu.com/news/4871844, section 3); with num_iters >= 1 the MhcPreSinkhorn backward
     (the forward's Sinkhorn planes are then inputs). x_f16: x, grad_h_in, grad_x_post
-    and grad_x in float16 (else bfloat16). Owns its workspace; calls through one
+    and grad_x in float16 (else bfloat16). Owns its workspace (by default): calls through one
     instance must not overlap."""
 
-    def __init__(self, T, n, D, *, hc_eps=1e-6, num_iters=0, x_f16=False, device="cuda"):
+    def __init__(self, T, n, D, *, hc_eps=1e-6, num_iters=0, x_f16=False, device="cuda", own_workspace=True):
+        """own_workspace=False: each call takes a workspace of its own instead (calls may then overlap)."""
         torch = _torch()
         load()
         self.T, self.n, self.D = int(T), int(n), int(D)
@@ -328,7 +333,12 @@ class PreBackward:
         self.x_f16 = bool(x_f16)
         self.params = make_bwd_params(T, n, D, hc_eps, num_iters, self.x_f16)
         self.ws_bytes = bwd_workspace_size(self.params)
-        self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+        self.workspace = self._new_workspace() if own_workspace else None
+
+    def _new_workspace(self):
+        # from torch's allocator, which orders the memory's next use behind the current stream
+        torch = _torch()
+        return torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
 
     def alloc_outputs(self, gamma=False):
         torch = _torch()
@@ -388,17 +398,24 @@ class PreBackward:
                 "sum_out": _ptr(sum_out) if it else None, "norm_out": _ptr(norm_out) if it else None}
         for k, v in out.items():
             ptrs[k] = _ptr(v)
+        ws = self.workspace if self.workspace is not None else self._new_workspace()
         if ck is not None:
             with _on_gpu(dev):
-                st = raw_backward_checkpoint(self.params, ptrs, _ptr(ck.codes), _ptr(ck.scales), _ptr(self.workspace),
+                st = raw_backward_checkpoint(self.params, ptrs, _ptr(ck.codes), _ptr(ck.scales), _ptr(ws),
                                              self.ws_bytes, _stream(dev))
             if st != MHC_OK:
                 raise MhcError(st, "mhc_pre_backward_checkpoint")
             return out
-        st = raw_backward(self.params, ptrs, _ptr(self.workspace), self.ws_bytes, _stream(dev))
+        st = raw_backward(self.params, ptrs, _ptr(ws), self.ws_bytes, _stream(dev))
         if st != MHC_OK:
             raise MhcError(st, "mhc_pre_backward")
         return out
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_runner(T, n, D, hc_eps, num_iters, x_f16, device):
+    # holds no device memory: each call has a workspace of its own
+    return PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters, x_f16=x_f16, device=device, own_workspace=False)
 
 
 def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms, h_mix, h_pre,
@@ -426,8 +443,7 @@ def mhc_pre_backward(x, phi, alpha, grad_h_in, grad_h_post, grad_h_res, inv_rms,
         x2 = Checkpoint(ck.codes.reshape(T, n, D), ck.scales.reshape(T, n, -(-D // CHECKPOINT_BLOCK)), ck.dtype)
     else:
         x2 = x.reshape(T, n, D)
-    # a workspace for this call alone: it returns to torch's allocator, which orders its next use behind this stream
-    r = PreBackward(T, n, D, hc_eps=hc_eps, num_iters=num_iters, x_f16=f16, device=xt.device)
+    r = _backward_runner(T, n, D, hc_eps, num_iters, f16, xt.device)
     M = n * n + 2 * n
     rs = lambda t, *shape: None if t is None else t.reshape(*shape)
     out = r(x2, phi, alpha, rs(grad_h_in, T, D), rs(grad_h_post, T, n),

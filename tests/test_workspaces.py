@@ -1,7 +1,6 @@
 """The workspaces of calls that may run at the same time, on the host: the library call is replaced by one that notes its
 arguments, so nothing is launched."""
 import contextlib
-import ctypes
 
 import pytest
 
@@ -48,12 +47,13 @@ def test_backward_calls_in_flight_share_no_workspace(monkeypatch, checkpoint):
 @pytest.fixture
 def forward(monkeypatch):
     """mhc_pre on tensors of a size, on a stream of that handle or under capture: the workspace it took."""
-    where = {"stream": None, "capturing": False}
+    where = {"stream": 0, "capturing": False}
     seen = []
 
     class Device:           # a GPU's name over host memory
-        type, index = "cuda", None
-        __str__ = lambda self: "cuda:0"
+        type, index = "cuda", 0
+
+    gpu = Device()
 
     def make(*a, device, **k):
         return real(*a, device="cpu", **k)
@@ -65,14 +65,14 @@ def forward(monkeypatch):
     real = mhc.PreForward
     monkeypatch.setattr(mhc, "PreForward", make)
     monkeypatch.setattr(mhc, "raw_forward", launch)
-    monkeypatch.setattr(mhc, "_stream", lambda device: where["stream"])
+    monkeypatch.setattr(mhc, "_raw_stream", lambda device: where["stream"])
     monkeypatch.setattr(mhc, "_capturing", lambda device: where["capturing"], raising=False)
     monkeypatch.setattr(mhc, "_RUNNERS", type(mhc._RUNNERS)())
     keep = []
 
     def call(tokens, stream, capturing=False):
-        where.update(stream=ctypes.c_void_p(stream) if stream else None, capturing=capturing)
-        r = mhc._runner(tokens, N, D, 3, 20, 1e-6, 1e-6, False, Device())
+        where.update(stream=stream, capturing=capturing)
+        r = mhc._runner(tokens, N, D, 3, 20, 1e-6, 1e-6, False, gpu)
         keep.append(r)
         z = torch.zeros
         r(z((tokens, N, D), dtype=torch.bfloat16), z((M, N * D)), z(3), z(M))
