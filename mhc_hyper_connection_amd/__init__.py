@@ -399,16 +399,14 @@ class PreBackward:
         for k, v in out.items():
             ptrs[k] = _ptr(v)
         ws = self.workspace if self.workspace is not None else self._new_workspace()
-        if ck is not None:
-            with _on_gpu(dev):
-                st = raw_backward_checkpoint(self.params, ptrs, _ptr(ck.codes), _ptr(ck.scales), _ptr(ws),
-                                             self.ws_bytes, _stream(dev))
-            if st != MHC_OK:
-                raise MhcError(st, "mhc_pre_backward_checkpoint")
-            return out
-        st = raw_backward(self.params, ptrs, _ptr(ws), self.ws_bytes, _stream(dev))
+        with _on_gpu(dev):
+            if ck is not None:
+                what, st = "mhc_pre_backward_checkpoint", raw_backward_checkpoint(
+                    self.params, ptrs, _ptr(ck.codes), _ptr(ck.scales), _ptr(ws), self.ws_bytes, _stream(dev))
+            else:
+                what, st = "mhc_pre_backward", raw_backward(self.params, ptrs, _ptr(ws), self.ws_bytes, _stream(dev))
         if st != MHC_OK:
-            raise MhcError(st, "mhc_pre_backward")
+            raise MhcError(st, what)
         return out
 
 

@@ -44,6 +44,28 @@ def test_backward_calls_in_flight_share_no_workspace(monkeypatch, checkpoint):
             assert a + size <= b or b + other <= a, "two calls in flight write to one workspace"
 
 
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_backward_runs_with_its_tensors_device_current(monkeypatch, checkpoint):
+    # as on a second GPU while the first is the current one
+    current = []
+
+    @contextlib.contextmanager
+    def on_gpu(device):
+        current.append(device)
+        yield
+        current.pop()
+
+    def launch(*args):
+        assert current == [torch.device("cpu")]      # the tensors' device here
+        return mhc.MHC_OK
+
+    monkeypatch.setattr(mhc, "raw_backward", launch)
+    monkeypatch.setattr(mhc, "raw_backward_checkpoint", launch)
+    monkeypatch.setattr(mhc, "_stream", lambda device: None)
+    monkeypatch.setattr(mhc, "_on_gpu", on_gpu)
+    mhc.mhc_pre_backward(*backward_inputs(checkpoint))
+
+
 @pytest.fixture
 def forward(monkeypatch):
     """mhc_pre on tensors of a size, on a stream of that handle or under capture: the workspace it took."""
