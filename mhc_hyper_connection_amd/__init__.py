@@ -23,7 +23,7 @@ from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        ACTS, glu_backward_workspace_size, make_glu_params, raw_glu, raw_glu_backward,
                        raw_checkpoint_restore, raw_post_checkpoint, raw_post_backward, raw_backward_checkpoint,
                        load, make_bwd_params, make_params, packed_size, raw_backward,
-                       raw_forward, raw_forward_noalloc, raw_forward_timed, raw_prepack, raw_wait_status,
+                       raw_forward, raw_forward_noalloc, capture_id, raw_forward_timed, raw_prepack, raw_wait_status,
                        status_string,
                        version, workspace_size)
 
@@ -249,7 +249,8 @@ class PreForward:
         return out
 
 
-_RUNNERS: dict = {}   # mhc_pre's launchers
+_RUNNERS: dict = {}         # mhc_pre's launchers, by size and stream
+_GRAPH_RUNNERS: dict = {}   # those that graphs replay with, by size and capture: kept as long as a graph may live
 _MAX_RUNNERS = 64
 
 
@@ -258,22 +259,28 @@ def _capturing(device):
 
 
 def _runner(T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, device, x_f16=False):
-    """The launcher of a size on the current stream: calls on one stream are ordered and share
-    its workspace, calls on different streams share none. A captured call has one of its own,
-    which the graph fills with zeros at each replay: the graph may be replayed on any stream."""
-    cached = not _capturing(device)
-    if cached:
-        key = (T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, device, x_f16,
-               _raw_stream(device) if device.type == "cuda" else 0)
-        r = _RUNNERS.get(key)
-        if r is not None:
-            return r
-    r = PreForward(T, n, D, n_alpha, num_iters=num_iters, norm_eps=norm_eps, hc_eps=hc_eps,
-                   need_backward=need_backward, device=device, x_f16=x_f16)
-    if cached:
-        _RUNNERS[key] = r
-        if len(_RUNNERS) > _MAX_RUNNERS:      # the oldest; its memory is freed in its stream's order
-            _RUNNERS.pop(next(iter(_RUNNERS)))
+    """The launcher of a size for the current stream: calls on one stream are ordered and share
+    its workspace, calls on different streams share none. Under capture it is the graph's alone: an
+    eager call's of this size, which eager calls then do without, or (no such call before, or none
+    since the last capture) a new one for each call, which the graph fills with zeros at every replay."""
+    size = (T, n, D, n_alpha, num_iters, norm_eps, hc_eps, need_backward, device, x_f16)
+    if not _capturing(device):
+        key, kept = (*size, _raw_stream(device) if device.type == "cuda" else 0), _RUNNERS
+    else:
+        capture = capture_id(_raw_stream(device))
+        key, kept = (*size, capture), _GRAPH_RUNNERS
+        if capture and key not in kept and len(kept) < _MAX_RUNNERS:
+            eager = next((k for k in reversed(_RUNNERS) if k[:-1] == size), None)
+            if eager is not None:
+                kept[key] = _RUNNERS.pop(eager)
+    r = kept.get(key)
+    if r is None:
+        r = PreForward(T, n, D, n_alpha, num_iters=num_iters, norm_eps=norm_eps, hc_eps=hc_eps,
+                       need_backward=need_backward, device=device, x_f16=x_f16)
+        if kept is _RUNNERS:
+            kept[key] = r
+            if len(kept) > _MAX_RUNNERS:      # the oldest; its memory is freed in its stream's order
+                kept.pop(next(iter(kept)))
     return r
 
 
@@ -289,6 +296,9 @@ def mhc_pre(x, phi, alpha, bias, gamma=None, pre_mix=None, *, num_iters=20, norm
 
     Returns (h_in, h_post, h_res, extras); extras holds inv_rms, h_mix, h_pre, sum_out
     and norm_out when need_backward is set. Shapes follow x's leading dimensions.
+    Calls on different streams share no workspace, and neither do captured calls with eager
+    ones or with another graph's. A capture takes over the workspace of the last eager call of
+    its size, which has to be over by the graph's first replay (torch.cuda.graph waits for it).
     """
     lead = tuple(x.shape[:-2])
     n, D = int(x.shape[-2]), int(x.shape[-1])

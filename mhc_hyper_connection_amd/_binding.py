@@ -343,3 +343,15 @@ def glu_backward_workspace_size(params: GluParams, from_checkpoint) -> int:
 def raw_glu_backward(params: GluParams, ptrs: dict, ws_ptr, ws_bytes, stream) -> int:
     t = GluBwdTensors(*[ptrs.get(f) for f in GLU_BWD_TENSOR_FIELDS])
     return int(load().mhc_glu_backward(ctypes.byref(params), ctypes.byref(t), ws_ptr, ws_bytes, stream))
+
+
+def capture_id(stream) -> int:
+    """The id of the graph capture that a stream (a raw handle) is part of, 0 if of none or unknown. Asked of the HIP
+    runtime that the library is linked with."""
+    get = getattr(load(), "hipStreamGetCaptureInfo", None)
+    if get is None:
+        return 0
+    get.restype = ctypes.c_int
+    get.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_ulonglong)]
+    status, number = ctypes.c_int(0), ctypes.c_ulonglong(0)
+    return int(number.value) if get(stream, ctypes.byref(status), ctypes.byref(number)) == 0 and status.value == 1 else 0

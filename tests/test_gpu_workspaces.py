@@ -136,3 +136,52 @@ def test_forward_first_called_under_capture(T, D):
         eager = [forward(a) for a in args]
         torch.cuda.synchronize()
         assert all(same(o, w) for o, w in zip(outs + eager, want + want)), rep
+
+
+@pytest.mark.parametrize("T,D", [(60, 1088), (1300, 264), (4100, 1024)])
+def test_forward_captured_after_eager_calls(T, D):
+    # the first graph takes the eager calls' workspace, the second has one of its own, later eager calls have a new one: replayed
+    # at the same time on streams of their own where no workgroups wait on each other (T > 64)
+    import torch
+    print(f"[case] forward captured after eager calls T={T} D={D}", file=sys.stderr, flush=True)
+    args = [forward_inputs(T, D, seed) for seed in (1, 2, 3)]
+    want = [bits(forward(a)) for a in args]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a in args[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            first = forward(a)
+            outs.append({**{"2 " + k: v for k, v in forward(a).items()}, **first})      # two calls in one graph
+        graphs.append(graph)
+    want2 = [{**{"2 " + k: v for k, v in w.items()}, **w} for w in want[:2]]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(device()) for _ in range(3)]
+    for rep in range(4):
+        for o in outs:
+            for v in o.values():
+                v.view(torch.uint8).fill_(0x7F)
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+            if T <= 64:
+                torch.cuda.synchronize()
+        with torch.cuda.stream(streams[2]):
+            eager = forward(args[2])
+        torch.cuda.synchronize()
+        assert same(eager, want[2]) and all(same(o, w) for o, w in zip(outs, want2)), rep
+
+
+def test_captures_are_told_apart():
+    import torch
+    from mhc_hyper_connection_amd import _binding as B
+    dev = device()
+    numbers = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            numbers.append([B.capture_id(torch.cuda.current_stream(dev).cuda_stream) for _ in range(2)])
+            torch.zeros(8, device=dev)
+    assert numbers[0][0] == numbers[0][1] > 0 and numbers[1][0] == numbers[1][1] > 0 and numbers[0][0] != numbers[1][0]
+    assert B.capture_id(torch.cuda.current_stream(dev).cuda_stream) == 0

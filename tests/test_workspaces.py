@@ -68,8 +68,8 @@ def test_backward_runs_with_its_tensors_device_current(monkeypatch, checkpoint):
 
 @pytest.fixture
 def forward(monkeypatch):
-    """mhc_pre on tensors of a size, on a stream of that handle or under capture: the workspace it took."""
-    where = {"stream": 0, "capturing": False}
+    """mhc_pre on tensors of a size, on a stream of that handle or in a capture of that number: the workspace it took."""
+    where = {"stream": 0, "capture": 0}
     seen = []
 
     class Device:           # a GPU's name over host memory
@@ -88,12 +88,14 @@ def forward(monkeypatch):
     monkeypatch.setattr(mhc, "PreForward", make)
     monkeypatch.setattr(mhc, "raw_forward", launch)
     monkeypatch.setattr(mhc, "_raw_stream", lambda device: where["stream"])
-    monkeypatch.setattr(mhc, "_capturing", lambda device: where["capturing"], raising=False)
-    monkeypatch.setattr(mhc, "_RUNNERS", type(mhc._RUNNERS)())
+    monkeypatch.setattr(mhc, "_capturing", lambda device: where["capture"] != 0)
+    monkeypatch.setattr(mhc, "capture_id", lambda stream: where["capture"] if where["capture"] > 0 else 0)
+    monkeypatch.setattr(mhc, "_RUNNERS", {})
+    monkeypatch.setattr(mhc, "_GRAPH_RUNNERS", {})
     keep = []
 
-    def call(tokens, stream, capturing=False):
-        where.update(stream=stream, capturing=capturing)
+    def call(tokens, stream, capture=0):
+        where.update(stream=stream, capture=capture)
         r = mhc._runner(tokens, N, D, 3, 20, 1e-6, 1e-6, False, gpu)
         keep.append(r)
         z = torch.zeros
@@ -109,14 +111,31 @@ def test_forward_calls_on_different_streams_share_no_workspace(forward):
     assert forward(T, 16) == first and forward(T, 32) == second and forward(T, 0) == default
 
 
-def test_captured_forward_calls_have_workspaces_of_their_own(forward):
+def test_graphs_share_no_workspace_with_eager_calls_or_each_other(forward):
+    eager, other = forward(T, 16), forward(T, 32)
+    a = forward(T, 48, capture=1)
+    assert a == other and forward(T, 48, capture=1) == a      # the last eager call's, zero-filled and used before; the same all through the graph
+    b = forward(T, 48, capture=2)
+    assert b == eager
+    c, d = forward(T, 48, capture=3), forward(T, 48, capture=3)
+    again, more = forward(T, 16), forward(T, 32)              # eager calls have new ones
+    assert len({a, b, c, d, again, more}) == 6
+    assert forward(T, 48, capture=1) == a and forward(T, 16) == again
+    e = forward(T + 1, 16)
+    assert forward(T, 48, capture=4) in (again, more) and forward(T + 1, 16) == e      # of its own size
+
+
+def test_a_capture_without_a_number_takes_no_eager_workspace(forward):
     eager = forward(T, 16)
-    a, b = forward(T, 16, capturing=True), forward(T, 16, capturing=True)
-    assert len({eager, a, b}) == 3
-    assert forward(T, 16) == eager          # and nothing of a capture serves a later eager call
+    a, b = forward(T, 48, capture=-1), forward(T, 48, capture=-1)
+    assert len({eager, a, b}) == 3 and forward(T, 16) == eager
 
 
 def test_forward_keeps_few_launchers(forward):
     for tokens in range(1, 2 * mhc._MAX_RUNNERS):
         forward(tokens, 0)
     assert len(mhc._RUNNERS) <= mhc._MAX_RUNNERS
+    for capture in range(1, 2 * mhc._MAX_RUNNERS):
+        forward(T, 0)
+        forward(T, 48, capture=capture)
+    assert len(mhc._GRAPH_RUNNERS) <= mhc._MAX_RUNNERS
