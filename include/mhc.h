@@ -605,12 +605,12 @@ mhc_status mhc_glu(const mhc_glu_params* params, const mhc_glu_tensors* tensors,
  * (fp32 sums, one rounding to x_dtype), and h again where asked for: the gradient of the
  * projection behind it needs it, so a caller need not keep it.
  * dg and du are operands of the matrix products and have x_dtype's precision and range, as
- * the gradient of a layer kept in that format has: the gradients carry two roundings, not
- * one (2.3e-3 of their norm in bf16, 2.9e-4 in fp16; one rounding is 1.7e-3 and 2.1e-4). In fp16 a value of dg or du from
- * 65520 on becomes infinite (then that token's grad_x, and that f's rows of the weights'
- * gradients, are infinite or NaN), and below 6e-5 values are multiples of 6e-8, zero under
- * 3e-8: the loss scale that keeps grad_h in fp16's range has to keep dh u act'(g) and
- * dh act(g) there too. bf16 has fp32's range.
+ * the gradient of a layer kept in that format has. The gradients carry two roundings, not
+ * one: 2.3e-3 of their norm in bf16 and 2.9e-4 in fp16, where one is 1.7e-3 and 2.1e-4. In
+ * fp16 a value of dg or du from 65520 on becomes infinite (then that token's grad_x, and
+ * that f's rows of the weights' gradients, are infinite or NaN), below 6e-5 values are
+ * multiples of 6e-8, and under 3e-8 they are zero: the loss scale that keeps grad_h in
+ * fp16's range has to keep dh u act'(g) and dh act(g) there too. bf16 has fp32's range.
  *   grad_h x_dtype [T, F]; x x_dtype [T, D], or x_codes int8 [T, D] and x_scales uint8
  *   [T, ceil(D / 32)] (then x NULL; the values are restored into the workspace);
  *   w_gate, w_up x_dtype [F, D]; grad_x x_dtype [T, D]; grad_w_gate, grad_w_up x_dtype

@@ -19,10 +19,10 @@
 //   bwd_token_kernel    one wave per token: the hPre gradient in fp64, the gate backward,
 //                       gMix, c3 = gInv invRms^3 / (n D), and the token's alpha/bias terms
 //   bwd_main_kernel     one workgroup per (token group, d-block, stream group), or per (token
-//                       group, run of d-blocks, stream) for large x: per tile of 64 tokens, xrsGrad on
-//                       the matrix cores (phi terms x gMix terms, six products), gradX, the gradGamma sums, and gMix^T . x on the
-//                       matrix cores, both transposed on their way out of LDS; group sums to
-//                       partials
+//                       group, run of d-blocks, stream) for large x: per tile of 64 tokens,
+//                       xrsGrad on the matrix cores (phi terms x gMix terms, six products),
+//                       gradX, the gradGamma sums, and gMix^T . x on the matrix cores, both
+//                       transposed on their way out of LDS; group sums to partials
 //   bwd_reduce_*        fixed-order fp64 sums of the partials (gradPhi, gradGamma) and
 //                       of the per-token terms (gradAlpha, gradBias)
 // x, gradHIn, gradXPost and gradX are bf16, or all fp16 (the guide's section 8.2: gradX

@@ -142,7 +142,7 @@ MHC_BWD_HOST_DEVICE inline bool run_task(int64_t blk, int runs, int n, int64_t t
 //   n = 8  D = 1024, no gradXPost   1.02 - 1.03, 1.01 - 1.02, 0.98 - 1.00; with it 0.94 - 1.06, 0.91 - 1.00, 0.91 - 0.97
 //          D = 520                  0.96 - 1.08, 0.93 - 1.01, 0.97 - 1.04
 // The lowest of each at n = 6 and 8 is fp16 with gradXPost and no gamma, where only the runs
-// have room for a second register set. fp16 splits x and gains from its size on a little later.
+// have room for a second register set. Without gradXPost fp16 gains only from larger sizes on.
 inline bool by_runs(const Geometry& g, int64_t T, bool gamma, bool xpost)
 {
     constexpr int64_t kMi = 1 << 20;
