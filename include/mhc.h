@@ -640,6 +640,216 @@ mhc_status mhc_glu_backward_workspace_size(const mhc_glu_params* params, int32_t
 mhc_status mhc_glu_backward(const mhc_glu_params* params, const mhc_glu_bwd_tensors* tensors, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ routing to experts
+ *
+ * A sub-layer whose feed-forward block is a mixture of experts: each token goes to top_k of E
+ * experts (gated projections of their own), whose results are added up by the token's weights.
+ * mhc_route chooses them from the router's logits l (hIn times the router's weight, a plain
+ * matrix product of the caller's):
+ *   s = softmax(l) over the E logits (MHC_SCORE_SOFTMAX) or sigmoid(l) (MHC_SCORE_SIGMOID)
+ *   c = s + bias                                  the choice; bias (optional) balances the load
+ *   groups > 1: the experts are `groups` equal runs; a group's value is the sum of its
+ *     group_top (1 or 2) largest c, and the top_groups groups of the largest values stay
+ *   the top_k experts with the largest c of what stays, in descending order
+ *   weights[j] = scale s_j, or with renormalise scale s_j / (the sum of the chosen s)
+ * Ties go to the lowest index. Scores, choices and sums are fp64 (without a bias the logits, whose
+ * order is that of the scores, are compared themselves), and each weight is rounded once.
+ * An expert whose logit or bias is -inf is masked: it is never chosen (a masked logit has the score
+ * 0; an expert masked by its bias still counts in the softmax). Where fewer than top_k experts
+ * are left (none, say, for a padded token whose logits are all -inf), the remaining slots hold expert
+ * -1 and weight 0; weights of scores that are all 0 are 0. A NaN among a token's logits
+ * or the biases, or with softmax a logit of +inf, makes all its weights NaN and its experts -1.
+ *   0 <= T <= 2^26, T * top_k < 2^31; 1 <= E <= 1024; 1 <= groups <= 16, a divisor of E;
+ *   1 <= top_groups <= groups; 1 <= top_k <= min(32, E / groups * top_groups); 0 < scale <= 1e30
+ *   logits  logits_dtype [T, E]     bias f32 [E] or NULL     weights f32 [T, top_k]
+ *   experts int32 [T, top_k]
+ * Pointers may be NULL only when T == 0 (nothing is launched). Asynchronous on `stream`, no
+ * workspace, no allocation; results are bitwise reproducible. Errors: NULLPTR, PARAM_INVALID,
+ * RUNTIME. */
+#define MHC_SCORE_SOFTMAX 0
+#define MHC_SCORE_SIGMOID 1
+#define MHC_DTYPE_F32 2
+
+typedef struct mhc_route_params {
+    int64_t T;
+    int32_t E;
+    int32_t top_k;
+    int32_t groups;
+    int32_t top_groups;
+    int32_t group_top;
+    int32_t score;          /* MHC_SCORE_SOFTMAX or MHC_SCORE_SIGMOID */
+    int32_t renormalise;    /* 0 or 1 */
+    int32_t logits_dtype;   /* MHC_DTYPE_BF16, MHC_DTYPE_F16 or MHC_DTYPE_F32 */
+    double scale;
+} mhc_route_params;
+
+mhc_status mhc_route(const mhc_route_params* params, const void* logits, const float* bias, float* weights,
+                     int32_t* experts, void* stream);
+
+/* Its backward: the logits' gradient from the weights' (the choice itself has none, and nor
+ * has the bias). With g = grad_weights, p_j = weights_j / scale and S = sum_j g_j p_j:
+ *   softmax, renormalise   dl_j = weights_j (g_j - S)                 at the chosen experts
+ *   sigmoid, renormalise   dl_j = weights_j (1 - s_j) (g_j - S)       at the chosen experts
+ *   sigmoid                dl_j = weights_j (1 - s_j) g_j             at the chosen experts
+ *   softmax                dl_e = [e chosen] weights_e g_e - s_e sum_j weights_j g_j
+ * and zero elsewhere. Slots with an expert that is not in [0, E) count for nothing; a token
+ * with a NaN weight gets NaN. The terms of a token's slots are fp64, the scores of its other
+ * experts fp32, with one rounding to logits_dtype. An expert in two slots of a token gets their sum.
+ *   params as in the forward (groups, top_groups and group_top are checked and not used)
+ *   grad_weights f32 [T, top_k]; logits, weights, experts as in the forward;
+ *   grad_logits logits_dtype [T, E]: overwritten, must not alias the inputs
+ * Rules and errors as mhc_route's. */
+mhc_status mhc_route_backward(const mhc_route_params* params, const float* grad_weights, const void* logits,
+                              const float* weights, const int32_t* experts, void* grad_logits, void* stream);
+
+/* What the experts' products read of a routing: the P = T * top_k pairs (token, slot), numbered
+ * t * top_k + j, sorted by expert, each expert's in their order, the pairs without an expert (-1, or
+ * any number outside [0, E)) last.
+ *   0 <= P < 2^31; 1 <= E <= 1024
+ *   experts int32 [P]
+ *   offsets int32 [E + 1]: expert e has the sorted pairs [offsets[e], offsets[e + 1]); offsets[E] is
+ *           where those without an expert begin
+ *   pairs   int32 [P]
+ * experts and pairs may be NULL when P == 0 (the offsets are then zeros). The workspace (of
+ * mhc_experts_plan_workspace_size bytes, 0 for few pairs, 256-byte aligned) needs no
+ * initialisation, and calls that may overlap need distinct ones. Asynchronous on `stream`, no
+ * allocation; the result does not depend on the order of execution. Errors: NULLPTR,
+ * PARAM_INVALID, RUNTIME. */
+mhc_status mhc_experts_plan_workspace_size(int64_t P, int32_t E, size_t* bytes);
+
+mhc_status mhc_experts_plan(int64_t P, int32_t E, const int32_t* experts, int32_t* offsets, int32_t* pairs,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ microscaled 4-bit floats
+ *
+ * Rows of D values in 4 bits each with one power of two for each block of 32 along D (the last may be
+ * shorter). A code is e2m1: 0, 1/2, 1, 3/2, 2, 3, 4, 6 for 0 .. 7, their negatives for 8 .. 15. With
+ * a = the largest magnitude in a block, its step is 2^e with e the least exponent for which a is
+ * under 7 steps (not below -127, nor above what keeps 6 steps finite: 13 for fp16, 125 for bf16); a
+ * value's code is its nearest multiple's, ties to the even code, within +-6. Every value is off by at
+ * most a / 5, or by 2^-129 where that is more (by a / 4 where a passes 7 steps of the largest e).
+ * code * step is exact in the 16-bit format it came from. The scale byte is e + 127; 255 marks a
+ * block that held a NaN or an infinity, whose values come back NaN and whose products are NaN.
+ *   codes    uint8 [rows, 16 * ceil(D / 32)]: two to a byte, the even value's in the low half
+ *   scales   uint8 [rows, 4 * ceil(D / 128)]: a row's in whole 32-bit words
+ * Codes behind D and scale bytes behind the last block are written as zeros; the products take them for that
+ * (a scale byte of 255 there would spoil its row).
+ *   rows >= 0; 1 <= D <= 65536;  x x_dtype [rows, D], 16-byte aligned; codes 16-byte, scales
+ *   4-byte aligned; rows * ceil(D / 128) * 16 <= 2^32 - 256
+ * Pointers may be NULL only when rows == 0 (nothing is launched). Asynchronous on `stream`,
+ * no workspace, no allocation; outputs must not alias inputs. Errors: NULLPTR,
+ * PARAM_INVALID, RUNTIME. */
+typedef struct mhc_mxfp4_params {
+    int64_t rows;
+    int32_t D;
+    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16 */
+} mhc_mxfp4_params;
+
+mhc_status mhc_mxfp4(const mhc_mxfp4_params* params, const uint16_t* x, uint8_t* codes, uint8_t* scales, void* stream);
+
+mhc_status mhc_mxfp4_restore(const mhc_mxfp4_params* params, const uint8_t* codes, const uint8_t* scales, uint16_t* x,
+                             void* stream);
+
+/* ------------------------------------------------------------------ products with 4-bit weights
+ *
+ * y = x w^T, both in microscaled 4-bit floats on the matrix cores: sums in fp32 of products that are exact, one
+ * rounding to x_dtype. For serving: there is no gradient of a rounding to 4 bits. x comes in 16
+ * bits and is rounded to 4 as mhc_mxfp4 does, into the workspace, or in 4 bits.
+ *   T >= 0; 1 <= K <= 65536; N a multiple of 8 in [8, 65536]; T * 16 ceil(K / 32) < 2^31
+ *   x x_dtype [T, K] (16-byte aligned), or x_codes and x_scales (as mhc_mxfp4 lays them out);
+ *   w_codes [N, 16 ceil(K / 32)], w_scales [N, 4 ceil(K / 128)];
+ *   y x_dtype [T, N], 16-byte aligned
+ * With T == 0 nothing is launched, and x and y may be NULL. The workspace (256-byte aligned, of
+ * mhc_mxfp4_product_workspace_size bytes; x_mxfp4 1 where x comes in 4 bits, which needs
+ * none, else 0) needs no initialisation, and calls that may overlap need distinct ones. Asynchronous on
+ * `stream`, no allocation; every sum in a fixed order. y must not alias the inputs. Errors: NULLPTR
+ * (neither form of x given, or codes without scales), PARAM_INVALID (both forms given), RUNTIME. */
+typedef struct mhc_mxfp4_product_params {
+    int64_t T;
+    int32_t K;
+    int32_t N;
+    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16: x's (where it is in 16 bits) and y's */
+    int32_t reserved;   /* must be 0 */
+} mhc_mxfp4_product_params;
+
+typedef struct mhc_mxfp4_product_tensors {
+    const uint16_t* x;
+    const uint8_t* x_codes;
+    const uint8_t* x_scales;
+    const uint8_t* w_codes;
+    const uint8_t* w_scales;
+    uint16_t* y;
+} mhc_mxfp4_product_tensors;
+
+mhc_status mhc_mxfp4_product_workspace_size(const mhc_mxfp4_product_params* params, int32_t x_mxfp4, size_t* bytes);
+
+mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_mxfp4_product_tensors* tensors,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The experts' products, over the pairs of mhc_experts_plan:
+ *   mhc_experts_glu    h[t, j] = act(x[t] Wg[e]^T) (.) (x[t] Wu[e]^T),  e = experts[t, j]
+ *   mhc_experts_down   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
+ * with the weights of E experts in 4 bits, x and h in 16 bits (rounded to 4 into the workspace) or in 4. act as
+ * mhc_glu's. h is zero, and adds weights times zero, for pairs without an expert. Sums, activations and
+ * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype. A token's result does
+ * not depend on the other tokens but through the sizes T, E and top_k, which choose the order of the sums.
+ *   T >= 0, T * top_k < 2^31; 1 <= E <= 1024; 1 <= top_k <= 32; D, F multiples of 8 in [8, 65536];
+ *   of x (T rows of D values) and h (T * top_k rows of F): rows * 16 ceil(width / 32) < 2^31;
+ *   of mhc_experts_down: T * top_k * D < 2^35
+ *   x x_dtype [T, D], or codes and scales      h x_dtype [T, top_k, F], or (down) codes and scales
+ *   offsets int32 [E + 1], pairs int32 [T * top_k]   mhc_experts_plan's (pairs and offsets outside
+ *   [0, T * top_k] are taken for none, never read through)
+ *   w_gate, w_up [E, F, D], w_down [E, D, F]: codes [.., 16 ceil(width / 32)] and scales [.., 4
+ *   ceil(width / 128)] along their last dimension
+ *   weights f32 [T, top_k]      y x_dtype [T, D]
+ * 16-bit tensors and codes 16-byte, the others 4-byte aligned. With T == 0 nothing is launched, and
+ * the tensors of tokens and pairs may be NULL. Workspace, order and errors as mhc_mxfp4_product's (the
+ * workspace of mhc_experts_down holds T * top_k results of D fp32 values too). */
+typedef struct mhc_experts_params {
+    int64_t T;
+    int32_t E;
+    int32_t top_k;
+    int32_t D;
+    int32_t F;
+    int32_t act;        /* MHC_ACT_SILU or MHC_ACT_GELU_TANH (mhc_experts_down: not used, but checked) */
+    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16 */
+} mhc_experts_params;
+
+typedef struct mhc_experts_glu_tensors {
+    const uint16_t* x;
+    const uint8_t* x_codes;
+    const uint8_t* x_scales;
+    const int32_t* offsets;
+    const int32_t* pairs;
+    const uint8_t* w_gate_codes;
+    const uint8_t* w_gate_scales;
+    const uint8_t* w_up_codes;
+    const uint8_t* w_up_scales;
+    uint16_t* h;
+} mhc_experts_glu_tensors;
+
+typedef struct mhc_experts_down_tensors {
+    const uint16_t* h;
+    const uint8_t* h_codes;
+    const uint8_t* h_scales;
+    const int32_t* offsets;
+    const int32_t* pairs;
+    const float* weights;
+    const uint8_t* w_down_codes;
+    const uint8_t* w_down_scales;
+    uint16_t* y;
+} mhc_experts_down_tensors;
+
+mhc_status mhc_experts_glu_workspace_size(const mhc_experts_params* params, int32_t x_mxfp4, size_t* bytes);
+
+mhc_status mhc_experts_glu(const mhc_experts_params* params, const mhc_experts_glu_tensors* tensors, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+mhc_status mhc_experts_down_workspace_size(const mhc_experts_params* params, int32_t h_mxfp4, size_t* bytes);
+
+mhc_status mhc_experts_down(const mhc_experts_params* params, const mhc_experts_down_tensors* tensors, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

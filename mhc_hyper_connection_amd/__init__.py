@@ -21,6 +21,9 @@ from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        MHC_ERR_RUNTIME, MHC_OK, STAGES, MhcError, Params, bwd_workspace_size,
                        forward_path, raw_inv_rms, raw_post, raw_sinkhorn, raw_checkpoint,
                        ACTS, glu_backward_workspace_size, make_glu_params, raw_glu, raw_glu_backward,
+                       SCORES, ExpertsDownTensors, ExpertsGluTensors, ExpertsParams, Mxfp4ProductParams, ProductTensors,
+                       RouteParams, experts_plan_workspace_size, products_workspace_size, raw_experts_plan, raw_mxfp4,
+                       raw_mxfp4_restore, raw_products, raw_route, raw_route_backward,
                        raw_checkpoint_restore, raw_post_checkpoint, raw_post_backward, raw_backward_checkpoint,
                        load, make_bwd_params, make_params, packed_size, raw_backward,
                        raw_forward, raw_forward_noalloc, capture_id, raw_forward_timed, raw_prepack, raw_wait_status,
@@ -30,6 +33,8 @@ from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
 __all__ = ["PreForward", "PreBackward", "mhc_pre", "mhc_pre_backward", "mhc_post", "mhc_pre_inv_rms",
            "mhc_pre_sinkhorn", "prepack", "version", "Checkpoint", "mhc_checkpoint", "mhc_checkpoint_restore",
            "mhc_post_checkpoint", "mhc_post_backward", "mhc_glu", "mhc_glu_backward",
+           "mhc_route", "mhc_route_backward", "ExpertsPlan", "mhc_experts_plan", "Mxfp4", "mhc_mxfp4", "mhc_mxfp4_restore",
+           "mhc_mxfp4_product", "mhc_experts_glu", "mhc_experts_down",
            "status_string", "MhcError", "FORWARD_EVENTS", "STAGES",
            "make_params", "packed_size", "workspace_size", "load",
            "MHC_OK", "MHC_ERR_NULLPTR", "MHC_ERR_PARAM_INVALID", "MHC_ERR_RUNTIME"]
@@ -687,6 +692,298 @@ def mhc_glu_backward(grad_h, x, w_gate, w_up, *, act="silu", need_h=False, out=N
         st = raw_glu_backward(params, ptrs, _ptr(ws), ws_bytes, _stream(dev))
     if st != MHC_OK:
         raise MhcError(st, "mhc_glu_backward")
+    return out
+
+
+_LOGITS = {"bfloat16": 0, "float16": 1, "float32": 2}   # mhc_route_params.logits_dtype
+
+
+def _route_params(logits, top_k, groups, top_groups, group_top, score, renormalise, scale):
+    if score not in SCORES:
+        raise ValueError(f"score: {score!r}, expected one of {sorted(SCORES)}")
+    dt = _LOGITS.get(str(logits.dtype)[6:])
+    if dt is None:
+        raise ValueError(f"logits: dtype {logits.dtype}, expected torch.float32, torch.bfloat16 or torch.float16")
+    if logits.dim() < 1:
+        raise ValueError("logits: at least one dimension expected")
+    if top_k < 1:
+        raise ValueError(f"top_k: {top_k}, expected 1 or more")
+    return RouteParams(math.prod(logits.shape[:-1]), logits.shape[-1], top_k, groups, top_groups, group_top, SCORES[score],
+                       int(bool(renormalise)), dt, scale)
+
+
+def mhc_route(logits, top_k, *, bias=None, score="softmax", groups=1, top_groups=1, group_top=2, renormalise=True,
+              scale=1.0, out=None):
+    """The experts of each token and their weights, from the router's logits [..., E] (f32, bf16
+    or fp16). Scores are softmax or sigmoid of the logits (score); the top_k experts with the largest score + bias
+    (bias f32 [E], for balance; the weights are of the scores alone) are taken, with groups > 1 from the
+    top_groups groups whose group_top largest values have the largest sum; weights = scale * score, with
+    renormalise divided by their sum. Ties go to the lowest index, and the order is exact: fp64.
+    A logit of -inf masks its expert; slots without an expert hold -1 and weight 0, and a NaN makes a
+    token's weights NaN and its experts -1 (mhc_route in include/mhc.h has the rules and limits).
+    Returns (or fills: out a pair) weights f32 [..., top_k] and experts int32 [..., top_k]."""
+    torch = _torch()
+    params = _route_params(logits, top_k, groups, top_groups, group_top, score, renormalise, scale)
+    shape, dev = (*logits.shape[:-1], top_k), logits.device
+    _check(logits, "logits", logits.dtype, logits.shape, dev)
+    _check(bias, "bias", torch.float32, (logits.shape[-1],), dev)
+    if out is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        experts = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        weights, experts = out
+        for t, name, dt in ((weights, "out[0]", torch.float32), (experts, "out[1]", torch.int32)):
+            if t is None:
+                raise ValueError(f"{name} is required")
+            _check(t, name, dt, shape, dev)
+    with _on_gpu(dev):
+        st = raw_route(params, _ptr(logits), _ptr(bias), _ptr(weights), _ptr(experts), _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_route")
+    return weights, experts
+
+
+def mhc_route_backward(grad_weights, logits, weights, experts, *, score="softmax", renormalise=True, scale=1.0, out=None):
+    """mhc_route's gradient: from grad_weights f32 [..., top_k], the gradient with respect to its weights, and
+    its logits, weights and experts, the logits' gradient [..., E] in their dtype. score,
+    renormalise and scale as in the forward. The choice has no gradient, and so nor has the bias."""
+    torch = _torch()
+    if experts.dim() < 1:
+        raise ValueError("experts: at least one dimension expected")
+    params = _route_params(logits, experts.shape[-1], 1, 1, 1, score, renormalise, scale)
+    shape, dev = (*logits.shape[:-1], experts.shape[-1]), logits.device
+    _check(logits, "logits", logits.dtype, logits.shape, dev)
+    for t, name, dt in ((grad_weights, "grad_weights", torch.float32), (weights, "weights", torch.float32),
+                        (experts, "experts", torch.int32)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _check(t, name, dt, shape, dev)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    else:
+        _check(out, "out", logits.dtype, logits.shape, dev)
+    with _on_gpu(dev):
+        st = raw_route_backward(params, _ptr(grad_weights), _ptr(logits), _ptr(weights), _ptr(experts), _ptr(out),
+                                _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_route_backward")
+    return out
+
+
+ExpertsPlan = namedtuple("ExpertsPlan", ("offsets", "pairs", "shape"))
+ExpertsPlan.__doc__ = """What the experts' products read of a routing (mhc_experts_plan): offsets int32 [E + 1], where each
+expert's pairs begin; pairs int32 [P], the pairs' numbers sorted by expert; shape, that of `experts`, [..., top_k]."""
+
+
+def mhc_experts_plan(experts, num_experts):
+    """The ExpertsPlan of experts int32 [..., top_k], mhc_route's: a pair (token, slot) has the number of
+    its place in `experts`. Pairs of one expert keep their order; those without one (-1) come last, from offsets[-1] on."""
+    torch = _torch()
+    if experts.dim() < 1:
+        raise ValueError("experts: at least one dimension expected")
+    shape, dev = tuple(experts.shape), experts.device
+    _check(experts, "experts", torch.int32, shape, dev)
+    P, E = experts.numel(), int(num_experts)
+    ws_bytes = experts_plan_workspace_size(P, E)
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    pairs = torch.empty((P,), dtype=torch.int32, device=dev)
+    with _on_gpu(dev):
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        st = raw_experts_plan(P, E, _ptr(experts), _ptr(offsets), _ptr(pairs), _ptr(ws), ws_bytes, _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_experts_plan")
+    return ExpertsPlan(offsets, pairs, shape)
+
+
+Mxfp4 = namedtuple("Mxfp4", ("codes", "scales", "dtype", "size"))
+Mxfp4.__doc__ = """A tensor [..., size] in microscaled 4-bit floats (mhc_mxfp4 in include/mhc.h): codes uint8
+[..., 16 ceil(size / 32)], two to a byte; scales uint8 [..., 4 ceil(size / 128)], a power of two for each 32
+values; the dtype (torch.bfloat16 or torch.float16) it came from and is restored to; and its last dimension."""
+
+
+def _mxfp4_shapes(shape):
+    D = shape[-1]
+    return (*shape[:-1], 16 * -(-D // 32)), (*shape[:-1], 4 * -(-D // 128))
+
+
+def _check_mxfp4(m, name, shape, device):
+    torch = _torch()
+    if not isinstance(m, Mxfp4):
+        raise ValueError(f"{name}: an Mxfp4 expected, got {type(m).__name__}")
+    if m.size != shape[-1]:
+        raise ValueError(f"{name}: of {m.size} values, expected {shape[-1]}")
+    codes, scales = _mxfp4_shapes(shape)
+    _check(m.codes, f"{name}.codes", torch.uint8, codes, device)
+    _check(m.scales, f"{name}.scales", torch.uint8, scales, device)
+
+
+def mhc_mxfp4(x, *, out=None):
+    """x (bf16 or fp16 [..., D], any D) as its Mxfp4: four bits a value and a power of two for each 32 along D
+    (mhc_mxfp4 in include/mhc.h has the format; every value is off by at most a fifth of its
+    block's largest magnitude, and a block with a NaN or an infinity comes back as NaN). out: an
+    Mxfp4 to fill. The stream is torch's current stream on x's device."""
+    torch = _torch()
+    xdt = _x_dtype(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x: at least one dimension expected")
+    shape, dev = tuple(x.shape), x.device
+    _check(x, "x", xdt, shape, dev)
+    if out is None:
+        codes, scales = _mxfp4_shapes(shape)
+        out = Mxfp4(torch.empty(codes, dtype=torch.uint8, device=dev), torch.empty(scales, dtype=torch.uint8, device=dev),
+                    xdt, shape[-1])
+    else:
+        _check_mxfp4(out, "out", shape, dev)
+        if out.dtype != xdt:
+            raise ValueError(f"out: of dtype {out.dtype}, expected {xdt}")
+    with _on_gpu(dev):
+        st = raw_mxfp4(math.prod(shape[:-1]), shape[-1], xdt == torch.float16, _ptr(x), _ptr(out.codes), _ptr(out.scales),
+                       _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_mxfp4")
+    return out
+
+
+def mhc_mxfp4_restore(m, *, out=None):
+    """The 16-bit tensor [..., D] (in m.dtype) that an Mxfp4 stands for."""
+    torch = _torch()
+    xdt = m.dtype
+    if xdt not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"m: of dtype {xdt}, expected torch.bfloat16 or torch.float16")
+    if m.codes.dim() < 1:
+        raise ValueError("m: at least one dimension expected")
+    shape, dev = (*m.codes.shape[:-1], m.size), m.codes.device
+    _check_mxfp4(m, "m", shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=xdt, device=dev)
+    else:
+        _check(out, "out", xdt, shape, dev)
+    with _on_gpu(dev):
+        st = raw_mxfp4_restore(math.prod(shape[:-1]), shape[-1], xdt == torch.float16, _ptr(m.codes), _ptr(m.scales),
+                               _ptr(out), _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_mxfp4_restore")
+    return out
+
+
+def _left(x, name):
+    """The left operand of a product with 4-bit weights: its shape, device, dtype, and the pointers of its 16-bit tensor
+    or of its codes and scales."""
+    torch = _torch()
+    if isinstance(x, Mxfp4):
+        if x.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"{name}: of dtype {x.dtype}, expected torch.bfloat16 or torch.float16")
+        if x.codes.dim() < 1:
+            raise ValueError(f"{name}: at least one dimension expected")
+        shape, dev = (*x.codes.shape[:-1], x.size), x.codes.device
+        _check_mxfp4(x, name, shape, dev)
+        return shape, dev, x.dtype, (None, _ptr(x.codes), _ptr(x.scales))
+    xdt = _x_dtype(x, name)
+    shape, dev = tuple(x.shape), x.device
+    if not shape:
+        raise ValueError(f"{name}: at least one dimension expected")
+    _check(x, name, xdt, shape, dev)
+    return shape, dev, xdt, (_ptr(x), None, None)
+
+
+def _run_products(name, params, tensors, in_4_bits, dev):
+    torch = _torch()
+    ws_bytes = products_workspace_size(name, params, in_4_bits)
+    with _on_gpu(dev):
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        st = raw_products(name, params, tensors, _ptr(ws), ws_bytes, _stream(dev))
+    if st != MHC_OK:
+        raise MhcError(st, name)
+
+
+def mhc_mxfp4_product(x, w, *, out=None):
+    """y = x w^T with w an Mxfp4 [N, K] and x [..., K] in bf16 or fp16, which is rounded to 4 bits as
+    mhc_mxfp4 does, or an Mxfp4 already: y [..., N] in x's dtype, exact products summed in fp32, one
+    rounding. For serving (there is no backward). The workspace is the call's own."""
+    torch = _torch()
+    shape, dev, xdt, ptrs = _left(x, "x")
+    if not isinstance(w, Mxfp4) or w.codes.dim() != 2:
+        raise ValueError("w: an Mxfp4 [N, K] expected")
+    N, K = int(w.codes.shape[0]), shape[-1]
+    _check_mxfp4(w, "w", (N, K), dev)
+    if out is None:
+        out = torch.empty((*shape[:-1], N), dtype=xdt, device=dev)
+    else:
+        _check(out, "out", xdt, (*shape[:-1], N), dev)
+    params = Mxfp4ProductParams(math.prod(shape[:-1]), K, N, int(xdt == torch.float16), 0)
+    _run_products("mhc_mxfp4_product", params, ProductTensors(*ptrs, _ptr(w.codes), _ptr(w.scales), _ptr(out)),
+                  isinstance(x, Mxfp4), dev)
+    return out
+
+
+def _check_plan(plan, E, device):
+    torch = _torch()
+    if not isinstance(plan, ExpertsPlan):
+        raise ValueError(f"plan: an ExpertsPlan expected, got {type(plan).__name__}")
+    if len(plan.shape) < 1:
+        raise ValueError("plan: of a shape [..., top_k]")
+    _check(plan.offsets, "plan.offsets", torch.int32, (E + 1,), device)
+    _check(plan.pairs, "plan.pairs", torch.int32, (math.prod(plan.shape),), device)
+
+
+def mhc_experts_glu(x, plan, w_gate, w_up, *, act="silu", out=None):
+    """The experts' gated projection: h[t, j] = act(x[t] w_gate[e]^T) * (x[t] w_up[e]^T) for each pair of the
+    plan, e its expert. x [..., D] (mhc_pre's hIn) in bf16 or fp16, which is rounded to 4 bits as mhc_mxfp4 does, or an
+    Mxfp4; plan of shape [..., top_k] with the same leading dimensions; w_gate and w_up Mxfp4 [E, F, D];
+    act "silu" or "gelu_tanh". Returns (or fills) h [..., top_k, F] in x's dtype, zero for pairs without
+    an expert. fp32 sums and activation, one rounding. For serving (there is no backward). The workspace is the
+    call's own."""
+    torch = _torch()
+    if act not in ACTS:
+        raise ValueError(f"act: {act!r}, expected one of {sorted(ACTS)}")
+    shape, dev, xdt, ptrs = _left(x, "x")
+    if not isinstance(w_gate, Mxfp4) or w_gate.codes.dim() != 3:
+        raise ValueError("w_gate: an Mxfp4 [E, F, D] expected")
+    (E, F), D = w_gate.codes.shape[:2], shape[-1]
+    _check_mxfp4(w_gate, "w_gate", (E, F, D), dev)
+    _check_mxfp4(w_up, "w_up", (E, F, D), dev)
+    _check_plan(plan, E, dev)
+    if tuple(plan.shape[:-1]) != shape[:-1]:
+        raise ValueError(f"plan: of shape {tuple(plan.shape)}, expected {(*shape[:-1], 'top_k')}")
+    if out is None:
+        out = torch.empty((*plan.shape, F), dtype=xdt, device=dev)
+    else:
+        _check(out, "out", xdt, (*plan.shape, F), dev)
+    params = ExpertsParams(math.prod(shape[:-1]), E, plan.shape[-1], D, F, ACTS[act], int(xdt == torch.float16))
+    tensors = ExpertsGluTensors(*ptrs, _ptr(plan.offsets), _ptr(plan.pairs), _ptr(w_gate.codes), _ptr(w_gate.scales),
+                                _ptr(w_up.codes), _ptr(w_up.scales), _ptr(out))
+    _run_products("mhc_experts_glu", params, tensors, isinstance(x, Mxfp4), dev)
+    return out
+
+
+def mhc_experts_down(h, plan, weights, w_down, *, out=None):
+    """The experts' projection back and each token's weighted sum: y[t] = sum over its slots of weights[t, j]
+    (h[t, j] w_down[e]^T), e the slot's expert. h [..., top_k, F] (mhc_experts_glu's) in bf16 or fp16, which is rounded
+    to 4 bits as mhc_mxfp4 does, or an Mxfp4; plan as there; weights f32 [..., top_k], mhc_route's; w_down
+    Mxfp4 [E, D, F]. Returns (or fills) y [..., D] in h's dtype (what mhc_post takes): fp32 sums, in the slots'
+    order, one rounding. A pair without an expert adds its weight times zero. For serving (there is no
+    backward). The workspace is the call's own, with an fp32 result for each pair."""
+    torch = _torch()
+    shape, dev, xdt, ptrs = _left(h, "h")
+    if not isinstance(w_down, Mxfp4) or w_down.codes.dim() != 3:
+        raise ValueError("w_down: an Mxfp4 [E, D, F] expected")
+    (E, D), F = w_down.codes.shape[:2], shape[-1]
+    _check_mxfp4(w_down, "w_down", (E, D, F), dev)
+    _check_plan(plan, E, dev)
+    if tuple(plan.shape) != shape[:-1]:
+        raise ValueError(f"plan: of shape {tuple(plan.shape)}, expected {shape[:-1]}")
+    if weights is None:
+        raise ValueError("weights is required")
+    _check(weights, "weights", torch.float32, shape[:-1], dev)
+    lead = shape[:-2]
+    if out is None:
+        out = torch.empty((*lead, D), dtype=xdt, device=dev)
+    else:
+        _check(out, "out", xdt, (*lead, D), dev)
+    params = ExpertsParams(math.prod(lead), E, plan.shape[-1], D, F, 0, int(xdt == torch.float16))
+    tensors = ExpertsDownTensors(*ptrs, _ptr(plan.offsets), _ptr(plan.pairs), _ptr(weights), _ptr(w_down.codes),
+                                 _ptr(w_down.scales), _ptr(out))
+    _run_products("mhc_experts_down", params, tensors, isinstance(h, Mxfp4), dev)
     return out
 
 

@@ -60,7 +60,10 @@ EXPORTS = ("mhc_version", "mhc_status_string", "mhc_pre_packed_size",
            "mhc_pre_backward", "mhc_post", "mhc_pre_inv_rms", "mhc_pre_sinkhorn",
            "mhc_pre_wait_status", "mhc_pre_forward_noalloc", "mhc_checkpoint", "mhc_checkpoint_restore",
            "mhc_post_checkpoint", "mhc_post_backward", "mhc_pre_backward_checkpoint", "mhc_glu",
-           "mhc_glu_backward_workspace_size", "mhc_glu_backward")
+           "mhc_glu_backward_workspace_size", "mhc_glu_backward", "mhc_route", "mhc_route_backward",
+           "mhc_experts_plan_workspace_size", "mhc_experts_plan", "mhc_mxfp4", "mhc_mxfp4_restore",
+           "mhc_mxfp4_product_workspace_size", "mhc_mxfp4_product", "mhc_experts_glu_workspace_size", "mhc_experts_glu",
+           "mhc_experts_down_workspace_size", "mhc_experts_down")
 
 # MHC_FORWARD_EVENTS: events of mhc_pre_forward_timed (before the first kernel, then one
 # after each of pack, projection, epilogue, hIn)
@@ -120,6 +123,53 @@ class GluBwdTensors(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in GLU_BWD_TENSOR_FIELDS]
 
 
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class RouteParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("logits_dtype", ctypes.c_int32), ("scale", ctypes.c_double)]
+
+
+class Mxfp4Params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int32), ("x_dtype", ctypes.c_int32)]
+
+
+class Mxfp4ProductParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ExpertsParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("F", ctypes.c_int32), ("act", ctypes.c_int32), ("x_dtype", ctypes.c_int32)]
+
+
+PRODUCT_TENSOR_FIELDS = ("x", "x_codes", "x_scales", "w_codes", "w_scales", "y")
+EXPERTS_GLU_TENSOR_FIELDS = ("x", "x_codes", "x_scales", "offsets", "pairs", "w_gate_codes", "w_gate_scales", "w_up_codes",
+                             "w_up_scales", "h")
+EXPERTS_DOWN_TENSOR_FIELDS = ("h", "h_codes", "h_scales", "offsets", "pairs", "weights", "w_down_codes", "w_down_scales",
+                              "y")
+
+
+class ProductTensors(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in PRODUCT_TENSOR_FIELDS]
+
+
+class ExpertsGluTensors(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in EXPERTS_GLU_TENSOR_FIELDS]
+
+
+class ExpertsDownTensors(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in EXPERTS_DOWN_TENSOR_FIELDS]
+
+
+_PRODUCTS = (("mhc_mxfp4_product", Mxfp4ProductParams, ProductTensors),
+             ("mhc_experts_glu", ExpertsParams, ExpertsGluTensors),
+             ("mhc_experts_down", ExpertsParams, ExpertsDownTensors))
+
+
 def load(path: str | None = None):
     """Load and bind libmhc.so. Raises if it has not been built."""
     global _lib
@@ -177,7 +227,17 @@ def load(path: str | None = None):
             ("mhc_glu", [ctypes.POINTER(GluParams), ctypes.POINTER(GluTensors), vp]),
             ("mhc_glu_backward_workspace_size", [ctypes.POINTER(GluParams), ctypes.c_int32,
                                                  ctypes.POINTER(ctypes.c_size_t)]),
-            ("mhc_glu_backward", [ctypes.POINTER(GluParams), ctypes.POINTER(GluBwdTensors), vp, ctypes.c_size_t, vp])):
+            ("mhc_glu_backward", [ctypes.POINTER(GluParams), ctypes.POINTER(GluBwdTensors), vp, ctypes.c_size_t, vp]),
+            ("mhc_route", [ctypes.POINTER(RouteParams), vp, vp, vp, vp, vp]),
+            ("mhc_route_backward", [ctypes.POINTER(RouteParams), vp, vp, vp, vp, vp, vp]),
+            ("mhc_experts_plan_workspace_size", [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+            ("mhc_experts_plan", [ctypes.c_int64, ctypes.c_int32, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            ("mhc_mxfp4", [ctypes.POINTER(Mxfp4Params), vp, vp, vp, vp]),
+            ("mhc_mxfp4_restore", [ctypes.POINTER(Mxfp4Params), vp, vp, vp, vp]),
+            *((f"{name}_workspace_size", [ctypes.POINTER(params), ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)])
+              for name, params, _ in _PRODUCTS),
+            *((name, [ctypes.POINTER(params), ctypes.POINTER(tensors), vp, ctypes.c_size_t, vp])
+              for name, params, tensors in _PRODUCTS)):
         getattr(lib, name).restype = ctypes.c_int32
         getattr(lib, name).argtypes = argtypes
     if path is None:
@@ -343,6 +403,51 @@ def glu_backward_workspace_size(params: GluParams, from_checkpoint) -> int:
 def raw_glu_backward(params: GluParams, ptrs: dict, ws_ptr, ws_bytes, stream) -> int:
     t = GluBwdTensors(*[ptrs.get(f) for f in GLU_BWD_TENSOR_FIELDS])
     return int(load().mhc_glu_backward(ctypes.byref(params), ctypes.byref(t), ws_ptr, ws_bytes, stream))
+
+
+def raw_route(params: RouteParams, logits_ptr, bias_ptr, weights_ptr, experts_ptr, stream) -> int:
+    return int(load().mhc_route(ctypes.byref(params), logits_ptr, bias_ptr, weights_ptr, experts_ptr, stream))
+
+
+def raw_route_backward(params: RouteParams, grad_weights_ptr, logits_ptr, weights_ptr, experts_ptr, grad_logits_ptr,
+                       stream) -> int:
+    return int(load().mhc_route_backward(ctypes.byref(params), grad_weights_ptr, logits_ptr, weights_ptr, experts_ptr,
+                                         grad_logits_ptr, stream))
+
+
+def experts_plan_workspace_size(P, E) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().mhc_experts_plan_workspace_size(int(P), int(E), ctypes.byref(out))
+    if st != MHC_OK:
+        raise MhcError(st, "mhc_experts_plan_workspace_size")
+    return int(out.value)
+
+
+def raw_experts_plan(P, E, experts_ptr, offsets_ptr, pairs_ptr, ws_ptr, ws_bytes, stream) -> int:
+    return int(load().mhc_experts_plan(int(P), int(E), experts_ptr, offsets_ptr, pairs_ptr, ws_ptr, ws_bytes, stream))
+
+
+def raw_mxfp4(rows, D, x_f16, x_ptr, codes_ptr, scales_ptr, stream) -> int:
+    p = Mxfp4Params(int(rows), int(D), int(bool(x_f16)))
+    return int(load().mhc_mxfp4(ctypes.byref(p), x_ptr, codes_ptr, scales_ptr, stream))
+
+
+def raw_mxfp4_restore(rows, D, x_f16, codes_ptr, scales_ptr, x_ptr, stream) -> int:
+    p = Mxfp4Params(int(rows), int(D), int(bool(x_f16)))
+    return int(load().mhc_mxfp4_restore(ctypes.byref(p), codes_ptr, scales_ptr, x_ptr, stream))
+
+
+def products_workspace_size(name, params, in_4_bits) -> int:
+    """The workspace of mhc_mxfp4_product, mhc_experts_glu or mhc_experts_down (`name`)."""
+    out = ctypes.c_size_t(0)
+    st = getattr(load(), name + "_workspace_size")(ctypes.byref(params), int(bool(in_4_bits)), ctypes.byref(out))
+    if st != MHC_OK:
+        raise MhcError(st, name + "_workspace_size")
+    return int(out.value)
+
+
+def raw_products(name, params, tensors, ws_ptr, ws_bytes, stream) -> int:
+    return int(getattr(load(), name)(ctypes.byref(params), ctypes.byref(tensors), ws_ptr, ws_bytes, stream))
 
 
 def capture_id(stream) -> int:

@@ -23,8 +23,9 @@ ARCH = os.environ.get("MHC_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = [os.path.join(CSRC, "mhc_kernels.hip"), os.path.join(CSRC, "mhc_bwd.hip"), os.path.join(CSRC, "mhc_post.hip"),
            os.path.join(CSRC, "mhc_scratch.hip"), os.path.join(CSRC, "mhc_ckpt.hip"), os.path.join(CSRC, "mhc_post_bwd.hip"),
-           os.path.join(CSRC, "mhc_glu.hip"),
-           os.path.join(CSRC, "mhc_api.cpp"), os.path.join(CSRC, "mhc_api_train.cpp")]
+           os.path.join(CSRC, "mhc_glu.hip"), os.path.join(CSRC, "mhc_route.hip"), os.path.join(CSRC, "mhc_mxfp4.hip"),
+           os.path.join(CSRC, "mhc_experts.hip"),
+           os.path.join(CSRC, "mhc_api.cpp"), os.path.join(CSRC, "mhc_api_train.cpp"), os.path.join(CSRC, "mhc_api_experts.cpp")]
 # -amdgpu-mfma-vgpr-form=1 keeps matrix-core sources and accumulators in ordinary VGPRs.
 # With the default accumulation-register form, this toolchain's code for the projection
 # kernel produced wrong sums on gfx950 (deterministically, for every schedule tried); the

@@ -1,0 +1,133 @@
+// mhc_experts_plan.h -- geometry, launch shapes and workspace layout of the products with
+// 4-bit weights: y = x w^T, the experts' gated projection, and their projection back.
+//
+// Host-side and plain C++ (no HIP headers), like mhc_plan.h.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "mhc_mxfp4_plan.h"
+
+#ifdef __HIP__
+#define MHC_EXPERTS_HOST_DEVICE __host__ __device__
+#else
+#define MHC_EXPERTS_HOST_DEVICE
+#endif
+
+namespace mhc {
+namespace experts {
+
+constexpr int kMaxE = 1024;
+constexpr int kMaxTopK = 32;
+constexpr int kMaxDim = 65536;        // D, F, K, N
+
+enum Op { kProduct = 0, kGlu = 1, kDown = 2 };
+
+// P rows of results of R values each over a reduction of K. An x row serves `share` result rows (the
+// experts' gated projection: a token's k pairs).
+struct Geometry {
+    int op = 0;
+    int64_t P = 0, X = 0;     // result rows, x rows
+    int E = 1, share = 1;
+    int K = 0, R = 0;
+    int act = 0, f16 = 0;
+    int64_t kb() const { return mx::code_bytes(K); }
+    int64_t sb() const { return mx::scale_bytes(K); }
+};
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// A unit: `rows` weight rows (of the gated projection: of both weights together) and up to `cols`
+// pairs of one expert.
+enum Shape { kSkinny16, kSkinny32, kSkinny64, kSmall, kLarge };
+struct Tiling {
+    int shape = kLarge;
+    int rows = 256, cols = 256, threads = 512;
+    int64_t na = 0;           // units along the weight rows
+    int64_t nb = 0;           // units along the pairs, at most: every expert may end in a part of one
+};
+
+inline Tiling make_tiling(const Geometry& g)
+{
+    Tiling t;
+    const int64_t mean = cdiv(g.P, g.E);
+    if (mean <= 16) t = {kSkinny16, 32, 16, 256};
+    else if (mean <= 32) t = {kSkinny32, 32, 32, 256};
+    else if (mean <= 64) t = {kSkinny64, 32, 64, 256};
+    else {
+        const int64_t rows = g.op == kGlu ? 2 * (int64_t)g.R : g.R;
+        const int64_t nl = cdiv(rows, 256) * (cdiv(g.P, 256) + g.E - 1), ns = cdiv(rows, 128) * (cdiv(g.P, 128) + g.E - 1);
+        if (3 * cdiv(nl, 256) <= 2 * cdiv(ns, 512)) t = {kLarge, 256, 256, 512};
+        else t = {kSmall, 128, 128, 256};
+    }
+    t.na = cdiv(g.op == kGlu ? 2 * (int64_t)g.R : g.R, t.rows);
+    // of the experts' buckets and that of the pairs without one
+    t.nb = g.op == kProduct ? cdiv(g.P, t.cols) : g.P / t.cols + g.E + 1;
+    if (t.nb > g.P) t.nb = g.P;
+    return t;
+}
+
+inline bool valid(const Geometry& g)
+{
+    if (g.P < 0 || g.P > 0x7fffffff || g.X < 0) return false;
+    if (g.E < 1 || g.E > kMaxE || g.share < 1 || g.share > kMaxTopK) return false;
+    if (g.K < 1 || g.K > kMaxDim || g.R < 8 || g.R > kMaxDim || g.R % 8 != 0) return false;
+    if (g.act != 0 && g.act != 1) return false;
+    // x's codes are addressed in 31 bits
+    if (g.X * g.kb() > 0x7fffffff) return false;
+    if (mx::octet_blocks(g.X, g.K) < 0) return false;
+    // the weighted sum: workgroups of 256 threads of eight results
+    if (g.op == kDown && g.P * g.R / 2048 >= 0xffffff) return false;
+    const Tiling t = make_tiling(g);
+    return t.na * t.nb + 8 < (int64_t)1 << 23;     // workgroups of at most 512 threads within a grid's 2^32 - 1
+}
+
+struct Workspace {
+    size_t off_codes = 0, off_scales = 0, off_part = 0, bytes = 0;
+};
+// quantise: x comes in 16 bits
+inline Workspace make_workspace(const Geometry& g, bool quantise)
+{
+    Workspace w;
+    size_t off = 0;
+    w.off_codes = off;
+    if (quantise) off = align_up(off + (size_t)g.X * (size_t)g.kb(), 256);
+    w.off_scales = off;
+    if (quantise) off = align_up(off + (size_t)g.X * (size_t)g.sb(), 256);
+    w.off_part = off;
+    if (g.op == kDown) off = align_up(off + (size_t)g.P * (size_t)g.R * 4, 256);
+    w.bytes = off;
+    return w;
+}
+
+// Unit t of an expert's na x nb units: the pairs of kGroup rows of units before the next rows', so that
+// the units in flight on an XCD share a few operands of either kind in its L2.
+constexpr uint32_t kGroup = 4;
+MHC_EXPERTS_HOST_DEVICE inline void place(uint32_t t, uint32_t na, uint32_t nb, uint32_t* a, uint32_t* b)
+{
+    const uint32_t group = t / (kGroup * nb), r = t - group * kGroup * nb;
+    const uint32_t rows = na - group * kGroup < kGroup ? na - group * kGroup : kGroup;
+    *b = r / rows;
+    *a = group * kGroup + (r - *b * rows);
+}
+
+struct Args {
+    const uint8_t* x_codes;       // [X, kb]
+    const uint8_t* x_scales;      // [X, sb]
+    const uint8_t* w_codes[2];    // [E, R, kb] (the gated projection: gate and up)
+    const uint8_t* w_scales[2];   // [E, R, sb]
+    const int32_t* offsets;       // [E + 1], or NULL: one expert, pair i is row i
+    const int32_t* pairs;         // [P]
+    const float* weights;         // [P] (kDown)
+    void* out;                    // [P, R] 16-bit (kDown: [P / k, R])
+    float* part;                  // kDown: [P, R]
+    int64_t top_k;                // kDown
+};
+
+// Implemented in mhc_experts.hip. Returns 0 or the HIP error code.
+int launch_products(const Geometry& g, const Args& a, void* stream);
+
+}  // namespace experts
+}  // namespace mhc
