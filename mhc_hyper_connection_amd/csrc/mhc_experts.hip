@@ -27,21 +27,29 @@ enum Out { kOutBf16, kOutF16, kOutF32 };
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kLine = 128;            // bytes of a row's codes in a stage: 256 values, 8 scale bytes
 
+// BA, BB: the bytes of sa and sb that hold the scales
+template <int BA, int BB>
 __device__ __forceinline__ f32x4 mfma4(i32x4 a, i32x4 b, f32x4 c, int sa, int sb)
 {
     const i32x4 z = {0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(__builtin_shufflevector(a, z, 0, 1, 2, 3, 4, 5, 6, 7),
                                                             __builtin_shufflevector(b, z, 0, 1, 2, 3, 4, 5, 6, 7),
-                                                            c, 4, 4, 0, sa, 0, sb);
+                                                            c, 4, 4, BA, sa, BB, sb);
 }
 // 64 lanes x 4 bytes from the buffer to LDS at `lds` (lane l to lds + 4 l); as buffer_to_lds.
 __device__ __forceinline__ void word_to_lds(u32x4 desc, uint32_t offset, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(offset), "s"(desc), "s"(lds) : "memory");
 }
+
+template <int N>
+struct Number {
+    static constexpr int value = N;
+};
 
 struct TileArgs {
     Args t;
@@ -167,12 +175,15 @@ __device__ __forceinline__ void store_results(const TileArgs& p, int64_t pair, i
 
 // WA x WB waves of IA x IB 16 x 16 results each; rows: weights (gated: gate and up side by side, so that a wave
 // holds both of the same f), columns: pairs. A stage of the reduction is 256 values: a row's 128 bytes
-// of codes, which direct loads take as whole lines, and two words of scales. LDS holds two stages. A wave's
-// operands of half a stage (128 values, the depth of one matrix instruction) are read while it
+// of codes, which direct loads take as whole lines. LDS holds two stages of them, and the scales of two groups of
+// four stages: 32 bytes of a row at a time, since a row's piece of scales takes a request of its own however short it
+// is (8 bytes at a time, the requests were as many as those of the codes: 860 us instead of 720 at 65536 pairs, D = 4096,
+// F = 2048). A wave's operands of half a stage (128 values, the depth of one matrix instruction) are read while it
 // multiplies the half before:
 //   first half of stage m    read the second half of m
-//   wait for the loads of stage m + 1, meet the other waves (whose reads of stage m are then done)
-//   second half of stage m   read the first half of m + 1, send off the loads of stage m + 2
+//   wait for all loads, meet the other waves (whose reads of stage m are then done)
+//   second half of stage m   read the first half of m + 1, send off the loads of stage m + 2 and (but for the
+//                            group's last stage) a third of those of the next group's scales
 // Loads past the end of the reduction bring zeros.
 template <bool GATED, int OUT, int WA, int WB, int IA, int IB>
 __global__ void __launch_bounds__(64 * WA * WB, WA * WB == 4 && IA * IB == 64 ? 1 : 2)
@@ -180,12 +191,12 @@ tile_kernel(TileArgs p)
 {
     constexpr int NW = WA * WB;
     constexpr int AR = 16 * WA * IA, BC = 16 * WB * IB;
-    constexpr int ASZ = AR * kLine, BSZ = BC * kLine, SSZ = (AR + BC) * 8, STAGE = ASZ + BSZ + SSZ;
-    constexpr int QA = ASZ / 1024 / NW, QB = BSZ / 1024 / NW, QS = SSZ / 256 / NW, Q = QA + QB + QS;
-    static_assert(QA * 1024 * NW == ASZ && QB * 1024 * NW == BSZ && QS * 256 * NW == SSZ, "whole direct loads");
-    static_assert(!GATED || QA % 2 == 0, "a direct load is of one of the two weights");
+    constexpr int ASZ = AR * kLine, BSZ = BC * kLine, STAGE = ASZ + BSZ, GROUP = (AR + BC) * 32;
+    constexpr int QA = ASZ / 1024 / NW, QB = BSZ / 1024 / NW, SA = AR / 8 / NW, SB = BC / 8 / NW;   // a wave's loads; of a group's scales
+    static_assert(QA * 1024 * NW == ASZ && QB * 1024 * NW == BSZ && SA * 8 * NW == AR && SB * 8 * NW == BC, "whole direct loads");
+    static_assert(!GATED || (QA % 2 == 0 && SA % 2 == 0), "a direct load is of one of the two weights");
     static_assert(IA % (GATED ? 4 : 2) == 0, "blocks in pairs");
-    __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE + 2 * GROUP];
 
     Unit u;
     if (!unit_of<BC>(p, &u)) return;
@@ -208,134 +219,150 @@ tile_kernel(TileArgs p)
         const int64_t w0 = u.e * R + a0;
         const u32x4 dc0 = descriptor(p.t.w_codes[0] + w0 * kb, arow * kb);
         const u32x4 dc1 = GATED ? descriptor(p.t.w_codes[1] + w0 * kb, arow * kb) : dc0;
-        // a load of scales is of the weights or of the pairs, and a wave's of one of the two weights
-        static_assert(AR % (32 * NW) == 0 && ROWS % 32 == 0, "loads of one tensor");
-        const u32x4 dsw = descriptor(p.t.w_scales[GATED && (32 * wave) % AR >= ROWS ? 1 : 0] + w0 * sb, arow * sb);
+        const u32x4 ds0 = descriptor(p.t.w_scales[0] + w0 * sb, arow * sb);
+        const u32x4 ds1 = GATED ? descriptor(p.t.w_scales[1] + w0 * sb, arow * sb) : ds0;
         const u32x4 dxc = descriptor(p.t.x_codes, p.x_rows * kb), dxs = descriptor(p.t.x_scales, p.x_rows * sb);
         const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds));
 
-        // --- loads of codes, 1 KiB each: 8 LDS rows of 128 bytes; the 16-byte chunk c of row r sits at
-        // c ^ s(r). Weight rows are read 4 of every 8, with s = 2 ((r / 8) % 4) + (r / 2) % 2, columns 16 in a
-        // run, with s = (r / 2) % 8: either way each of the four turns of a 16-byte read meets all banks once.
-        uint32_t va[QA], vb[QB], vs[QS];
-        uint32_t ka[QA], kx[QB];
+        // --- loads of codes, 1 KiB each: 8 LDS rows of 128 bytes. A lane group kg takes the blocks 2 kg and 2 kg + 1 of a
+        // stage, one in each half, so that their scales are neighbours; the 16-byte chunk c of row r sits at c ^ s(r), where with
+        // the reading lane's number j of 16, s has the bits (j >> 3 ^ j >> 2, j >> 1, j >> 2): each of the four turns of a 16-byte
+        // read (the first of lanes 0-3, 12-15 and 20-27) then meets all banks once.
+        auto swizzle = [](int j) __attribute__((always_inline)) { return (((j >> 3) ^ (j >> 2)) & 1) * 4 + (j & 2) + ((j >> 2) & 1); };
         auto x_row = [=](int c) __attribute__((always_inline)) {
             const int64_t q = pair_of(p, u, c);
             return q < 0 ? -1 : (int)((uint32_t)q / p.share);
         };
+        // the weight rows of a pair of results are 8 (j / 4) + 4 h + j % 4
+        const int r0 = 8 * wave + lane / 8;                      // this lane's row of a wave's first load; the others' have the same swizzle
+        const uint32_t ka = 16 * ((lane & 7) ^ swizzle(((r0 >> 1) & 12) + (r0 & 3))), kx = 16 * ((lane & 7) ^ swizzle(r0 & 15));
+        static_assert(NW % 4 == 0, "rows 32 apart");
+        uint32_t va[QA], vb[QB], vs[SB];
 #pragma unroll
-        for (int q = 0; q < QA; ++q) {
-            const int r = 8 * (wave + NW * q) + lane / 8, c = (lane & 7) ^ (2 * ((r >> 3) & 3) + ((r >> 1) & 1));
-            ka[q] = 16 * c;
-            va[q] = (uint32_t)(r % ROWS) * kb + ka[q];
-        }
+        for (int q = 0; q < QA; ++q) va[q] = (uint32_t)((r0 + 8 * NW * q) % ROWS) * kb + ka;
 #pragma unroll
         for (int q = 0; q < QB; ++q) {
-            const int r = 8 * (wave + NW * q) + lane / 8, c = (lane & 7) ^ ((r >> 1) & 7);
-            const int x = x_row(r);
-            kx[q] = x < 0 ? kb : 16 * c;      // no such column: past the end at once
-            vb[q] = x < 0 ? 0u : (uint32_t)x * kb + kx[q];
+            const int x = x_row(r0 + 8 * NW * q);
+            vb[q] = x < 0 ? kOutOfRange : (uint32_t)x * kb + kx;
+            if (q < SB) vs[q] = x < 0 ? kOutOfRange : (uint32_t)x * sb;
         }
-        // scales, 256 bytes each: 32 rows of two words
-        uint32_t ks[QS];
-#pragma unroll
-        for (int q = 0; q < QS; ++q) {
-            const int r = 32 * (wave + NW * q) + lane / 2;
-            ks[q] = 4 * (lane & 1);
-            if (r < AR) vs[q] = (uint32_t)(r % ROWS) * sb + ks[q];
-            else {
-                const int x = x_row(r - AR);
-                if (x < 0) ks[q] = sb;
-                vs[q] = x < 0 ? 0u : (uint32_t)x * sb + ks[q];
-            }
-        }
+        static_assert(SB == QB && SA == QA, "a load of scales has the rows of one of codes");
+        // scales, 8 rows of 8 words a load; the pair of words of a row's stage n of 4 sits at n ^ (r / 8) % 4, so that the
+        // rows of a block of results, 8 apart or 16 in a run, meet different banks
+        const uint32_t ks = 4 * ((lane & 7) ^ (2 * (wave & 3)));
         // load q of this wave's part of a stage of the weights, of the pairs, of either's scales
         auto issue_a = [=](int step, int slot, int q) __attribute__((always_inline)) {
             const uint32_t k = (uint32_t)step * kLine;
-            buffer_to_lds(!GATED || q < QA / 2 ? dc0 : dc1, k + ka[q] < kb ? va[q] + k : kOutOfRange, lds0 + slot * STAGE + (wave + q * NW) * 1024);
+            buffer_to_lds(!GATED || q < QA / 2 ? dc0 : dc1, k + ka < kb ? va[q] + k : kOutOfRange, lds0 + slot * STAGE + (wave + q * NW) * 1024);
         };
         auto issue_b = [=](int step, int slot, int q) __attribute__((always_inline)) {
             const uint32_t k = (uint32_t)step * kLine;
-            buffer_to_lds(dxc, k + kx[q] < kb ? vb[q] + k : kOutOfRange, lds0 + slot * STAGE + ASZ + (wave + q * NW) * 1024);
+            buffer_to_lds(dxc, k + kx < kb ? vb[q] + k : kOutOfRange, lds0 + slot * STAGE + ASZ + (wave + q * NW) * 1024);
         };
-        auto issue_s = [=](int step, int slot, int q) __attribute__((always_inline)) {
-            const uint32_t s = (uint32_t)step * 8;
-            word_to_lds(q * 32 * NW < AR ? dsw : dxs, s + ks[q] < sb ? vs[q] + s : kOutOfRange, lds0 + slot * STAGE + ASZ + BSZ + (wave + NW * q) * 256);
+        auto issue_s = [=](int group, uint32_t slot, int n) __attribute__((always_inline)) {
+            const uint32_t s = (uint32_t)group * 32 + ks, at = lds0 + 2 * STAGE + slot;
+            if (n < SA) word_to_lds(!GATED || n < SA / 2 ? ds0 : ds1, s < sb ? (uint32_t)((r0 + 8 * NW * n) % ROWS) * sb + s : kOutOfRange, at + (wave + NW * n) * 256);
+            else word_to_lds(dxs, s < sb ? vs[n - SA] + s : kOutOfRange, at + (wave + NW * n) * 256);
         };
 
-        // --- operand reads: lane (j, kg) takes block kg of row j; the weight rows of a pair of results (h =
-        // 0, 1) are 8 (j / 4) + 4 h + j % 4, so that a lane's two results are 8 consecutive rows.
+        // --- operand reads: lane (j, kg) takes block 2 kg + half of row j of each block of 16
         constexpr int WR = GATED ? 16 * IA / 2 : 16 * IA;       // a wave's rows of one weight
         const uint32_t arow0 = (uint32_t)(wa * WR + 8 * (j >> 2) + (j & 3)), brow0 = (uint32_t)(16 * wb * IB + j);
-        const uint32_t aoff = arow0 * kLine + ((kg ^ (j >> 1)) << 4), boff = ASZ + brow0 * kLine + ((kg ^ (j >> 1)) << 4);
-        const uint32_t asc = ASZ + BSZ + arow0 * 8 + kg, bsc = ASZ + BSZ + (AR + brow0) * 8 + kg;
+        const uint32_t chunk = (uint32_t)((2 * kg) ^ swizzle(j)) << 4;
+        const uint32_t aoff = arow0 * kLine + chunk, boff = ASZ + brow0 * kLine + chunk;
+        const uint32_t asc = lds0 + 2 * STAGE + arow0 * 32 + (j >> 2) * 8 + 2 * kg, bsc = lds0 + 2 * STAGE + (AR + brow0) * 32 + (j >> 3) * 8 + 2 * kg;
         struct Operands {
             i32x4 a[IA], b[IB];
-            int sa[IA], sb[IB];
+        };
+        struct Scales {                // of a stage: two bytes, one for each half, of two blocks of results in a word
+            u16x2 a[IA / 2], b[IB / 2];
+        };
+        auto row_of = [](int i) __attribute__((always_inline)) {
+            const int i2 = GATED ? i % (IA / 2) : i;
+            return (GATED && i >= IA / 2 ? ROWS : 0) + (i2 / 2) * 32 + (i2 % 2) * 4;
         };
         auto read_a = [=](int slot, int half, int i, Operands& o) __attribute__((always_inline)) {
-            const int i2 = GATED ? i % (IA / 2) : i, row = (GATED && i >= IA / 2 ? ROWS : 0) + (i2 / 2) * 32 + (i2 % 2) * 4;
-            const uint32_t la = lds0 + slot * STAGE;
-            o.a[i] = *(const MHC_LDS i32x4*)(uintptr_t)(la + (aoff ^ (half << 6)) + row * kLine);
-            o.sa[i] = *(const MHC_LDS uint8_t*)(uintptr_t)(la + asc + half * 4 + row * 8);
+            o.a[i] = *(const MHC_LDS i32x4*)(uintptr_t)(lds0 + slot * STAGE + (aoff ^ (half << 4)) + row_of(i) * kLine);
         };
         auto read_b = [=](int slot, int half, int q, Operands& o) __attribute__((always_inline)) {
-            const uint32_t la = lds0 + slot * STAGE;
-            o.b[q] = *(const MHC_LDS i32x4*)(uintptr_t)(la + (boff ^ (half << 6)) + q * 16 * kLine);
-            o.sb[q] = *(const MHC_LDS uint8_t*)(uintptr_t)(la + bsc + half * 4 + q * 16 * 8);
+            o.b[q] = *(const MHC_LDS i32x4*)(uintptr_t)(lds0 + slot * STAGE + (boff ^ (half << 4)) + q * 16 * kLine);
+        };
+        // of stage n of the group in `slot`
+        auto read_sa = [=](uint32_t slot, int n, int i, Scales& o) __attribute__((always_inline)) {
+            o.a[i / 2][i % 2] = *(const MHC_LDS uint16_t*)(uintptr_t)((asc ^ (n << 3)) + slot + row_of(i) * 32);
+        };
+        auto read_sb = [=](uint32_t slot, int n, int q, Scales& o) __attribute__((always_inline)) {
+            o.b[q / 2][q % 2] = *(const MHC_LDS uint16_t*)(uintptr_t)((bsc ^ ((n ^ 2 * (q & 1)) << 3)) + slot + q * 16 * 32);
         };
 
         const int steps = (int)((kb + kLine - 1) / kLine);
         Operands op[2];
+        Scales sc[2];
+#pragma unroll
+        for (int n = 0; n < SA + SB; ++n) issue_s(0, 0, n);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int q = 0; q < QA; ++q) issue_a(s, s, q);
 #pragma unroll
             for (int q = 0; q < QB; ++q) issue_b(s, s, q);
-#pragma unroll
-            for (int q = 0; q < QS; ++q) issue_s(s, s, q);
         }
-        wait_loads_and_barrier<Q>();
+        wait_loads_and_barrier<QA + QB>();
 #pragma unroll
-        for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]);
+        for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]), read_sb(0, 0, q, sc[0]);
 #pragma unroll
-        for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]);
-        // half h of stage m in slot s: the products of `now` in IA parts, the reads of the next half and the loads
-        // dealt out over them
-        auto half = [&](int m, int s, int h, const Operands& now, Operands& next) __attribute__((always_inline)) {
-            constexpr int READS = IA + IB;
-            const int rs = (s + h) % 2;
+        for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]), read_sa(0, 0, i, sc[0]);
+        // half H2 of stage m = 4 group + n: the products of `now` in IA parts, the reads of the next half (and of the next
+        // stage's scales) and the loads dealt out over them; `slot`: where the next stage's scales are, `other`: the next group's
+        auto half = [&](auto number, int m, int n, const Operands& now, Operands& next, const Scales& sn, Scales& sx, uint32_t slot,
+                        uint32_t other) __attribute__((always_inline)) {
+            constexpr int READS = IA + IB, H2 = decltype(number)::value;
+            const int s = n % 2, rs = (s + H2) % 2;
+            // the next group's scales go with the first three stages: they have to be there when the fourth reads them
+            const int QN = n < 3 ? (n + 1) * (SA + SB) / 3 - n * (SA + SB) / 3 : 0;
 #pragma unroll
             for (int i = 0; i < IA; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = i * READS / IA; r < (i + 1) * READS / IA; ++r) {
-                    if (r < IB) read_b(rs, 1 - h, r, next);
-                    else read_a(rs, 1 - h, r - IB, next);
+                    if (r < IB) {
+                        read_b(rs, 1 - H2, r, next);
+                        if (H2) read_sb(slot, (n + 1) % 4, r, sx);
+                    } else {
+                        read_a(rs, 1 - H2, r - IB, next);
+                        if (H2) read_sa(slot, (n + 1) % 4, r - IB, sx);
+                    }
                 }
+                const int sa = __builtin_bit_cast(int, sn.a[i / 2]);
 #pragma unroll
-                for (int q = 0; q < IB; ++q) acc[i][q] = mfma4(now.a[i], now.b[q], acc[i][q], now.sa[i], now.sb[q]);
+                for (int q = 0; q < IB; ++q) {
+                    const int sb2 = __builtin_bit_cast(int, sn.b[q / 2]);
+                    f32x4& c = acc[i][q];
+                    if (i % 2 == 0) c = q % 2 == 0 ? mfma4<H2, H2>(now.a[i], now.b[q], c, sa, sb2) : mfma4<H2, 2 + H2>(now.a[i], now.b[q], c, sa, sb2);
+                    else c = q % 2 == 0 ? mfma4<2 + H2, H2>(now.a[i], now.b[q], c, sa, sb2) : mfma4<2 + H2, 2 + H2>(now.a[i], now.b[q], c, sa, sb2);
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                if (h == 1) {
+                if (H2 == 1) {
 #pragma unroll
                     for (int q = i * QA / IA; q < (i + 1) * QA / IA; ++q) issue_a(m + 2, s, q);
 #pragma unroll
                     for (int q = i * QB / IA; q < (i + 1) * QB / IA; ++q) issue_b(m + 2, s, q);
 #pragma unroll
-                    for (int q = i * QS / IA; q < (i + 1) * QS / IA; ++q) issue_s(m + 2, s, q);
+                    for (int q = i * QN / IA; q < (i + 1) * QN / IA; ++q) issue_s(m / 4 + 1, other, n * (SA + SB) / 3 + q);
                 }
             }
         };
-        for (int m = 0; m < steps; m += 2) {
+        uint32_t slot = 0;
+        for (int m = 0; m < steps; m += 4) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (m + s < steps) {
-                    half(m + s, s, 0, op[0], op[1]);
+            for (int n = 0; n < 4; ++n) {
+                if (m + n < steps) {
+                    half(Number<0>{}, m + n, n, op[0], op[1], sc[n % 2], sc[1 - n % 2], slot, slot ^ GROUP);
                     wait_loads_and_barrier<0>();
-                    half(m + s, s, 1, op[1], op[0]);
+                    half(Number<1>{}, m + n, n, op[1], op[0], sc[n % 2], sc[1 - n % 2], n == 3 ? slot ^ GROUP : slot, slot ^ GROUP);
                 }
             }
+            slot ^= GROUP;
         }
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // no load is left behind in LDS at the end
     }
@@ -460,8 +487,8 @@ skinny_kernel(TileArgs p)
                         for (int n = 0; n < NT; ++n) {
                             const i32x4 x = *(const MHC_LDS i32x4*)(uintptr_t)(at + (32 + 16 * n) * kLine);
                             const int sx = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 256 + n * 128);
-                            acc[0][n] = mfma4(w0v, x, acc[0][n], s0, sx);
-                            acc[1][n] = mfma4(w1v, x, acc[1][n], s1, sx);
+                            acc[0][n] = mfma4<0, 0>(w0v, x, acc[0][n], s0, sx);
+                            acc[1][n] = mfma4<0, 0>(w1v, x, acc[1][n], s1, sx);
                         }
                     }
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // read, before the slot is loaded again
