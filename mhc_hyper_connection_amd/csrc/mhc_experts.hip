@@ -27,7 +27,6 @@ enum Out { kOutBf16, kOutF16, kOutF32 };
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kLine = 128;            // bytes of a row's codes in a stage: 256 values, 8 scale bytes
 
@@ -46,6 +45,13 @@ __device__ __forceinline__ void word_to_lds(u32x4 desc, uint32_t offset, uint32_
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(offset), "s"(desc), "s"(lds) : "memory");
 }
 
+// wait_loads_and_barrier<0>, without the wait for memory where m is 0. In one piece: a branch that the compiler sees
+// would split the loop's body, and the registers would no longer do.
+__device__ __forceinline__ void wait_unless_zero_and_barrier(int m)
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lmeet%=\n\ts_waitcnt vmcnt(0)\n.Lmeet%=:\n\ts_barrier" : : "s"(m) : "scc", "memory");
+}
+
 template <int N>
 struct Number {
     static constexpr int value = N;
@@ -60,8 +66,8 @@ struct TileArgs {
     uint32_t x_rows;
 };
 
-// The unit of this workgroup: of expert e the units' row a and the pairs [first, first + cols). An
-// XCD (workgroups b, b + 8, ..) takes a contiguous run of the units. The experts' buckets are counted from the plan's
+// A unit: of expert e the units' row a and the pairs [first, first + cols). An XCD (workgroups b, b + 8, ..) takes a
+// contiguous run of the units, each of its workgroups every so many of them. The experts' buckets are counted from the plan's
 // offsets, which are bounded here: whatever they hold, pairs stay in [0, P).
 struct Unit {
     int e;
@@ -69,80 +75,78 @@ struct Unit {
     int64_t first;
     int cols;
 };
-template <int BC>
-__device__ __forceinline__ bool find_unit(const TileArgs& p, Unit* u)
+// The same in every lane: to a scalar register, which the direct loads' descriptors have to be in.
+__device__ __forceinline__ int scalar(int x)
 {
-    const int lane = threadIdx.x & 63;
-    const uint32_t xcd = blockIdx.x % 8, i = blockIdx.x / 8;
-    auto bucket = [&](int e, int64_t* begin, int64_t* end) {
-        const int64_t b = e <= p.E ? p.t.offsets[e] : p.P, n = e < p.E ? p.t.offsets[e + 1] : p.P;
-        *begin = b < 0 ? 0 : (b > p.P ? p.P : b);
-        *end = n < *begin ? *begin : (n > p.P ? p.P : n);
-        return (int)((*end - *begin + BC - 1) / BC);
-    };
-    int64_t begin, end;
-    uint32_t total = 0, nb, at;
-    if (!p.t.offsets) {
-        total = (uint32_t)((p.P + BC - 1) / BC);
-    } else {
-        for (int e0 = 0; e0 <= p.E; e0 += 64) {
-            int n = bucket(e0 + lane, &begin, &end);
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-            total += (uint32_t)__builtin_amdgcn_readfirstlane(n);
-        }
-    }
-    const uint32_t units = total * p.na, per = (units + 7) / 8, unit = xcd * per + i;
-    if (i >= per || unit >= units) return false;
-    uint32_t b;
-    if (!p.t.offsets) {
-        place(unit, p.na, total, &u->a, &b);
-        u->e = 0;
-        u->first = (int64_t)b * BC;
-        u->cols = (int)(p.P - u->first < BC ? p.P - u->first : BC);
-        return true;
-    }
-    const uint32_t q = unit / p.na;
-    at = 0;
-    for (int e0 = 0; e0 <= p.E; e0 += 64) {
-        const int n = bucket(e0 + lane, &begin, &end);
-        int scan = n;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(scan, d);
-            if (lane >= d) scan += o;
-        }
-        const uint64_t past = __ballot(q < at + (uint32_t)scan);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            nb = (uint32_t)__builtin_amdgcn_readlane(n, l);
-            at += (uint32_t)(__builtin_amdgcn_readlane(scan, l) - (int)nb);
-            const int b0 = __builtin_amdgcn_readlane((int)begin, l), b1 = __builtin_amdgcn_readlane((int)end, l);
-            place(unit - at * p.na, p.na, nb, &u->a, &b);
-            u->e = e0 + l;
-            u->first = b0 + (int64_t)b * BC;
-            u->cols = (int)(b1 - u->first < BC ? b1 - u->first : BC);
-            return true;
-        }
-        at += (uint32_t)__builtin_amdgcn_readlane(scan, 63);
-    }
-    return false;
+    int s;
+    asm volatile("s_nop 1\n\tv_readfirstlane_b32 %0, %1" : "=s"(s) : "v"(x));
+    return s;
+}
+// A bucket's first and last pair and its units of BC pairs; bucket E: the pairs without an expert.
+template <int BC>
+__device__ __forceinline__ int bucket(const TileArgs& p, int e, int* begin, int* end)
+{
+    const int P = (int)p.P;
+    const int b = e <= p.E ? p.t.offsets[e] : P, n = e < p.E ? p.t.offsets[e + 1] : P;
+    *begin = b < 0 ? 0 : (b > P ? P : b);
+    *end = n < *begin ? *begin : (n > P ? P : n);
+    return (int)(((int64_t)*end - *begin + BC - 1) / BC);
 }
 template <int BC>
-__device__ __forceinline__ bool unit_of(const TileArgs& p, Unit* u)
+__device__ __forceinline__ uint32_t count_units(const TileArgs& p)   // along the pairs
 {
-    Unit v = {0, 0, 0, 0};
-    if (!find_unit<BC>(p, &v)) return false;
-    // the same in every lane: to scalar registers, which the direct loads' descriptors have to be in
-    auto scalar = [](int x) {
-        int s;
-        asm volatile("s_nop 1\n\tv_readfirstlane_b32 %0, %1" : "=s"(s) : "v"(x));
-        return s;
-    };
-    u->e = scalar(v.e);
-    u->a = (uint32_t)scalar((int)v.a);
-    u->first = (int64_t)(uint32_t)scalar((int)v.first);    // under 2^31
-    u->cols = scalar(v.cols);
+    if (!p.t.offsets) return (uint32_t)((p.P + BC - 1) / BC);
+    const int lane = threadIdx.x & 63;
+    uint32_t total = 0;
+    for (int e0 = 0; e0 <= p.E; e0 += 64) {
+        int begin, end, n = bucket<BC>(p, e0 + lane, &begin, &end);
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+        total += (uint32_t)__builtin_amdgcn_readfirstlane(n);
+    }
+    return total;
+}
+// Unit i of this workgroup's XCD, of total x na in all; false past the last.
+template <int BC>
+__device__ __forceinline__ bool unit_of(const TileArgs& p, uint32_t total, uint32_t i, Unit* u)
+{
+    const int lane = threadIdx.x & 63;
+    const uint32_t units = total * p.na, per = (units + 7) / 8, unit = blockIdx.x % 8 * per + i;
+    if (i >= per || unit >= units) return false;
+    uint32_t a = 0, b = 0;
+    int e = 0, b0 = 0, b1 = (int)p.P;
+    if (!p.t.offsets) place(unit, p.na, total, &a, &b);
+    else {
+        const uint32_t q = unit / p.na;
+        uint32_t at = 0;
+        for (int e0 = 0; e0 <= p.E; e0 += 64) {
+            int begin, end;
+            const int n = bucket<BC>(p, e0 + lane, &begin, &end);
+            int scan = n;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(scan, d);
+                if (lane >= d) scan += o;
+            }
+            const uint64_t past = __ballot(q < at + (uint32_t)scan);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                const uint32_t nb = (uint32_t)__builtin_amdgcn_readlane(n, l);
+                at += (uint32_t)(__builtin_amdgcn_readlane(scan, l) - (int)nb);
+                b0 = __builtin_amdgcn_readlane(begin, l);
+                b1 = __builtin_amdgcn_readlane(end, l);
+                place(unit - at * p.na, p.na, nb, &a, &b);
+                e = e0 + l;
+                break;
+            }
+            at += (uint32_t)__builtin_amdgcn_readlane(scan, 63);
+        }
+    }
+    const int64_t first = b0 + (int64_t)b * BC;
+    u->e = scalar(e);
+    u->a = (uint32_t)scalar((int)a);
+    u->first = (int64_t)(uint32_t)scalar((int)first);    // under 2^31
+    u->cols = scalar((int)(b1 - first < BC ? b1 - first : BC));
     return true;
 }
 // The pair in column c of the unit; -1 past its columns (and for what is no pair).
@@ -198,202 +202,283 @@ tile_kernel(TileArgs p)
     static_assert(IA % (GATED ? 4 : 2) == 0, "blocks in pairs");
     __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE + 2 * GROUP];
 
-    Unit u;
-    if (!unit_of<BC>(p, &u)) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wa = wave / WB, wb = wave % WB;
     const int j = lane & 15, kg = lane >> 4;
     const uint32_t kb = p.kb, sb = p.sb;
+    const int64_t R = p.R;
     constexpr int ROWS = GATED ? AR / 2 : AR;                    // of one weight
-    const int64_t a0 = (int64_t)u.a * ROWS, R = p.R;
-    const uint32_t arow = (uint32_t)(R - a0 < ROWS ? R - a0 : ROWS);
-    const bool routed = u.e < p.E;
+    const u32x4 dxc = descriptor(p.t.x_codes, p.x_rows * kb), dxs = descriptor(p.t.x_scales, p.x_rows * sb);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds));
 
-    f32x4 acc[IA][IB];
-#pragma unroll
-    for (int i = 0; i < IA; ++i)
-#pragma unroll
-        for (int q = 0; q < IB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    if (routed) {
-        const int64_t w0 = u.e * R + a0;
-        const u32x4 dc0 = descriptor(p.t.w_codes[0] + w0 * kb, arow * kb);
-        const u32x4 dc1 = GATED ? descriptor(p.t.w_codes[1] + w0 * kb, arow * kb) : dc0;
-        const u32x4 ds0 = descriptor(p.t.w_scales[0] + w0 * sb, arow * sb);
-        const u32x4 ds1 = GATED ? descriptor(p.t.w_scales[1] + w0 * sb, arow * sb) : ds0;
-        const u32x4 dxc = descriptor(p.t.x_codes, p.x_rows * kb), dxs = descriptor(p.t.x_scales, p.x_rows * sb);
-        const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds));
-
-        // --- loads of codes, 1 KiB each: 8 LDS rows of 128 bytes. A lane group kg takes the blocks 2 kg and 2 kg + 1 of a
-        // stage, one in each half, so that their scales are neighbours; the 16-byte chunk c of row r sits at c ^ s(r), where with
-        // the reading lane's number j of 16, s has the bits (j >> 3 ^ j >> 2, j >> 1, j >> 2): each of the four turns of a 16-byte
-        // read (the first of lanes 0-3, 12-15 and 20-27) then meets all banks once.
-        auto swizzle = [](int j) __attribute__((always_inline)) { return (((j >> 3) ^ (j >> 2)) & 1) * 4 + (j & 2) + ((j >> 2) & 1); };
-        auto x_row = [=](int c) __attribute__((always_inline)) {
-            const int64_t q = pair_of(p, u, c);
-            return q < 0 ? -1 : (int)((uint32_t)q / p.share);
-        };
-        // the weight rows of a pair of results are 8 (j / 4) + 4 h + j % 4
-        const int r0 = 8 * wave + lane / 8;                      // this lane's row of a wave's first load; the others' have the same swizzle
-        const uint32_t ka = 16 * ((lane & 7) ^ swizzle(((r0 >> 1) & 12) + (r0 & 3))), kx = 16 * ((lane & 7) ^ swizzle(r0 & 15));
-        static_assert(NW % 4 == 0, "rows 32 apart");
-        uint32_t va[QA], vb[QB], vs[SB];
-#pragma unroll
-        for (int q = 0; q < QA; ++q) va[q] = (uint32_t)((r0 + 8 * NW * q) % ROWS) * kb + ka;
+    // --- loads of codes, 1 KiB each: 8 LDS rows of 128 bytes. A lane group kg takes the blocks 2 kg and 2 kg + 1 of a
+    // stage, one in each half, so that their scales are neighbours; the 16-byte chunk c of row r sits at c ^ s(r), where with
+    // the reading lane's number j of 16, s has the bits (j >> 3 ^ j >> 2, j >> 1, j >> 2): each of the four turns of a 16-byte
+    // read (the first of lanes 0-3, 12-15 and 20-27) then meets all banks once.
+    auto swizzle = [](int j) __attribute__((always_inline)) { return (((j >> 3) ^ (j >> 2)) & 1) * 4 + (j & 2) + ((j >> 2) & 1); };
+    // the weight rows of a pair of results are 8 (j / 4) + 4 h + j % 4
+    const int r0 = 8 * wave + lane / 8;                      // this lane's row of a wave's first load; the others' have the same swizzle
+    const uint32_t ka = 16 * ((lane & 7) ^ swizzle(((r0 >> 1) & 12) + (r0 & 3))), kx = 16 * ((lane & 7) ^ swizzle(r0 & 15));
+    static_assert(NW % 4 == 0 && ROWS % (8 * NW) == 0, "rows 32 apart, and a load within one weight");
+    // scales, 8 rows of 8 words a load; the pair of words of a row's stage n of 4 sits at n ^ (r / 8) % 4, so that the
+    // rows of a block of results, 8 apart or 16 in a run, meet different banks
+    const uint32_t ks = 4 * ((lane & 7) ^ (2 * (wave & 3)));
+    // where a unit's loads begin
+    struct Loads {
+        u32x4 dc0, dc1, ds0, ds1;
+        uint32_t vb[QB], vs[SB];
+    };
+    const uint32_t va = (uint32_t)r0 * kb + ka, vsa = (uint32_t)r0 * sb + ks;
+    static_assert(SB == QB && SA == QA, "a load of scales has the rows of one of codes");
+    // ln: the lane, hidden from the compiler, which would keep all that follows from it through the products
+    auto set_up = [=](int ln, const Unit& u, Loads& l) __attribute__((always_inline)) {
+        const int64_t a0 = (int64_t)u.a * ROWS, w0 = u.e * R + a0;
+        const uint32_t arow = (uint32_t)(R - a0 < ROWS ? R - a0 : ROWS);
+        l.dc0 = descriptor(p.t.w_codes[0] + w0 * kb, arow * kb);
+        l.dc1 = GATED ? descriptor(p.t.w_codes[1] + w0 * kb, arow * kb) : l.dc0;
+        l.ds0 = descriptor(p.t.w_scales[0] + w0 * sb, arow * sb);
+        l.ds1 = GATED ? descriptor(p.t.w_scales[1] + w0 * sb, arow * sb) : l.ds0;
+        const int r0 = 8 * wave + ln / 8;
+        const uint32_t kx = 16 * ((ln & 7) ^ swizzle(r0 & 15));
 #pragma unroll
         for (int q = 0; q < QB; ++q) {
-            const int x = x_row(r0 + 8 * NW * q);
-            vb[q] = x < 0 ? kOutOfRange : (uint32_t)x * kb + kx;
-            if (q < SB) vs[q] = x < 0 ? kOutOfRange : (uint32_t)x * sb;
+            const int64_t pair = pair_of(p, u, r0 + 8 * NW * q);
+            const uint32_t x = pair < 0 ? 0u : (uint32_t)pair / p.share;
+            l.vb[q] = pair < 0 ? kOutOfRange : x * kb + kx;
+            l.vs[q] = pair < 0 ? kOutOfRange : x * sb + ks;
         }
-        static_assert(SB == QB && SA == QA, "a load of scales has the rows of one of codes");
-        // scales, 8 rows of 8 words a load; the pair of words of a row's stage n of 4 sits at n ^ (r / 8) % 4, so that the
-        // rows of a block of results, 8 apart or 16 in a run, meet different banks
-        const uint32_t ks = 4 * ((lane & 7) ^ (2 * (wave & 3)));
-        // load q of this wave's part of a stage of the weights, of the pairs, of either's scales
-        auto issue_a = [=](int step, int slot, int q) __attribute__((always_inline)) {
-            const uint32_t k = (uint32_t)step * kLine;
-            buffer_to_lds(!GATED || q < QA / 2 ? dc0 : dc1, k + ka < kb ? va[q] + k : kOutOfRange, lds0 + slot * STAGE + (wave + q * NW) * 1024);
-        };
-        auto issue_b = [=](int step, int slot, int q) __attribute__((always_inline)) {
-            const uint32_t k = (uint32_t)step * kLine;
-            buffer_to_lds(dxc, k + kx < kb ? vb[q] + k : kOutOfRange, lds0 + slot * STAGE + ASZ + (wave + q * NW) * 1024);
-        };
-        auto issue_s = [=](int group, uint32_t slot, int n) __attribute__((always_inline)) {
-            const uint32_t s = (uint32_t)group * 32 + ks, at = lds0 + 2 * STAGE + slot;
-            if (n < SA) word_to_lds(!GATED || n < SA / 2 ? ds0 : ds1, s < sb ? (uint32_t)((r0 + 8 * NW * n) % ROWS) * sb + s : kOutOfRange, at + (wave + NW * n) * 256);
-            else word_to_lds(dxs, s < sb ? vs[n - SA] + s : kOutOfRange, at + (wave + NW * n) * 256);
-        };
+    };
+    // where this wave's loads go
+    const uint32_t codes_at = (uint32_t)scalar((int)(lds0 + wave * 1024)), scales_at = (uint32_t)scalar((int)(lds0 + 2 * STAGE + wave * 256));
+    // hidden anew at each use from the compiler, which would keep the sums with every slot and load, in more registers than there are
+    auto hidden = [](uint32_t v) __attribute__((always_inline)) {
+        asm volatile("" : "+s"(v));
+        return v;
+    };
+    // load q of this wave's part of a stage of the weights, of the pairs, of either's scales
+    auto issue_a = [=](const Loads& l, int step, int slot, int q) __attribute__((always_inline)) {
+        const uint32_t k = hidden((uint32_t)step * kLine);
+        buffer_to_lds(!GATED || q < QA / 2 ? l.dc0 : l.dc1, k + ka < kb ? va + (k + (8 * NW * q) % ROWS * kb) : kOutOfRange, hidden(codes_at) + slot * STAGE + q * NW * 1024);
+    };
+    auto issue_b = [=](const Loads& l, int step, int slot, int q) __attribute__((always_inline)) {
+        const uint32_t k = hidden((uint32_t)step * kLine);
+        buffer_to_lds(dxc, k + kx < kb ? l.vb[q] + k : kOutOfRange, hidden(codes_at) + slot * STAGE + ASZ + q * NW * 1024);
+    };
+    auto issue_s = [=](const Loads& l, int group, uint32_t slot, int n) __attribute__((always_inline)) {
+        const uint32_t s = hidden((uint32_t)group * 32), at = hidden(scales_at) + slot;
+        if (n < SA) word_to_lds(!GATED || n < SA / 2 ? l.ds0 : l.ds1, s + ks < sb ? vsa + (s + (8 * NW * n) % ROWS * sb) : kOutOfRange, at + NW * n * 256);
+        else word_to_lds(dxs, s + ks < sb ? l.vs[n - SA] + s : kOutOfRange, at + NW * n * 256);
+    };
 
-        // --- operand reads: lane (j, kg) takes block 2 kg + half of row j of each block of 16
-        constexpr int WR = GATED ? 16 * IA / 2 : 16 * IA;       // a wave's rows of one weight
-        const uint32_t arow0 = (uint32_t)(wa * WR + 8 * (j >> 2) + (j & 3)), brow0 = (uint32_t)(16 * wb * IB + j);
-        const uint32_t chunk = (uint32_t)((2 * kg) ^ swizzle(j)) << 4;
-        const uint32_t aoff = arow0 * kLine + chunk, boff = ASZ + brow0 * kLine + chunk;
-        const uint32_t asc = lds0 + 2 * STAGE + arow0 * 32 + (j >> 2) * 8 + 2 * kg, bsc = lds0 + 2 * STAGE + (AR + brow0) * 32 + (j >> 3) * 8 + 2 * kg;
-        struct Operands {
-            i32x4 a[IA], b[IB];
-        };
-        struct Scales {                // of a stage: two bytes, one for each half, of two blocks of results in a word
-            u16x2 a[IA / 2], b[IB / 2];
-        };
-        auto row_of = [](int i) __attribute__((always_inline)) {
-            const int i2 = GATED ? i % (IA / 2) : i;
-            return (GATED && i >= IA / 2 ? ROWS : 0) + (i2 / 2) * 32 + (i2 % 2) * 4;
-        };
-        auto read_a = [=](int slot, int half, int i, Operands& o) __attribute__((always_inline)) {
-            o.a[i] = *(const MHC_LDS i32x4*)(uintptr_t)(lds0 + slot * STAGE + (aoff ^ (half << 4)) + row_of(i) * kLine);
-        };
-        auto read_b = [=](int slot, int half, int q, Operands& o) __attribute__((always_inline)) {
-            o.b[q] = *(const MHC_LDS i32x4*)(uintptr_t)(lds0 + slot * STAGE + (boff ^ (half << 4)) + q * 16 * kLine);
-        };
-        // of stage n of the group in `slot`
-        auto read_sa = [=](uint32_t slot, int n, int i, Scales& o) __attribute__((always_inline)) {
-            o.a[i / 2][i % 2] = *(const MHC_LDS uint16_t*)(uintptr_t)((asc ^ (n << 3)) + slot + row_of(i) * 32);
-        };
-        auto read_sb = [=](uint32_t slot, int n, int q, Scales& o) __attribute__((always_inline)) {
-            o.b[q / 2][q % 2] = *(const MHC_LDS uint16_t*)(uintptr_t)((bsc ^ ((n ^ 2 * (q & 1)) << 3)) + slot + q * 16 * 32);
-        };
+    // --- operand reads: lane (j, kg) takes block 2 kg + half of row j of each block of 16
+    constexpr int WR = GATED ? 16 * IA / 2 : 16 * IA;       // a wave's rows of one weight
+    const uint32_t arow0 = (uint32_t)(wa * WR + 8 * (j >> 2) + (j & 3)), brow0 = (uint32_t)(16 * wb * IB + j);
+    const uint32_t chunk = (uint32_t)((2 * kg) ^ swizzle(j)) << 4;
+    const uint32_t aoff = arow0 * kLine + chunk, boff = ASZ + brow0 * kLine + chunk;
+    const uint32_t asc = lds0 + 2 * STAGE + arow0 * 32 + (j >> 2) * 8 + 2 * kg, bsc = lds0 + 2 * STAGE + (AR + brow0) * 32 + (j >> 3) * 8 + 2 * kg;
+    struct Operands {
+        i32x4 a[IA], b[IB];
+    };
+    struct Scales {                // of a stage: two bytes, one for each half
+        int a[IA], b[IB];
+    };
+    struct Pairs {                 // those of two blocks of results in a word
+        int a[IA / 2], b[IB / 2];
+    };
+    auto row_of = [](int i) __attribute__((always_inline)) {
+        const int i2 = GATED ? i % (IA / 2) : i;
+        return (GATED && i >= IA / 2 ? ROWS : 0) + (i2 / 2) * 32 + (i2 % 2) * 4;
+    };
+    auto read_a = [=](int slot, int half, int i, Operands& o) __attribute__((always_inline)) {
+        o.a[i] = *(const MHC_LDS i32x4*)(uintptr_t)(lds0 + slot * STAGE + (aoff ^ (half << 4)) + row_of(i) * kLine);
+    };
+    auto read_b = [=](int slot, int half, int q, Operands& o) __attribute__((always_inline)) {
+        o.b[q] = *(const MHC_LDS i32x4*)(uintptr_t)(lds0 + slot * STAGE + (boff ^ (half << 4)) + q * 16 * kLine);
+    };
+    // of stage n of the group in `slot`
+    auto read_sa = [=](uint32_t slot, int n, int i, Scales& o) __attribute__((always_inline)) {
+        o.a[i] = *(const MHC_LDS uint16_t*)(uintptr_t)((asc ^ (n << 3)) + slot + row_of(i) * 32);
+    };
+    auto read_sb = [=](uint32_t slot, int n, int q, Scales& o) __attribute__((always_inline)) {
+        o.b[q] = *(const MHC_LDS uint16_t*)(uintptr_t)((bsc ^ ((n ^ 2 * (q & 1)) << 3)) + slot + q * 16 * 32);
+    };
 
-        const int steps = (int)((kb + kLine - 1) / kLine);
-        Operands op[2];
-        Scales sc[2];
+    // a unit's first loads: its first group of scales and two stages
+    auto first_loads = [=](const Loads& l) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < SA + SB; ++n) issue_s(0, 0, n);
+        for (int n = 0; n < SA + SB; ++n) issue_s(l, 0, 0, n);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int q = 0; q < QA; ++q) issue_a(s, s, q);
+            for (int q = 0; q < QA; ++q) issue_a(l, s, s, q);
 #pragma unroll
-            for (int q = 0; q < QB; ++q) issue_b(s, s, q);
+            for (int q = 0; q < QB; ++q) issue_b(l, s, s, q);
         }
-        wait_loads_and_barrier<QA + QB>();
+    };
+
+    const int steps = (int)((kb + kLine - 1) / kLine);
+    const uint32_t total = (uint32_t)scalar((int)count_units<BC>(p));
+    uint32_t i0 = blockIdx.x / 8;
+    Unit u, next;
+    if (!unit_of<BC>(p, total, i0, &u)) return;
+    Loads l;
+    if (u.e < p.E) {
+        set_up(lane, u, l);
+        first_loads(l);
+    }
+    wait_loads_and_barrier<GATED ? QA + QB : 0>();
+    while (true) {
+        f32x4 acc[IA][IB];
 #pragma unroll
-        for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]), read_sb(0, 0, q, sc[0]);
+        for (int i = 0; i < IA; ++i)
 #pragma unroll
-        for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]), read_sa(0, 0, i, sc[0]);
-        // half H2 of stage m = 4 group + n: the products of `now` in IA parts, the reads of the next half (and of the next
-        // stage's scales) and the loads dealt out over them; `slot`: where the next stage's scales are, `other`: the next group's
-        auto half = [&](auto number, int m, int n, const Operands& now, Operands& next, const Scales& sn, Scales& sx, uint32_t slot,
-                        uint32_t other) __attribute__((always_inline)) {
-            constexpr int READS = IA + IB, H2 = decltype(number)::value;
-            const int s = n % 2, rs = (s + H2) % 2;
-            // the next group's scales go with the first three stages: they have to be there when the fourth reads them
-            const int QN = n < 3 ? (n + 1) * (SA + SB) / 3 - n * (SA + SB) / 3 : 0;
+            for (int q = 0; q < IB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        bool more = false;
+        if constexpr (!GATED) {
+            i0 += gridDim.x / 8;
+            more = unit_of<BC>(p, total, i0, &next);             // while this unit's first loads are on their way
+        }
+
+        if (u.e < p.E) {
+            Operands op[2];
+            Scales sc;
+            Pairs sp;
 #pragma unroll
-            for (int i = 0; i < IA; ++i) {
-                __builtin_amdgcn_sched_barrier(0);
+            for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]), read_sb(0, 0, q, sc);
 #pragma unroll
-                for (int r = i * READS / IA; r < (i + 1) * READS / IA; ++r) {
-                    if (r < IB) {
-                        read_b(rs, 1 - H2, r, next);
-                        if (H2) read_sb(slot, (n + 1) % 4, r, sx);
-                    } else {
-                        read_a(rs, 1 - H2, r - IB, next);
-                        if (H2) read_sa(slot, (n + 1) % 4, r - IB, sx);
+            for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]), read_sa(0, 0, i, sc);
+            // half H2 of stage m = 4 group + n: the products of `now` in IA parts, the reads of the next half (and of the next
+            // stage's scales) and the loads dealt out over them; `slot`: where the next stage's scales are, `other`: the next group's
+            auto half = [&](auto number, int m, int n, const Operands& now, Operands& next, uint32_t slot,
+                            uint32_t other) __attribute__((always_inline)) {
+                constexpr int READS = IA + IB, H2 = decltype(number)::value;
+                const int s = n % 2, rs = (s + H2) % 2;
+                // the next group's scales go with the first three stages: they have to be there when the fourth reads them
+                const int QN = n < 3 ? (n + 1) * (SA + SB) / 3 - n * (SA + SB) / 3 : 0;
+#pragma unroll
+                for (int i = 0; i < IA; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int r = i * READS / IA; r < (i + 1) * READS / IA; ++r) {
+                        if (r < IB) {
+                            read_b(rs, 1 - H2, r, next);
+                            if (H2) read_sb(slot, (n + 1) % 4, r, sc);
+                        } else {
+                            read_a(rs, 1 - H2, r - IB, next);
+                            if (H2) read_sa(slot, (n + 1) % 4, r - IB, sc);
+                        }
+                    }
+                    if (!H2) {     // the scales read in the half before
+                        if (i % 2 == 0) sp.a[i / 2] = sc.a[i] | sc.a[i + 1] << 16;
+#pragma unroll
+                        for (int q = 0; q < (i == 0 ? IB : 0); q += 2) sp.b[q / 2] = sc.b[q] | sc.b[q + 1] << 16;
+                    }
+                    const int sa = sp.a[i / 2];
+#pragma unroll
+                    for (int q = 0; q < IB; ++q) {
+                        const int sb2 = sp.b[q / 2];
+                        f32x4& c = acc[i][q];
+                        if (i % 2 == 0) c = q % 2 == 0 ? mfma4<H2, H2>(now.a[i], now.b[q], c, sa, sb2) : mfma4<H2, 2 + H2>(now.a[i], now.b[q], c, sa, sb2);
+                        else c = q % 2 == 0 ? mfma4<2 + H2, H2>(now.a[i], now.b[q], c, sa, sb2) : mfma4<2 + H2, 2 + H2>(now.a[i], now.b[q], c, sa, sb2);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (H2 == 1) {
+#pragma unroll
+                        for (int q = i * QA / IA; q < (i + 1) * QA / IA; ++q) issue_a(l, m + 2, s, q);
+#pragma unroll
+                        for (int q = i * QB / IA; q < (i + 1) * QB / IA; ++q) issue_b(l, m + 2, s, q);
+#pragma unroll
+                        for (int q = i * QN / IA; q < (i + 1) * QN / IA; ++q) issue_s(l, m / 4 + 1, other, n * (SA + SB) / 3 + q);
                     }
                 }
-                const int sa = __builtin_bit_cast(int, sn.a[i / 2]);
+            };
+            uint32_t slot = 0;
+            for (int m = 0; m < steps; m += 4) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    if (m + n < steps) {
+                        half(Number<0>{}, m + n, n, op[0], op[1], slot, slot ^ GROUP);
+                        // stage 1 is there from before; the last unit's stores may still be on their way
+                        if (!GATED && n == 0) wait_unless_zero_and_barrier(m);
+                        else wait_loads_and_barrier<0>();
+                        half(Number<1>{}, m + n, n, op[1], op[0], n == 3 ? slot ^ GROUP : slot, slot ^ GROUP);
+                    }
+                }
+                slot ^= GROUP;
+            }
+            wait_loads_and_barrier<0>();   // no load is left behind in LDS, and every wave has read it
+        }
+
+        // --- results: lane (j, kg) holds rows 4 kg .. 4 kg + 3 of column j of each 16 x 16 block: 8 kg .. 8 kg + 7 of the 32 rows of
+        // a pair of blocks
+        const int64_t a0 = (int64_t)u.a * ROWS + wa * WR;        // the wave's first row
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        if constexpr (GATED) {
+            auto results = [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
                 for (int q = 0; q < IB; ++q) {
-                    const int sb2 = __builtin_bit_cast(int, sn.b[q / 2]);
-                    f32x4& c = acc[i][q];
-                    if (i % 2 == 0) c = q % 2 == 0 ? mfma4<H2, H2>(now.a[i], now.b[q], c, sa, sb2) : mfma4<H2, 2 + H2>(now.a[i], now.b[q], c, sa, sb2);
-                    else c = q % 2 == 0 ? mfma4<2 + H2, H2>(now.a[i], now.b[q], c, sa, sb2) : mfma4<2 + H2, 2 + H2>(now.a[i], now.b[q], c, sa, sb2);
+                    const int64_t pair = pair_of(p, u, 16 * (wb * IB + q) + j);
+#pragma unroll
+                    for (int i = 0; i < IA / 4; ++i) {
+                        const int64_t f = a0 + 32 * i + 8 * kg;
+                        float v[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            v[r] = activation<decltype(act)::value>(acc[2 * i + r / 4][q][r % 4]).a * acc[IA / 2 + 2 * i + r / 4][q][r % 4];
+                        if (pair >= 0 && f < R) store_results<OUT>(p, pair, f, v);
+                    }
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                if (H2 == 1) {
-#pragma unroll
-                    for (int q = i * QA / IA; q < (i + 1) * QA / IA; ++q) issue_a(m + 2, s, q);
-#pragma unroll
-                    for (int q = i * QB / IA; q < (i + 1) * QB / IA; ++q) issue_b(m + 2, s, q);
-#pragma unroll
-                    for (int q = i * QN / IA; q < (i + 1) * QN / IA; ++q) issue_s(m / 4 + 1, other, n * (SA + SB) / 3 + q);
-                }
-            }
-        };
-        uint32_t slot = 0;
-        for (int m = 0; m < steps; m += 4) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                if (m + n < steps) {
-                    half(Number<0>{}, m + n, n, op[0], op[1], sc[n % 2], sc[1 - n % 2], slot, slot ^ GROUP);
-                    wait_loads_and_barrier<0>();
-                    half(Number<1>{}, m + n, n, op[1], op[0], sc[n % 2], sc[1 - n % 2], n == 3 ? slot ^ GROUP : slot, slot ^ GROUP);
-                }
-            }
-            slot ^= GROUP;
+            };
+            if (p.act) results(Number<1>{});
+            else results(Number<0>{});
+            return;
         }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // no load is left behind in LDS at the end
-    }
-
-    // --- results: lane (j, kg) holds rows 4 kg .. 4 kg + 3 of column j of each 16 x 16 block
+        // They are stored once the next unit's first loads are there, and are on their way while its first stages are
+        // multiplied. A store takes four (fp32: eight) neighbouring lanes to a column, whose 16-byte pieces are one run of memory.
+        if (more && next.e < p.E) {
+            set_up(ln, next, l);
+            first_loads(l);
+        }
+        constexpr int LC = OUT == kOutF32 ? 8 : 4, NC = 64 / LC; // lanes to a column, columns to a store
+        int pair[IB][16 / NC];
 #pragma unroll
-    for (int q = 0; q < IB; ++q) {
-        const int64_t pair = pair_of(p, u, 16 * (wb * IB + q) + j);
-        if (pair < 0) continue;
-        if constexpr (GATED) {
+        for (int q = 0; q < IB; ++q)
 #pragma unroll
-            for (int i = 0; i < IA / 4; ++i) {
-                const int64_t f = a0 + wa * (16 * IA / 2) + 32 * i + 8 * kg;
-                float v[8];
+            for (int c = 0; c < 16 / NC; ++c) pair[q][c] = (int)pair_of(p, u, 16 * (wb * IB + q) + NC * c + ln / LC);
+        wait_loads_and_barrier<0>();
+        auto from = [](int lane4, uint32_t v) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_ds_bpermute(lane4, (int)v); };
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float g = acc[2 * i + r / 4][q][r % 4], up = acc[IA / 2 + 2 * i + r / 4][q][r % 4];
-                    v[r] = (p.act ? activation<1>(g) : activation<0>(g)).a * up;
-                }
-                if (f < R) store_results<OUT>(p, pair, f, v);
-            }
-        } else {
+        for (int q = 0; q < IB; ++q) {
 #pragma unroll
             for (int i = 0; i < IA / 2; ++i) {
-                const int64_t f = a0 + wa * (16 * IA) + 32 * i + 8 * kg;
-                float v[8];
+                if constexpr (OUT == kOutF32) {
+                    const int64_t f = a0 + 32 * i + 4 * (ln & 7);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) v[r] = acc[2 * i + r / 4][q][r % 4];
-                if (f < R) store_results<OUT>(p, pair, f, v);
+                    for (int c = 0; c < 2; ++c) {
+                        const int src = 4 * (8 * c + ln / 8 + 16 * ((ln & 7) >> 1));
+                        u32x4 w;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t lo = from(src, __float_as_uint(acc[2 * i][q][e])), hi = from(src, __float_as_uint(acc[2 * i + 1][q][e]));
+                            w[e] = ln & 1 ? hi : lo;
+                        }
+                        if (pair[q][c] >= 0 && f < R) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p.t.part + (int64_t)pair[q][c] * R + f));
+                    }
+                } else {
+                    const int64_t f = a0 + 32 * i + 8 * (ln & 3);
+                    const int src = 4 * (ln / 4 + 16 * (ln & 3));
+                    u32x4 w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = from(src, pack_x16<OUT == kOutF16>(acc[2 * i + e / 2][q][2 * (e % 2)], acc[2 * i + e / 2][q][2 * (e % 2) + 1]));
+                    if (pair[q][0] >= 0 && f < R)
+                        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.t.out) + (int64_t)pair[q][0] * R + f));
+                }
             }
         }
+        if (!more) break;
+        u = next;
     }
 }
 
@@ -413,7 +498,7 @@ skinny_kernel(TileArgs p)
     static_assert(RING * STAGE >= 2 * NT * 64 * 16, "a wave's sums fit where its stages were");
     __shared__ __attribute__((aligned(1024))) char lds[W * RING * STAGE];
     Unit u;
-    if (!unit_of<16 * NT>(p, &u)) return;
+    if (!unit_of<16 * NT>(p, count_units<16 * NT>(p), blockIdx.x / 8, &u)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, kg = lane >> 4;
     const uint32_t kb = p.kb, sb = p.sb;
@@ -516,8 +601,13 @@ skinny_kernel(TileArgs p)
     if (pair < 0) return;
     if constexpr (GATED) {
         float v[4];
+        if (p.act) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (p.act ? activation<1>(v0[e]) : activation<0>(v0[e])).a * v1[e];
+            for (int e = 0; e < 4; ++e) v[e] = activation<1>(v0[e]).a * v1[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = activation<0>(v0[e]).a * v1[e];
+        }
         if (r < R) store_results<OUT>(p, pair, r, v);
     } else {
         const float lo[4] = {v0[0], v0[1], v0[2], v0[3]}, hi[4] = {v1[0], v1[1], v1[2], v1[3]};
@@ -554,7 +644,7 @@ combine_kernel(const float* __restrict__ part, const float* __restrict__ weights
 template <bool GATED, int OUT>
 hipError_t launch_tiles(const Tiling& t, const TileArgs& p, hipStream_t st)
 {
-    const dim3 grid((unsigned)(8 * cdiv(t.na * t.nb, 8))), block((unsigned)t.threads);
+    const dim3 grid((unsigned)t.grid()), block((unsigned)t.threads);
     switch (t.shape) {
         case kSkinny16: hipLaunchKernelGGL((skinny_kernel<GATED, OUT, 1>), grid, block, 0, st, p); break;
         case kSkinny32: hipLaunchKernelGGL((skinny_kernel<GATED, OUT, 2>), grid, block, 0, st, p); break;

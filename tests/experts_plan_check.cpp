@@ -35,13 +35,15 @@ static int check_units(const experts::Geometry& g, const std::vector<int64_t>& l
         nb[e] = (load[e] + t.cols - 1) / t.cols;
         before[e + 1] = before[e] + nb[e];
     }
-    const int64_t total = before.back(), units = total * t.na, grid = 8 * experts::cdiv(t.na * t.nb, 8), per = (units + 7) / 8;
+    const int64_t total = before.back(), units = total * t.na, grid = t.grid(), per = (units + 7) / 8;
     if (total > t.nb) return fail("units past the grid's", total, t.nb);
-    if ((per - 1) * 8 + 7 >= grid && units > 0) return fail("grid", per, grid);
+    if (grid % 8 || grid > 8 * experts::cdiv(t.na * t.nb, 8)) return fail("grid", grid, t.nb);
+    if (!t.places && (per - 1) * 8 + 7 >= grid && units > 0) return fail("grid", per, grid);
     std::vector<char> seen((size_t)units, 0);
     for (int64_t b = 0; b < grid; ++b) {
-        const int64_t i = b / 8, u = (b % 8) * per + i;
-        if (i >= per || u >= units) continue;
+      for (int64_t i = b / 8; i < per; i += t.places ? grid / 8 : per) {
+        const int64_t u = (b % 8) * per + i;
+        if (u >= units) break;
         const int64_t q = u / t.na;
         size_t e = 0;
         while (q >= before[e + 1]) ++e;
@@ -51,6 +53,7 @@ static int check_units(const experts::Geometry& g, const std::vector<int64_t>& l
         char& s = seen[(size_t)(before[e] * t.na + (int64_t)c * t.na + a)];
         if (s) return fail("twice", (long long)e, u);
         s = 1;
+      }
     }
     for (char s : seen)
         if (!s) return fail("never", units, total);
