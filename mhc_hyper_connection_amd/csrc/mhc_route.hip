@@ -5,8 +5,12 @@
 //   largest choices have the largest sums), weights w_j = scale s_j (/ the sum of the chosen s)
 //
 // Two experts may be nearer to each other than fp32 tells, and the order of a choice is an exact
-// result: scores, choices and their sums are fp64. Without a bias the scores are ordered as
+// result: that of fp64 scores, choices and sums. Without a bias the scores are ordered as
 // the logits are, which are then compared themselves. Ties go to the lowest index.
+// The choice is first made in fp32, with a bound on its error. Where two neighbours in the order are nearer than that,
+// experts are taken on until one is surely the last, and those few are put in order by their fp64 values; where
+// the last group in and the first one out are, or no expert is surely the last in time, the token's choice is made again
+// in fp64. (All in fp64: 35 us at T = 16384, E = 256, top 8, 4 of 8 groups.)
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -47,6 +51,8 @@ __device__ __forceinline__ double other(double v)
     const uint32_t lo = (uint32_t)other<S>((int)(uint32_t)u), hi = (uint32_t)other<S>((int)(uint32_t)(u >> 32));
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+template <int S>
+__device__ __forceinline__ uint32_t other(uint32_t v) { return (uint32_t)other<S>((int)v); }
 template <int S>
 __device__ __forceinline__ float other(float v) { return __int_as_float(other<S>(__float_as_int(v))); }
 
@@ -108,79 +114,100 @@ struct RouteArgs {
 };
 
 constexpr double kInf = __builtin_huge_val();
+constexpr float kInfF = __builtin_huge_valf();
+constexpr float kU = 5.9604645e-8f;       // 2^-24
 
-// L lanes a token, V experts a lane (lane + L v): E <= L V.
-template <int DT, int L, int V, bool GROUPS>
-__global__ void __launch_bounds__(kThr)
-route_kernel(RouteArgs p)
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int L>
+__device__ __forceinline__ uint32_t max_of(uint32_t v)
 {
-    constexpr int TOK = kThr / L;
-    __shared__ double shared_c[GROUPS ? TOK * L * V : 1];
-    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-    const int64_t t0 = (int64_t)blockIdx.x * TOK + slot;
-    const bool live = t0 < p.T;
-    const int64_t t = live ? t0 : p.T - 1;      // the lanes past the last token compute it again and store nothing
-    const int E = p.E;
-    const bool softmax = p.score == kSoftmax, biased = p.t.bias != nullptr;
+    return reduce<L>(v, [](uint32_t a, uint32_t b) { return max_u32(a, b); });
+}
+template <int L>
+__device__ __forceinline__ float max_of(float v)
+{
+    return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+// What a wave wrote to LDS is there for its other lanes.
+__device__ __forceinline__ void lds_of_the_wave() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
-    float l[V];
-    double c[V];
-    bool bad = false;
-    float top = -__builtin_huge_valf();
+// Whole numbers that are ordered as floats are, and back.
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t k)
+{
+    return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+
+// Largest first: Batcher's network over a power of two of registers.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&s)[N])
+{
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = lane + L * v;
-        l[v] = e < E ? load_logit<DT>(p.t.logits, t * E + e) : -__builtin_huge_valf();
-        bad |= l[v] != l[v];
-        top = fmaxf(top, l[v]);
-    }
-    double most = 0, total = 1;
-    if (softmax) {
-        top = reduce<L>(top, [](float a, float b) { return fmaxf(a, b); });
-        bad |= top == __builtin_huge_valf();
-        most = top > -__builtin_huge_valf() ? (double)top : 0.0;
-    }
-    auto raw = [&](float x) { return softmax ? exp((double)x - most) : 1.0 / (1.0 + exp(-(double)x)); };
-    if (softmax || biased || GROUPS) {
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = s[i + j], b = s[i + j + k];
+                        s[i + j] = max_u32(a, b);
+                        s[i + j + k] = a < b ? a : b;
+                    }
+}
+
+// A token's logits in L lanes, V a lane (expert lane + L v), and what of them both choices need.
+template <int L, int V>
+struct Token {
+    float l[V], b[V];       // -inf past E; the biases
+    uint32_t off;           // masked experts, a bit for each v
+    float top;              // the largest logit (0 where none is finite)
+    int lane, slot;
+};
+
+// The choice in fp64. Lane j gets expert j of the order (and, with 16 lanes, j + 16); -1 where none is left.
+template <int L, int V, bool GROUPS, int H>
+__device__ __forceinline__ void choose_exactly(const RouteArgs& p, const Token<L, V>& k, double* row, int (&mine)[H])
+{
+    const bool softmax = p.score == kSoftmax, biased = p.t.bias != nullptr;
+    double c[V];
+    if (biased || GROUPS) {
         double sum = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            c[v] = lane + L * v < E ? raw(l[v]) : 0.0;
+            const double x = (double)k.l[v];
+            c[v] = k.lane + L * v < p.E ? (softmax ? exp(x - (double)k.top) : 1.0 / (1.0 + exp(-x))) : 0.0;
             sum += c[v];
         }
         if (softmax) {
-            total = sum_of<L>(sum);
-            total = total > 0 ? total : 1.0;
+            sum = sum_of<L>(sum);
+            sum = sum > 0 ? sum : 1.0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) c[v] /= total;
+            for (int v = 0; v < V; ++v) c[v] /= sum;
         }
     }
-    // the choice; masked experts at -inf
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = lane + L * v;
-        bool masked = !(l[v] > -__builtin_huge_valf());
-        if (biased && e < E) {
-            const float b = p.t.bias[e];
-            bad |= b != b;
-            masked |= b == -__builtin_huge_valf();
-            c[v] += (double)b;
-        }
-        if (GROUPS) shared_c[slot * (L * V) + e] = masked ? -kInf : c[v];
-        if (!biased) c[v] = l[v];
+        const bool masked = (k.off >> v) & 1;
+        if (biased) c[v] += (double)k.b[v];
+        if (GROUPS) row[k.lane + L * v] = masked ? -kInf : c[v];
+        if (!biased) c[v] = (double)k.l[v];
         if (masked) c[v] = -kInf;
     }
-    bad = any_of<L>(bad);
-
     if constexpr (GROUPS) {
-        __syncthreads();
+        lds_of_the_wave();
         // a lane to a group: its largest, or the sum of its two largest
         double value = -kInf;
-        if (lane < p.groups) {
-            const double* const row = shared_c + slot * (L * V) + lane * p.per;
+        if (k.lane < p.groups) {
+            const double* const g = row + k.lane * p.per;
             double a = -kInf, b = -kInf;
             for (uint32_t i = 0; i < p.per; ++i) {
-                const double x = row[i];
+                const double x = g[i];
                 b = fmax(b, fmin(a, x));
                 a = fmax(a, x);
             }
@@ -188,50 +215,308 @@ route_kernel(RouteArgs p)
         }
         uint32_t open = 0;
         for (int i = 0; i < p.top_groups; ++i) {
-            const Best g = best_of<L>({value, lane});
+            const Best g = best_of<L>({value, k.lane});
             if (g.key > -kInf) open |= 1u << g.at;
-            if (lane == g.at) value = -kInf;
+            if (k.lane == g.at) value = -kInf;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint32_t g = ((uint32_t)(lane + L * v) * p.magic) >> 20;
+            const uint32_t g = ((uint32_t)(k.lane + L * v) * p.magic) >> 20;
             if (!((open >> (g & 31)) & 1)) c[v] = -kInf;
         }
     }
-
-    // lane j keeps the experts j and, past L lanes of 16, j + 16
-    constexpr int H = L == 16 ? 2 : 1;
-    int mine[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) mine[h] = -1;
     for (int j = 0; j < p.k; ++j) {
         Best b = {-kInf, kMaxE};
 #pragma unroll
-        for (int v = 0; v < V; ++v) better(b, c[v], lane + L * v);
+        for (int v = 0; v < V; ++v) better(b, c[v], k.lane + L * v);
         b = best_of<L>(b);
         if (b.key == -kInf) break;       // none left, for every lane of the token
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (lane + L * v == b.at) c[v] = -kInf;
+            if (k.lane + L * v == b.at) c[v] = -kInf;
 #pragma unroll
         for (int h = 0; h < H; ++h)
-            if (j == lane + L * h) mine[h] = b.at;
+            if (j == k.lane + L * h) mine[h] = b.at;
     }
-    double w[H], chosen = 0;
+}
+
+enum Found { kSure, kNear, kUnknown };   // in order; a set whose order fp64 has to say; neither
+
+// The choice in fp32: the first n experts of its order, n >= p.k (or all that there are). A score is off by at most A 2^-24 (softmax: the exponentials'
+// arguments, their sum of E terms and the division, 2 + 64 times the largest score; sigmoid: 8) and a choice by 2^-24 of
+// itself more. A lane sorts its experts by one word each: the choice as an ordered whole number, whose last four bits (32
+// 2^-24 of it) are the expert's place in the lane; of 16-bit logits alone all bits and the expert's number, so
+// that their many ties are in order too. Then the lanes' first ones are compared, and the winning lane's list moves up.
+template <int DT, int L, int V, bool GROUPS, int H>
+__device__ __forceinline__ Found choose(const RouteArgs& p, const Token<L, V>& k, float* row, int (&mine)[H], int* n)
+{
+    const bool softmax = p.score == kSoftmax, biased = p.t.bias != nullptr, numbered = DT != kF32 && !biased;
+    float c[V], A = 0.f;
+    bool sure = true;
+    if (biased || GROUPS) {
+        A = 8.f;
+        if (softmax) {
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                c[v] = __expf(k.l[v] - k.top);
+                sum += c[v];
+            }
+            sum = sum_of<L>(sum);
+            const float r = sum > 0.f ? 1.f / sum : 0.f;
+            A = 2.f + 64.f * r;
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] *= r;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] = __builtin_amdgcn_rcpf(1.f + __expf(-k.l[v]));
+        }
+    }
+    uint32_t open = ~0u;
+    if (biased)
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] += k.b[v];
+    if constexpr (GROUPS) {
+        const uint32_t wide = p.per + 4;      // groups four words apart, so that their lanes read different banks
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t e = (uint32_t)(k.lane + L * v), g = (e * p.magic) >> 20;
+            if (e < (uint32_t)p.E) row[e + 4 * g] = (k.off >> v) & 1 ? -kInfF : c[v];
+        }
+        lds_of_the_wave();
+        float value = -kInfF, size = 0.f;
+        if (k.lane < p.groups) {
+            const float* const g = row + k.lane * wide;
+            float a = -kInfF, b = -kInfF;
+            auto take = [&](float x) { b = __builtin_amdgcn_fmed3f(a, b, x), a = fmaxf(a, x); };   // b <= a
+            uint32_t i = 0;
+            if (p.per % 4 == 0)
+                for (; i < p.per; i += 4) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(g + i);
+                    take(x[0]), take(x[1]), take(x[2]), take(x[3]);
+                }
+            else
+                for (; i < p.per; ++i) take(g[i]);
+            const bool two = p.group_top == 2 && b > -kInfF;
+            value = two ? a + b : a;
+            size = value > -kInfF ? fabsf(a) + (two ? fabsf(b) : 0.f) : 0.f;
+        }
+        size = max_of<L>(size);
+        open = 0;
+        float least = kInfF;
+        for (int i = 0; i <= p.top_groups; ++i) {
+            const float m = max_of<L>(value);
+            if (i == p.top_groups) {      // the first one out
+                sure = m == -kInfF || least - m > kU * (4.f * A + 8.f * size);
+                break;
+            }
+            if (m == -kInfF) break;
+            least = m;
+            const uint64_t who = __ballot(value == m) >> (threadIdx.x & (64 - L));
+            const int at = __builtin_ctzll(who);   // of equal ones the first; another one, left out, is no surer than the bound
+            open |= 1u << at;
+            if (k.lane == at) value = -kInfF;
+        }
+    }
+    uint32_t s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint32_t e = (uint32_t)(k.lane + L * v);
+        bool out = (k.off >> v) & 1;
+        if (GROUPS) out |= !((open >> (((e * p.magic) >> 20) & 31)) & 1);
+        if (numbered) {
+            const float x = k.l[v] + 0.f;     // not -0
+            const uint32_t u = DT == kF16 ? pack_f16x2(0.f, x) : __float_as_uint(x);
+            s[v] = ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & 0xffff0000u) | (0xffffu - e);
+        } else s[v] = (ordered(biased ? c[v] : k.l[v]) & ~15u) | (15u - v);
+        s[v] = out ? 0u : s[v];
+    }
+    sort_down(s);
+#pragma unroll
+    for (int h = 0; h < H; ++h) mine[h] = -1;
+    Found found = sure ? kSure : kUnknown;
+    float last = 0.f;
+    int j = 0;
+    for (;; ++j) {
+        const uint32_t m = max_of<L>(s[0]);
+        if (m == 0 || (numbered && j == p.k)) break;
+        bool won = s[0] == m;
+        int e;
+        if (numbered) e = (int)(0xffffu - (m & 0xffffu));
+        else {
+            const uint64_t who = (__ballot(won) >> (threadIdx.x & (64 - L))) & (L == 64 ? ~0ull : 0xffffull);
+            const float now = from_ordered(m & ~15u);
+            // surely behind the one before (1e-36: what the factors lose where they are subnormal)
+            const bool apart = j == 0 || last - now > kU * (2.f * A + 40.f * fmaxf(fabsf(last), fabsf(now))) + 1e-36f;
+            if (j >= p.k && apart) break;
+            if (!apart && found == kSure) found = kNear;
+            if (j == L * H) {
+                found = kUnknown;
+                break;
+            }
+            last = now;
+            e = __builtin_ctzll(who);
+            won = k.lane == e;               // of lanes with the same word the first; the next one is not apart from it
+            e += L * (int)(15u - (m & 15u));
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            if (j == k.lane + L * h) mine[h] = e;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            uint32_t up = v + 1 < V ? s[v + 1 < V ? v + 1 : 0] : 0u;
+            asm("" : "+v"(up));              // a value: not a choice between two places of the array
+            s[v] = won ? up : s[v];
+        }
+    }
+    *n = j;
+    return found;
+}
+
+// The n experts of `mine` in the order of their fp64 values. Each lane counts those before its own.
+template <int L, int V, int H>
+__device__ __forceinline__ void put_in_order(const RouteArgs& p, const Token<L, V>& k, const void* logits, int64_t row, float (*load)(const void*, int64_t), int n,
+                                             int (&mine)[H])
+{
+    const bool softmax = p.score == kSoftmax, biased = p.t.bias != nullptr;
+    double sum = 1;
+    if (softmax && biased) {
+        sum = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += k.lane + L * v < p.E ? exp((double)k.l[v] - (double)k.top) : 0.0;
+        sum = sum_of<L>(sum);
+    }
+    double key[H];
+    int before[H], at[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-        w[h] = mine[h] < 0 ? 0.0 : raw(load_logit<DT>(p.t.logits, t * E + mine[h])) / total;
-        chosen += w[h];
+        const int e = mine[h];
+        key[h] = -kInf;
+        before[h] = 0;
+        at[h] = -1;
+        if (e >= 0) {
+            key[h] = (double)load(logits, row + e);
+            if (biased) key[h] = (softmax ? exp(key[h] - (double)k.top) / sum : 1.0 / (1.0 + exp(-key[h]))) + (double)p.t.bias[e];
+        }
     }
-    if (p.renormalise) {
-        chosen = sum_of<L>(chosen);
-        chosen = chosen > 0 ? chosen : 1.0;
-    } else chosen = 1.0;
+    const int lane0 = (threadIdx.x & 63) - k.lane;
+    for (int i = 0; i < n; ++i) {
+        const int src = lane0 + i % L;
+        const bool upper = H == 2 && i >= L;
+        const double x = __shfl(upper ? key[H - 1] : key[0], src);
+        const int e = __shfl(upper ? mine[H - 1] : mine[0], src);
+#pragma unroll
+        for (int h = 0; h < H; ++h) before[h] += x > key[h] || (x == key[h] && e < mine[h]) ? 1 : 0;
+    }
+    for (int i = 0; i < n; ++i) {
+        const int src = lane0 + i % L;
+        const bool upper = H == 2 && i >= L;
+        const int place = __shfl(upper ? before[H - 1] : before[0], src), e = __shfl(upper ? mine[H - 1] : mine[0], src);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            if (place == k.lane + L * h) at[h] = e;
+    }
+#pragma unroll
+    for (int h = 0; h < H; ++h) mine[h] = at[h];
+}
+
+// L lanes a token, V experts a lane (lane + L v): E <= L V.
+template <int DT, int L, int V, bool GROUPS>
+__global__ void __launch_bounds__(kThr)
+route_kernel(RouteArgs p)
+{
+    constexpr int TOK = kThr / L, ROW = L * V + 4 * kMaxGroups;     // floats, or doubles, of a token's row
+    __shared__ __attribute__((aligned(16))) double shared_c[GROUPS ? TOK * ROW : 1];
+    Token<L, V> k;
+    k.lane = threadIdx.x % L;
+    k.slot = threadIdx.x / L;
+    const int64_t t0 = (int64_t)blockIdx.x * TOK + k.slot;
+    const bool live = t0 < p.T;
+    const int64_t t = live ? t0 : p.T - 1;      // the lanes past the last token compute it again and store nothing
+    const int E = p.E;
+    const bool softmax = p.score == kSoftmax, biased = p.t.bias != nullptr;
+
+    bool bad = false;
+    k.top = -kInfF;
+    k.off = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = k.lane + L * v;
+        k.l[v] = e < E ? load_logit<DT>(p.t.logits, t * E + e) : -kInfF;
+        k.b[v] = biased && e < E ? p.t.bias[e] : 0.f;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        bad |= k.l[v] != k.l[v] || k.b[v] != k.b[v];
+        k.top = fmaxf(k.top, k.l[v]);
+        if (!(k.l[v] > -kInfF) || k.b[v] == -kInfF) k.off |= 1u << v;
+    }
+    if (softmax) {
+        k.top = max_of<L>(k.top);
+        bad |= k.top == kInfF;
+        if (!(k.top > -kInfF)) k.top = 0.f;
+    }
+    bad = any_of<L>(bad);
+
+    // lane j keeps the experts j and, past L lanes of 16, j + 16
+    constexpr int H = L == 16 ? 2 : 1;
+    int mine[H];
+    double* const row = shared_c + (GROUPS ? k.slot * ROW : 0);
+    int n;
+    Found found = choose<DT, L, V, GROUPS>(p, k, reinterpret_cast<float*>(row), mine, &n);
+    if (bad) found = kSure;
+    if (__ballot(found == kNear)) {
+        int other[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) other[h] = mine[h];
+        int most = found == kNear ? n : 0;       // tokens of a wave go through together
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_xor(most, d);
+            most = most > o ? most : o;
+        }
+        put_in_order<L, V>(p, k, p.t.logits, t * E, load_logit<DT>, most, other);
+#pragma unroll
+        for (int h = 0; h < H; ++h) mine[h] = found == kNear ? other[h] : mine[h];
+    }
+    if (__ballot(found == kUnknown)) {
+        int exact[H];
+        choose_exactly<L, V, GROUPS>(p, k, row, exact);
+#pragma unroll
+        for (int h = 0; h < H; ++h) mine[h] = found == kUnknown ? exact[h] : mine[h];
+    }
+    // a set in order is as long as it had to be for that
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+        if (k.lane + L * h >= p.k) mine[h] = -1;
+
+    // the weights, in fp64
+    auto score = [&](float x) { return softmax ? exp((double)x - (double)k.top) : 1.0 / (1.0 + exp(-(double)x)); };
+    double w[H], sum = 0;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-        const int j = lane + L * h;
+        w[h] = 0;
+        if (h == 0 || p.k > L) {
+            if (mine[h] >= 0) w[h] = score(load_logit<DT>(p.t.logits, t * E + mine[h]));
+            sum += w[h];
+        }
+    }
+    if (softmax && !p.renormalise) {
+        sum = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += k.lane + L * v < E ? score(k.l[v]) : 0.0;
+    }
+    if (softmax || p.renormalise) {
+        sum = sum_of<L>(sum);
+        sum = sum > 0 ? sum : 1.0;
+    } else sum = 1.0;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const int j = k.lane + L * h;
         if (live && j < p.k) {
-            p.t.weights[t * p.k + j] = bad ? __builtin_nanf("") : (float)(w[h] / chosen * p.scale);
+            p.t.weights[t * p.k + j] = bad ? __builtin_nanf("") : (float)(w[h] / sum * p.scale);
             p.t.experts[t * p.k + j] = bad ? -1 : mine[h];
         }
     }
@@ -381,7 +666,8 @@ place_kernel(const int32_t* __restrict__ experts, const int32_t* __restrict__ co
     __shared__ int n[W][kMaxE + 1];       // a wave's counts, then where its next pair of an expert goes
     __shared__ int part[W];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < W * (kMaxE + 1); i += kPlanThreads) (&n[0][0])[i] = 0;
+    for (int w = 0; w < W; ++w)
+        for (int e = tid; e <= E; e += kPlanThreads) n[w][e] = 0;
     __syncthreads();
     const int64_t i0 = blockIdx.x * chunk, i1 = i0 + chunk < P ? i0 + chunk : P;
     const int64_t run = ((i1 - i0 + W - 1) / W + 63) / 64 * 64;
@@ -396,9 +682,10 @@ place_kernel(const int32_t* __restrict__ experts, const int32_t* __restrict__ co
         int before = 0, all = 0;
         if (e <= E) {
             if (counts) {
-                for (int64_t b = 0; b < (int64_t)gridDim.x; ++b) {
-                    const int c = counts[b * (E + 1) + e];
-                    before += b < (int64_t)blockIdx.x ? c : 0;
+#pragma unroll 16
+                for (int b = 0; b < (int)gridDim.x; ++b) {
+                    const int c = counts[(int64_t)b * (E + 1) + e];
+                    before += b < (int)blockIdx.x ? c : 0;
                     all += c;
                 }
             } else {

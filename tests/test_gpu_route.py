@@ -98,17 +98,33 @@ def test_groups(E, groups, top_groups, k, score, biased, group_top):
         run(L, bias if biased else None, k, dev, "float32", 3, score=score, groups=groups, top_groups=top_groups, group_top=group_top, scale=2.5)
 
 
-def test_many_tokens_and_near_ties():
-    # scores nearer to each other than fp32 tells: the order is that of 64 bits
+@pytest.mark.parametrize("near", [1e-9, 3e-8, 1e-6, 3e-5])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_many_tokens_and_near_ties(score, near):
+    # scores nearer to each other than fp32 tells, or about as near: the order is that of 64 bits
     import torch
     dev = device()
     rng = np.random.default_rng(5)
-    T, E = 3001, 64
+    T, E = 1501, 64
     L = torch.from_numpy((np.round(rng.standard_normal((T, E)) * 4) / 4).astype(np.float32))
-    bias = torch.from_numpy((1e-9 * rng.permutation(E)).astype(np.float32))
-    for score in ("softmax", "sigmoid"):
-        print(f"[case] near ties {score}", file=sys.stderr, flush=True)
-        run(L, bias, 8, dev, "float32", 1, score=score)
+    bias = torch.from_numpy((near * rng.permutation(E)).astype(np.float32))
+    for groups, top_groups in ((1, 1), (8, 3)):
+        print(f"[case] near ties {score} {near} {groups}", file=sys.stderr, flush=True)
+        run(L, bias, 8, dev, "float32", 1, score=score, groups=groups, top_groups=top_groups)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_near_logits_without_a_bias(dtype):
+    # neighbours in the format, equal ones, zeros of either sign, subnormal ones
+    import torch
+    dev = device()
+    rng = np.random.default_rng(6)
+    for unit, offset in ((2.0 ** -22, 1.0), (2.0 ** -18, -2.0), (2.0 ** -149, 0.0), (2.0 ** -24, 0.0), (2.0 ** -7, 1.5), (2.0 ** -10, -1.0)):
+        L = torch.from_numpy((offset + unit * rng.integers(-20, 20, (300, 96))).astype(np.float32)).to(getattr(torch, dtype))
+        L[::3] = torch.where(L[::3] == 0, -L[::3], L[::3])
+        for groups, top_groups in ((1, 1), (4, 2)):
+            print(f"[case] near logits {dtype} {unit} {groups}", file=sys.stderr, flush=True)
+            run(L, None, 10, dev, dtype, 1, groups=groups, top_groups=top_groups)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
