@@ -40,9 +40,15 @@ __all__ = ["PreForward", "PreBackward", "mhc_pre", "mhc_pre_backward", "mhc_post
            "MHC_OK", "MHC_ERR_NULLPTR", "MHC_ERR_PARAM_INVALID", "MHC_ERR_RUNTIME"]
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t):
@@ -695,6 +701,20 @@ def mhc_glu_backward(grad_h, x, w_gate, w_up, *, act="silu", need_h=False, out=N
     return out
 
 
+def _launch(device, what, raw, *args):
+    """raw(*args, the current stream on `device`) with that device as the current one; raises for any status but success."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors on a GPU expected, got {device}")
+    if device.index == torch.cuda.current_device():
+        st = raw(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = raw(*args, _raw_stream(device))
+    if st != MHC_OK:
+        raise MhcError(st, what)
+
+
 _LOGITS = {"bfloat16": 0, "float16": 1, "float32": 2}   # mhc_route_params.logits_dtype
 
 
@@ -728,18 +748,15 @@ def mhc_route(logits, top_k, *, bias=None, score="softmax", groups=1, top_groups
     _check(logits, "logits", logits.dtype, logits.shape, dev)
     _check(bias, "bias", torch.float32, (logits.shape[-1],), dev)
     if out is None:
-        weights = torch.empty(shape, dtype=torch.float32, device=dev)
-        experts = torch.empty(shape, dtype=torch.int32, device=dev)
+        weights = torch.empty(*shape, dtype=torch.float32, device=dev)
+        experts = torch.empty(*shape, dtype=torch.int32, device=dev)
     else:
         weights, experts = out
         for t, name, dt in ((weights, "out[0]", torch.float32), (experts, "out[1]", torch.int32)):
             if t is None:
                 raise ValueError(f"{name} is required")
             _check(t, name, dt, shape, dev)
-    with _on_gpu(dev):
-        st = raw_route(params, _ptr(logits), _ptr(bias), _ptr(weights), _ptr(experts), _stream(dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_route")
+    _launch(dev, "mhc_route", raw_route, params, logits.data_ptr(), _ptr(bias), weights.data_ptr(), experts.data_ptr())
     return weights, experts
 
 
@@ -762,11 +779,8 @@ def mhc_route_backward(grad_weights, logits, weights, experts, *, score="softmax
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     else:
         _check(out, "out", logits.dtype, logits.shape, dev)
-    with _on_gpu(dev):
-        st = raw_route_backward(params, _ptr(grad_weights), _ptr(logits), _ptr(weights), _ptr(experts), _ptr(out),
-                                _stream(dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_route_backward")
+    _launch(dev, "mhc_route_backward", raw_route_backward, params, grad_weights.data_ptr(), logits.data_ptr(),
+            weights.data_ptr(), experts.data_ptr(), out.data_ptr())
     return out
 
 
@@ -783,15 +797,15 @@ def mhc_experts_plan(experts, num_experts):
         raise ValueError("experts: at least one dimension expected")
     shape, dev = tuple(experts.shape), experts.device
     _check(experts, "experts", torch.int32, shape, dev)
+    if dev.type != "cuda":
+        raise ValueError(f"tensors on a GPU expected, got {dev}")
     P, E = experts.numel(), int(num_experts)
     ws_bytes = experts_plan_workspace_size(P, E)
-    offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-    pairs = torch.empty((P,), dtype=torch.int32, device=dev)
-    with _on_gpu(dev):
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-        st = raw_experts_plan(P, E, _ptr(experts), _ptr(offsets), _ptr(pairs), _ptr(ws), ws_bytes, _stream(dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_experts_plan")
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    pairs = torch.empty(P, dtype=torch.int32, device=dev)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _launch(dev, "mhc_experts_plan", raw_experts_plan, P, E, experts.data_ptr(), offsets.data_ptr(), pairs.data_ptr(),
+            _ptr(ws), ws_bytes)
     return ExpertsPlan(offsets, pairs, shape)
 
 
@@ -830,17 +844,14 @@ def mhc_mxfp4(x, *, out=None):
     _check(x, "x", xdt, shape, dev)
     if out is None:
         codes, scales = _mxfp4_shapes(shape)
-        out = Mxfp4(torch.empty(codes, dtype=torch.uint8, device=dev), torch.empty(scales, dtype=torch.uint8, device=dev),
+        out = Mxfp4(torch.empty(*codes, dtype=torch.uint8, device=dev), torch.empty(*scales, dtype=torch.uint8, device=dev),
                     xdt, shape[-1])
     else:
         _check_mxfp4(out, "out", shape, dev)
         if out.dtype != xdt:
             raise ValueError(f"out: of dtype {out.dtype}, expected {xdt}")
-    with _on_gpu(dev):
-        st = raw_mxfp4(math.prod(shape[:-1]), shape[-1], xdt == torch.float16, _ptr(x), _ptr(out.codes), _ptr(out.scales),
-                       _stream(dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_mxfp4")
+    _launch(dev, "mhc_mxfp4", raw_mxfp4, math.prod(shape[:-1]), shape[-1], xdt == torch.float16, x.data_ptr(),
+            out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
 
@@ -858,11 +869,8 @@ def mhc_mxfp4_restore(m, *, out=None):
         out = torch.empty(shape, dtype=xdt, device=dev)
     else:
         _check(out, "out", xdt, shape, dev)
-    with _on_gpu(dev):
-        st = raw_mxfp4_restore(math.prod(shape[:-1]), shape[-1], xdt == torch.float16, _ptr(m.codes), _ptr(m.scales),
-                               _ptr(out), _stream(dev))
-    if st != MHC_OK:
-        raise MhcError(st, "mhc_mxfp4_restore")
+    _launch(dev, "mhc_mxfp4_restore", raw_mxfp4_restore, math.prod(shape[:-1]), shape[-1], xdt == torch.float16,
+            m.codes.data_ptr(), m.scales.data_ptr(), out.data_ptr())
     return out
 
 
@@ -888,12 +896,11 @@ def _left(x, name):
 
 def _run_products(name, params, tensors, in_4_bits, dev):
     torch = _torch()
+    if dev.type != "cuda":
+        raise ValueError(f"tensors on a GPU expected, got {dev}")
     ws_bytes = products_workspace_size(name, params, in_4_bits)
-    with _on_gpu(dev):
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-        st = raw_products(name, params, tensors, _ptr(ws), ws_bytes, _stream(dev))
-    if st != MHC_OK:
-        raise MhcError(st, name)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _launch(dev, name, raw_products, name, params, tensors, _ptr(ws), ws_bytes)
 
 
 def mhc_mxfp4_product(x, w, *, out=None):

@@ -406,7 +406,7 @@ def raw_glu_backward(params: GluParams, ptrs: dict, ws_ptr, ws_bytes, stream) ->
 
 
 def raw_route(params: RouteParams, logits_ptr, bias_ptr, weights_ptr, experts_ptr, stream) -> int:
-    return int(load().mhc_route(ctypes.byref(params), logits_ptr, bias_ptr, weights_ptr, experts_ptr, stream))
+    return load().mhc_route(ctypes.byref(params), logits_ptr, bias_ptr, weights_ptr, experts_ptr, stream)
 
 
 def raw_route_backward(params: RouteParams, grad_weights_ptr, logits_ptr, weights_ptr, experts_ptr, grad_logits_ptr,

@@ -482,23 +482,22 @@ tile_kernel(TileArgs p)
     }
 }
 
-// Few pairs of an expert (16 NT at most to a unit): reading the weights once is the whole cost. A
+// Few pairs of an expert (16 at most to a unit): reading the weights once is the whole cost. A
 // workgroup takes 32 weight rows (gated: 16 of either weight), its W waves every W-th stage of 256 values; their
 // sums meet in LDS and are added in wave order. A wave keeps a ring of three stages of its own in LDS,
 // so that it waits for its own loads only and meets the others once.
-template <bool GATED, int OUT, int NT>
+template <bool GATED, int OUT>
 __global__ void __launch_bounds__(256)
 skinny_kernel(TileArgs p)
 {
-    constexpr int W = 4, RING = 3, ROWS = 32 + 16 * NT;
-    // loads of scales: 16 rows of a gated pair of weights each (half a load, the other lanes idle) or 32 rows;
-    // the pairs' 16 or 32 rows each
-    constexpr int SW = GATED ? 2 : 1, SX = (NT + 1) / 2, SXB = NT == 1 ? 128 : 256;
-    constexpr int CODES = ROWS * kLine, STAGE = CODES + 256 + SX * SXB, LOADS = ROWS / 8 + SW + SX;
-    static_assert(RING * STAGE >= 2 * NT * 64 * 16, "a wave's sums fit where its stages were");
+    constexpr int W = 4, RING = 3, ROWS = 32 + 16;
+    // loads of scales: 32 rows of a weight, or 16 of either of two; 16 of the pairs (half a load, the other lanes idle)
+    constexpr int SW = GATED ? 2 : 1;
+    constexpr int CODES = ROWS * kLine, STAGE = CODES + ROWS * 8, LOADS = ROWS / 8 + SW + 1;
+    static_assert(RING * STAGE >= 2 * 64 * 16, "a wave's sums fit where its stages were");
     __shared__ __attribute__((aligned(1024))) char lds[W * RING * STAGE];
     Unit u;
-    if (!unit_of<16 * NT>(p, count_units<16 * NT>(p), blockIdx.x / 8, &u)) return;
+    if (!unit_of<16>(p, count_units<16>(p), blockIdx.x / 8, &u)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, kg = lane >> 4;
     const uint32_t kb = p.kb, sb = p.sb;
@@ -506,9 +505,7 @@ skinny_kernel(TileArgs p)
     const int64_t a0 = (int64_t)u.a * WR, R = p.R;
     const uint32_t arow = (uint32_t)(R - a0 < WR ? R - a0 : WR);
 
-    f32x4 acc[2][NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[0][n] = acc[1][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     if (u.e < p.E) {
         const int64_t w0 = u.e * R + a0;
         const u32x4 dc0 = descriptor(p.t.w_codes[0] + w0 * kb, arow * kb), ds0 = descriptor(p.t.w_scales[0] + w0 * sb, arow * sb);
@@ -518,20 +515,17 @@ skinny_kernel(TileArgs p)
         const uint32_t mine = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds)) + wave * (RING * STAGE);
         // a load of codes takes 8 rows; chunk c of row r sits at c ^ (r / 2) % 8
         const int lr = lane / 8, lc = lane & 7;
-        uint32_t vx[2 * NT], kx[2 * NT], vs[SX], ks[SX];
+        uint32_t vx[2], kx[2], vs;
 #pragma unroll
-        for (int i = 0; i < 2 * NT; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int r = 8 * i + lr, c = lc ^ ((r >> 1) & 7);
             const int64_t q = pair_of(p, u, r);
-            kx[i] = q < 0 ? kb : 16 * c;                         // no such column: past the end at once
-            vx[i] = q < 0 ? 0u : ((uint32_t)q / p.share) * kb + kx[i];
+            kx[i] = 16 * c;
+            vx[i] = q < 0 ? kOutOfRange : ((uint32_t)q / p.share) * kb + kx[i];
         }
-#pragma unroll
-        for (int i = 0; i < SX; ++i) {
-            const int r = 32 * i + lane / 2;
-            const int64_t q = r < 16 * NT ? pair_of(p, u, r) : -1;
-            ks[i] = q < 0 ? sb : 4 * (lane & 1);
-            vs[i] = q < 0 ? 0u : ((uint32_t)q / p.share) * sb + ks[i];
+        {
+            const int64_t q = pair_of(p, u, lane / 2);           // lanes past 16 rows are idle
+            vs = q < 0 ? kOutOfRange : ((uint32_t)q / p.share) * sb;
         }
         auto issue = [=](int step, int slot) __attribute__((always_inline)) {
             const uint32_t k = (uint32_t)step * kLine, s = (uint32_t)step * 8, at = mine + slot * STAGE;
@@ -541,17 +535,14 @@ skinny_kernel(TileArgs p)
                 buffer_to_lds(GATED && i >= 2 ? dc1 : dc0, k + 16 * c < kb ? (uint32_t)r * kb + k + 16 * c : kOutOfRange, at + i * 1024);
             }
 #pragma unroll
-            for (int i = 0; i < 2 * NT; ++i)
+            for (int i = 0; i < 2; ++i)
                 buffer_to_lds(dxc, k + kx[i] < kb ? vx[i] + k : kOutOfRange, at + (4 + i) * 1024);
             const uint32_t w = s + 4 * (lane & 1);               // rows past the weight's are out of range
 #pragma unroll
             for (int i = 0; i < SW; ++i)
                 if (!GATED || lane < 32)
                     word_to_lds(i ? ds1 : ds0, w < sb ? (uint32_t)(lane / 2) * sb + w : kOutOfRange, at + CODES + i * 128);
-#pragma unroll
-            for (int i = 0; i < SX; ++i)
-                if (NT > 1 || lane < 32)
-                    word_to_lds(dxs, s + ks[i] < sb ? vs[i] + s : kOutOfRange, at + CODES + 256 + i * SXB);
+            if (lane < 32) word_to_lds(dxs, w < sb ? vs + w : kOutOfRange, at + CODES + 256);
         };
         const uint32_t at0 = mine + j * kLine + ((kg ^ (j >> 1)) << 4), sc0 = mine + CODES + j * 8 + kg;
         const int steps = (int)((kb + kLine - 1) / kLine);
@@ -568,13 +559,10 @@ skinny_kernel(TileArgs p)
                         const uint32_t at = (at0 ^ (h << 6)) + s * STAGE, sc = sc0 + s * STAGE + 4 * h;
                         const i32x4 w0v = *(const MHC_LDS i32x4*)(uintptr_t)at, w1v = *(const MHC_LDS i32x4*)(uintptr_t)(at + 16 * kLine);
                         const int s0 = *(const MHC_LDS uint8_t*)(uintptr_t)sc, s1 = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 128);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const i32x4 x = *(const MHC_LDS i32x4*)(uintptr_t)(at + (32 + 16 * n) * kLine);
-                            const int sx = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 256 + n * 128);
-                            acc[0][n] = mfma4<0, 0>(w0v, x, acc[0][n], s0, sx);
-                            acc[1][n] = mfma4<0, 0>(w1v, x, acc[1][n], s1, sx);
-                        }
+                        const i32x4 x = *(const MHC_LDS i32x4*)(uintptr_t)(at + 32 * kLine);
+                        const int sx = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 256);
+                        acc[0] = mfma4<0, 0>(w0v, x, acc[0], s0, sx);
+                        acc[1] = mfma4<0, 0>(w1v, x, acc[1], s1, sx);
                     }
                     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // read, before the slot is loaded again
                 }
@@ -584,20 +572,17 @@ skinny_kernel(TileArgs p)
     }
     // the sums, each wave's where its stages were
     auto red = [&](int w, int i) { return reinterpret_cast<f32x4*>(lds + w * (RING * STAGE)) + i * 64; };
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        red(wave, 2 * n)[lane] = acc[0][n];
-        red(wave, 2 * n + 1)[lane] = acc[1][n];
-    }
+    red(wave, 0)[lane] = acc[0];
+    red(wave, 1)[lane] = acc[1];
     __syncthreads();
-    if (wave >= NT) return;
-    f32x4 v0 = red(0, 2 * wave)[lane], v1 = red(0, 2 * wave + 1)[lane];   // wave n: columns 16 n ..
+    if (wave > 0) return;
+    f32x4 v0 = red(0, 0)[lane], v1 = red(0, 1)[lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-        v0 += red(w, 2 * wave)[lane];
-        v1 += red(w, 2 * wave + 1)[lane];
+        v0 += red(w, 0)[lane];
+        v1 += red(w, 1)[lane];
     }
-    const int64_t pair = pair_of(p, u, 16 * wave + j), r = a0 + 4 * kg;
+    const int64_t pair = pair_of(p, u, j), r = a0 + 4 * kg;
     if (pair < 0) return;
     if constexpr (GATED) {
         float v[4];
@@ -646,9 +631,7 @@ hipError_t launch_tiles(const Tiling& t, const TileArgs& p, hipStream_t st)
 {
     const dim3 grid((unsigned)t.grid()), block((unsigned)t.threads);
     switch (t.shape) {
-        case kSkinny16: hipLaunchKernelGGL((skinny_kernel<GATED, OUT, 1>), grid, block, 0, st, p); break;
-        case kSkinny32: hipLaunchKernelGGL((skinny_kernel<GATED, OUT, 2>), grid, block, 0, st, p); break;
-        case kSkinny64: hipLaunchKernelGGL((skinny_kernel<GATED, OUT, 4>), grid, block, 0, st, p); break;
+        case kSkinny: hipLaunchKernelGGL((skinny_kernel<GATED, OUT>), grid, block, 0, st, p); break;
         case kSmall: hipLaunchKernelGGL((tile_kernel<GATED, OUT, 2, 2, 4, 4>), grid, block, 0, st, p); break;
         default: hipLaunchKernelGGL((tile_kernel<GATED, OUT, 2, 4, 8, 4>), grid, block, 0, st, p); break;
     }

@@ -41,8 +41,8 @@ struct Geometry {
 };
 
 // A unit: `rows` weight rows (of the gated projection: of both weights together) and up to `cols`
-// pairs of one expert.
-enum Shape { kSkinny16, kSkinny32, kSkinny64, kSmall, kLarge };
+// pairs of one expert. Few pairs: kSkinny, whose workgroups stream the weights past 16 of them.
+enum Shape { kSkinny, kSmall, kLarge };
 struct Tiling {
     int shape = kLarge;
     int rows = 256, cols = 256, threads = 512;
@@ -59,21 +59,32 @@ struct Tiling {
 inline Tiling make_tiling(const Geometry& g)
 {
     Tiling t;
-    const int64_t mean = cdiv(g.P, g.E);
-    if (mean <= 16) t = {kSkinny16, 32, 16, 256};
-    else if (mean <= 32) t = {kSkinny32, 32, 32, 256};
-    else if (mean <= 64) t = {kSkinny64, 32, 64, 256};
-    else {
-        const int64_t rows = g.op == kGlu ? 2 * (int64_t)g.R : g.R;
-        const int64_t nl = cdiv(rows, 256) * (cdiv(g.P, 256) + g.E - 1), ns = cdiv(rows, 128) * (cdiv(g.P, 128) + g.E - 1);
-        if (3 * cdiv(nl, 256) <= 2 * cdiv(ns, 512)) t = {kLarge, 256, 256, 512, 0, 0, kCUs};
-        else t = {kSmall, 128, 128, 256, 0, 0, 2 * kCUs};
-    }
+    const int64_t rows = g.op == kGlu ? 2 * (int64_t)g.R : g.R, steps = cdiv(g.kb(), 128);
+    const int64_t d = g.P < g.E ? g.P : g.E;                     // experts that may have pairs
+    // units along the pairs: every expert's last one half full
+    auto across = [&](int64_t cols) {
+        const int64_t n = g.op == kProduct ? cdiv(g.P, cols) : cdiv(g.P, cols) + d / 2;
+        return n > d ? n : d;
+    };
+    const int64_t nl = cdiv(rows, 256) * across(256), ns = cdiv(rows, 128) * across(128);
+    // What either takes, in us, from the rates measured: HBM 5 MB, weights read again 12 MB, a stage of a small unit 0.85
+    // us. Measured against each other (streaming, small tiles; us a call): K = 7168, N = 16384: T = 1 18, 29, 64 29, 30, 128 50, 30;
+    // K = 14336, N = 4096, T = 128 30, 52; K = 2048, N = 16384, T = 128 31, 17; 64 experts, D = 7168, F = 2048, top 8:
+    // T = 1 27, 37, 8 117, 118, 32 175, 183; D = 4096: T = 1 21, 23, 8 85, 74, 64 155, 120; back to D = 7168: 1 28, 25, 8 110, 81.
+    const double mb = 1e-6 * (double)rows * (double)(g.kb() + g.sb());    // an expert's weights
+    const double once = mb * (double)d, again = mb * (double)(across(16) - d);
+    const double skinny = (once / 5 + again / 12) * (double)(steps + 4) / (double)steps + 3;
+    const double small = (double)cdiv(ns, 2 * kCUs) * (0.85 * (double)steps + 4);
+    if (skinny < (small > once / 5 ? small : once / 5) + once / 20) t = {kSkinny, 32, 16, 256, 0, 0, 0};
+    // A round of large units takes half as long again as one of small ones, two to a compute unit (large, small; us a call): 64 experts,
+    // D = 4096, F = 2048, top 8: T = 512 172, 167, 1024 197, 221, 2048 266, 321; N = K = 4096: T = 2048 37, 32, 4096 50, 55.
+    else if (3 * cdiv(nl, kCUs) <= 2 * cdiv(ns, 2 * kCUs)) t = {kLarge, 256, 256, 512, 0, 0, kCUs};
+    else t = {kSmall, 128, 128, 256, 0, 0, 2 * kCUs};
     // Workgroups that take units in turn send off a unit's first loads before the last one's results are stored, and the stores
     // run beside its first products: T = 16384, K = 4096, N = 16384 643 against 661 us. The gated projection takes
     // one unit each: its activation would hold up the next unit, 714 against 702 us for 65536 pairs, D = 4096, F = 2048.
     if (g.op == kGlu) t.places = 0;
-    t.na = cdiv(g.op == kGlu ? 2 * (int64_t)g.R : g.R, t.rows);
+    t.na = cdiv(rows, t.rows);
     // of the experts' buckets and that of the pairs without one
     t.nb = g.op == kProduct ? cdiv(g.P, t.cols) : g.P / t.cols + g.E + 1;
     if (t.nb > g.P) t.nb = g.P;
