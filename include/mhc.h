@@ -791,7 +791,9 @@ mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_m
  *   mhc_experts_down   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
  * with the weights of E experts in 4 bits, x and h in 16 bits (rounded to 4 into the workspace) or in 4. act as
  * mhc_glu's. h is zero, and adds weights times zero, for pairs without an expert. Sums, activations and
- * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype. A token's result does
+ * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype; but in bf16
+ * the terms that are added up may have been rounded to 11 significant bits (bf16 has 8), or to 2^-39 of
+ * the largest of 32 neighbours where that is more. A token's result does
  * not depend on the other tokens but through the sizes T, E and top_k, which choose the order of the sums.
  *   T >= 0, T * top_k < 2^31; 1 <= E <= 1024; 1 <= top_k <= 32; D, F multiples of 8 in [8, 65536];
  *   of x (T rows of D values) and h (T * top_k rows of F): rows * 16 ceil(width / 32) < 2^31;
@@ -804,7 +806,7 @@ mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_m
  *   weights f32 [T, top_k]      y x_dtype [T, D]
  * 16-bit tensors and codes 16-byte, the others 4-byte aligned. With T == 0 nothing is launched, and
  * the tensors of tokens and pairs may be NULL. Workspace, order and errors as mhc_mxfp4_product's (the
- * workspace of mhc_experts_down holds T * top_k results of D fp32 values too). */
+ * workspace of mhc_experts_down holds T * top_k results of D values in 16 or 32 bits too). */
 typedef struct mhc_experts_params {
     int64_t T;
     int32_t E;

@@ -968,8 +968,9 @@ def mhc_experts_down(h, plan, weights, w_down, *, out=None):
     (h[t, j] w_down[e]^T), e the slot's expert. h [..., top_k, F] (mhc_experts_glu's) in bf16 or fp16, which is rounded
     to 4 bits as mhc_mxfp4 does, or an Mxfp4; plan as there; weights f32 [..., top_k], mhc_route's; w_down
     Mxfp4 [E, D, F]. Returns (or fills) y [..., D] in h's dtype (what mhc_post takes): fp32 sums, in the slots'
-    order, one rounding. A pair without an expert adds its weight times zero. For serving (there is no
-    backward). The workspace is the call's own, with an fp32 result for each pair."""
+    order, one rounding (in bf16 of terms with at least 11 significant bits: include/mhc.h). A pair without an
+    expert adds its weight times zero. For serving (there is no backward). The workspace is the call's own, with a
+    result for each pair."""
     torch = _torch()
     shape, dev, xdt, ptrs = _left(h, "h")
     if not isinstance(w_down, Mxfp4) or w_down.codes.dim() != 3:

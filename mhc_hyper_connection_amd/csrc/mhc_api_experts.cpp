@@ -109,7 +109,10 @@ mhc_status run(const Geometry& g, const Operand& o, mhc::experts::Args a, void* 
         a.x_codes = codes;
         a.x_scales = scales;
     }
-    if (g.op == mhc::experts::kDown) a.part = reinterpret_cast<float*>(ws + w.off_part);
+    if (g.op == mhc::experts::kDown) {
+        a.part = ws + w.off_part;
+        a.part_scales = reinterpret_cast<uint8_t*>(ws + w.off_part_scales);
+    }
     return status_of(mhc::experts::launch_products(g, a, stream));
 }
 

@@ -7,6 +7,11 @@
 // codes and scale bytes as they are in memory: a lane's 16 bytes of codes are one block of 32
 // values, and its scale byte that block's. Products accumulate in fp32; the activation and the
 // weighted sum are fp32, one rounding to the 16-bit result.
+// The weighted sum is a pass of its own over the pairs' results, which wait in the workspace: for bf16 (in tiles) as
+// fp16 with a power of two for each 32 of a pair, by which the largest is in [2^14, 2^15). That keeps 11
+// significant bits down to 2^-28 of the largest, three more than the sum's result has, and halves what is written and
+// read again: 847 to 600 us a call (65536 pairs, D = 4096, F = 2048), and the result's distance from 64 bits, 1.7e-3 of its norm, stays. fp16
+// results, which have 11 bits themselves, and those of few pairs wait in fp32.
 //
 // A unit of work is a run of weight rows and up to a tile's columns of one expert's pairs, which are
 // gathered by the plan's list as their x rows are loaded. Pairs without an expert are a bucket of their own
@@ -22,7 +27,7 @@ namespace mhc {
 namespace experts {
 namespace {
 
-enum Out { kOutBf16, kOutF16, kOutF32 };
+enum Out { kOutBf16, kOutF16, kOutF32, kOutPart };
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -149,6 +154,81 @@ __device__ __forceinline__ bool unit_of(const TileArgs& p, uint32_t total, uint3
     u->cols = scalar((int)(b1 - first < BC ? b1 - first : BC));
     return true;
 }
+// The units of a tiled workgroup, lane n's the n-th (at most 64: the plan sees to it), found before its first loads: a search
+// between two units took 4 us, in which nothing was multiplied. `lds` holds the buckets' beginnings meanwhile.
+struct Units {
+    uint32_t place;        // e, a and cols - 1 in 11, 10 and 8 bits
+    int first;             // -1: no such unit
+    __device__ __forceinline__ bool at(int n, Unit* u) const
+    {
+        const uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)place, n);
+        const int f = __builtin_amdgcn_readlane(first, n);
+        u->e = (int)(w & 0x7ff);
+        u->a = (w >> 11) & 0x3ff;
+        u->cols = (int)(w >> 21) + 1;
+        u->first = f;
+        return f >= 0;
+    }
+};
+constexpr int kUnitsLds = 3 * (kMaxE + 2) * 4;
+template <int BC>
+__device__ __forceinline__ Units units_of(const TileArgs& p, int* lds)
+{
+    const int lane = threadIdx.x & 63;
+    int* const before = lds;                       // units along the pairs before a bucket's
+    int* const begin = lds + kMaxE + 2;
+    int* const end = begin + kMaxE + 2;
+    uint32_t total = (uint32_t)((p.P + BC - 1) / BC);
+    if (p.t.offsets) {
+        if (threadIdx.x < 64) {
+            int at = 0;
+            for (int e0 = 0; e0 <= p.E; e0 += 64) {
+                int b, n;
+                const int tiles = bucket<BC>(p, e0 + lane, &b, &n);
+                int scan = tiles;
+#pragma unroll
+                for (int d = 1; d < 64; d *= 2) {
+                    const int o = __shfl_up(scan, d);
+                    if (lane >= d) scan += o;
+                }
+                if (e0 + lane <= p.E) {
+                    before[e0 + lane] = at + scan - tiles;
+                    begin[e0 + lane] = b;
+                    end[e0 + lane] = n;
+                }
+                at += __builtin_amdgcn_readlane(scan, 63);
+            }
+            if (lane == 0) before[p.E + 1] = at;
+        }
+        __syncthreads();
+        total = (uint32_t)before[p.E + 1];
+    }
+    const uint32_t units = total * p.na, per = (units + 7) / 8, i = blockIdx.x / 8 + (uint32_t)lane * (gridDim.x / 8), unit = blockIdx.x % 8 * per + i;
+    Units u = {0, -1};
+    if (i < per && unit < units) {
+        uint32_t a, b;
+        int e = 0, b0 = 0, b1 = (int)p.P;
+        if (p.t.offsets) {
+            const int q = (int)(unit / p.na);
+            int up = p.E + 1;                      // before[e] <= q < before[up]
+            while (up - e > 1) {
+                const int mid = (e + up) / 2;
+                if (before[mid] <= q) e = mid;
+                else up = mid;
+            }
+            b0 = begin[e];
+            b1 = end[e];
+            place(unit - (uint32_t)before[e] * p.na, p.na, (uint32_t)(before[e + 1] - before[e]), &a, &b);
+        } else place(unit, p.na, total, &a, &b);
+        const int64_t first = b0 + (int64_t)b * BC;
+        if (first >= b0 && first < b1) {           // of a plan's offsets always
+            u.first = (int)first;
+            u.place = (uint32_t)e | a << 11 | (uint32_t)((b1 - first < BC ? (int)(b1 - first) : BC) - 1) << 21;
+        }
+    }
+    __syncthreads();
+    return u;
+}
 // The pair in column c of the unit; -1 past its columns (and for what is no pair).
 __device__ __forceinline__ int64_t pair_of(const TileArgs& p, const Unit& u, int c)
 {
@@ -166,7 +246,7 @@ __device__ __forceinline__ void store_results(const TileArgs& p, int64_t pair, i
     if constexpr (OUT == kOutF32) {
 #pragma unroll
         for (int h = 0; h < N / 4; ++h)
-            *reinterpret_cast<f32x4*>(p.t.part + pair * p.R + r + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+            *reinterpret_cast<f32x4*>(static_cast<float*>(p.t.part) + pair * p.R + r + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
     } else {
         uint16_t* const out = static_cast<uint16_t*>(p.t.out) + pair * p.R + r;
         uint32_t w[N / 2];
@@ -176,6 +256,28 @@ __device__ __forceinline__ void store_results(const TileArgs& p, int64_t pair, i
         else *reinterpret_cast<u32x2*>(out) = u32x2{w[0], w[1]};
     }
 }
+
+// The exponent field of the largest magnitude among 32 results of a column, eight in each of four lanes 16 apart; at least
+// 15, so that the powers of two below are normal numbers. 255: an infinity or a NaN, which stay what they are.
+__device__ __forceinline__ uint32_t exponent_of(f32x4 a, f32x4 b)
+{
+    // as whole numbers, which order like the values, NaN above all
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t x = __float_as_uint(a[e]) & 0x7fffffffu, y = __float_as_uint(b[e]) & 0x7fffffffu;
+        m = m > x ? m : x;
+        m = m > y ? m : y;
+    }
+    const auto s = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = s[0] > s[1] ? s[0] : s[1];
+    const auto t = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = (t[0] > t[1] ? t[0] : t[1]) >> 23;
+    return m < 15 ? 15 : m;
+}
+// The power of two that takes such results to [2^14, 2^15), and back.
+__device__ __forceinline__ uint32_t part_up(uint32_t exponent) { return (268u - exponent) << 23; }
+__device__ __forceinline__ uint32_t part_down(uint32_t exponent) { return (exponent - 14u) << 23; }
 
 // WA x WB waves of IA x IB 16 x 16 results each; rows: weights (gated: gate and up side by side, so that a wave
 // holds both of the same f), columns: pairs. A stage of the reduction is 256 values: a row's 128 bytes
@@ -317,10 +419,11 @@ tile_kernel(TileArgs p)
     };
 
     const int steps = (int)((kb + kLine - 1) / kLine);
-    const uint32_t total = (uint32_t)scalar((int)count_units<BC>(p));
-    uint32_t i0 = blockIdx.x / 8;
+    static_assert(BC <= 256 && kUnitsLds <= (int)sizeof(lds), "a unit's columns in 8 bits, the buckets where the stages go");
+    const Units mine = units_of<BC>(p, reinterpret_cast<int*>(lds));
+    int n = 0;
     Unit u, next;
-    if (!unit_of<BC>(p, total, i0, &u)) return;
+    if (!mine.at(0, &u)) return;
     Loads l;
     if (u.e < p.E) {
         set_up(lane, u, l);
@@ -333,11 +436,7 @@ tile_kernel(TileArgs p)
         for (int i = 0; i < IA; ++i)
 #pragma unroll
             for (int q = 0; q < IB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-        bool more = false;
-        if constexpr (!GATED) {
-            i0 += gridDim.x / 8;
-            more = unit_of<BC>(p, total, i0, &next);             // while this unit's first loads are on their way
-        }
+        const bool more = !GATED && ++n < 64 && mine.at(n, &next);
 
         if (u.e < p.E) {
             Operands op[2];
@@ -448,8 +547,10 @@ tile_kernel(TileArgs p)
             for (int c = 0; c < 16 / NC; ++c) pair[q][c] = (int)pair_of(p, u, 16 * (wb * IB + q) + NC * c + ln / LC);
         wait_loads_and_barrier<0>();
         auto from = [](int lane4, uint32_t v) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_ds_bpermute(lane4, (int)v); };
+        const int64_t RS = part_scales(R);
 #pragma unroll
         for (int q = 0; q < IB; ++q) {
+            uint32_t exponent = 0;       // of run kg
 #pragma unroll
             for (int i = 0; i < IA / 2; ++i) {
                 if constexpr (OUT == kOutF32) {
@@ -463,18 +564,31 @@ tile_kernel(TileArgs p)
                             const uint32_t lo = from(src, __float_as_uint(acc[2 * i][q][e])), hi = from(src, __float_as_uint(acc[2 * i + 1][q][e]));
                             w[e] = ln & 1 ? hi : lo;
                         }
-                        if (pair[q][c] >= 0 && f < R) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p.t.part + (int64_t)pair[q][c] * R + f));
+                        if (pair[q][c] >= 0 && f < R) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<float*>(p.t.part) + (int64_t)pair[q][c] * R + f));
                     }
                 } else {
                     const int64_t f = a0 + 32 * i + 8 * (ln & 3);
                     const int src = 4 * (ln / 4 + 16 * (ln & 3));
+                    float scale = 1.f;
+                    if constexpr (OUT == kOutPart) {
+                        const uint32_t e = exponent_of(acc[2 * i][q], acc[2 * i + 1][q]);
+                        scale = __uint_as_float(part_up(e));
+                        exponent = (ln >> 4) == i ? e : exponent;
+                    }
                     u32x4 w;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = from(src, pack_x16<OUT == kOutF16>(acc[2 * i + e / 2][q][2 * (e % 2)], acc[2 * i + e / 2][q][2 * (e % 2) + 1]));
+                    for (int e = 0; e < 4; ++e) {
+                        const float lo = acc[2 * i + e / 2][q][2 * (e % 2)], hi = acc[2 * i + e / 2][q][2 * (e % 2) + 1];
+                        w[e] = from(src, OUT == kOutPart ? pack_f16x2(lo * scale, hi * scale) : pack_x16<OUT == kOutF16>(lo, hi));
+                    }
                     if (pair[q][0] >= 0 && f < R)
-                        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.t.out) + (int64_t)pair[q][0] * R + f));
+                        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(OUT == kOutPart ? p.t.part : p.t.out) + (int64_t)pair[q][0] * R + f));
                 }
+            }
+            if constexpr (OUT == kOutPart) {
+                const uint32_t e = from(4 * (ln / 4 + 16 * (ln & 3)), exponent);
+                const int64_t run = a0 / 32 + (ln & 3);
+                if (pair[q][0] >= 0 && (ln & 3) < IA / 2 && run < RS) p.t.part_scales[(int64_t)pair[q][0] * RS + run] = (uint8_t)e;
             }
         }
         if (!more) break;
@@ -602,9 +716,10 @@ skinny_kernel(TileArgs p)
 }
 
 // A token's results by its weights: fp32 terms in the order of its slots, one rounding. A thread takes eight values.
-template <bool H>
+template <bool H, bool PART>
 __global__ void __launch_bounds__(256)
-combine_kernel(const float* __restrict__ part, const float* __restrict__ weights, uint16_t* __restrict__ out, int64_t T, int k, int R)
+combine_kernel(const void* __restrict__ part, const uint8_t* __restrict__ scales, const float* __restrict__ weights, uint16_t* __restrict__ out, int64_t T, int k,
+               int R)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int octets = R / 8;
@@ -614,13 +729,24 @@ combine_kernel(const float* __restrict__ part, const float* __restrict__ weights
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int s = 0; s < k; ++s) {
-        const f32x4* const row = reinterpret_cast<const f32x4*>(part + (t * k + s) * R + r);
-        const f32x4 a = row[0], b = row[1];
-        const float w = weights[t * k + s];
+        const int64_t row = t * k + s;
+        const float w = weights[row];
+        if constexpr (PART) {
+            const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(part) + row * R + r));
+            const float x = __uint_as_float(part_down(scales[row * part_scales(R) + r / 32]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[e] = fmaf(w, a[e], v[e]);
-            v[4 + e] = fmaf(w, b[e], v[4 + e]);
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = fmaf(w, f16_lo(a[e]) * x, v[2 * e]);
+                v[2 * e + 1] = fmaf(w, f16_hi(a[e]) * x, v[2 * e + 1]);
+            }
+        } else {
+            const f32x4* const at = reinterpret_cast<const f32x4*>(static_cast<const float*>(part) + row * R + r);
+            const f32x4 a = at[0], b = at[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = fmaf(w, a[e], v[e]);
+                v[4 + e] = fmaf(w, b[e], v[4 + e]);
+            }
         }
     }
     *reinterpret_cast<u32x4*>(out + t * R + r) = u32x4{pack_x16<H>(v[0], v[1]), pack_x16<H>(v[2], v[3]), pack_x16<H>(v[4], v[5]), pack_x16<H>(v[6], v[7])};
@@ -631,7 +757,9 @@ hipError_t launch_tiles(const Tiling& t, const TileArgs& p, hipStream_t st)
 {
     const dim3 grid((unsigned)t.grid()), block((unsigned)t.threads);
     switch (t.shape) {
-        case kSkinny: hipLaunchKernelGGL((skinny_kernel<GATED, OUT>), grid, block, 0, st, p); break;
+        case kSkinny:
+            if constexpr (OUT != kOutPart) hipLaunchKernelGGL((skinny_kernel<GATED, OUT>), grid, block, 0, st, p);
+            break;
         case kSmall: hipLaunchKernelGGL((tile_kernel<GATED, OUT, 2, 2, 4, 4>), grid, block, 0, st, p); break;
         default: hipLaunchKernelGGL((tile_kernel<GATED, OUT, 2, 4, 8, 4>), grid, block, 0, st, p); break;
     }
@@ -648,12 +776,16 @@ int launch_products(const Geometry& g, const Args& a, void* stream)
     const TileArgs p = {a, g.P, g.E, g.R, g.act, (uint32_t)g.kb(), (uint32_t)g.sb(), (uint32_t)t.na, (uint32_t)g.share, (uint32_t)g.X};
     if (g.op == kGlu) return (int)(g.f16 ? launch_tiles<true, kOutF16>(t, p, st) : launch_tiles<true, kOutBf16>(t, p, st));
     if (g.op == kProduct) return (int)(g.f16 ? launch_tiles<false, kOutF16>(t, p, st) : launch_tiles<false, kOutBf16>(t, p, st));
-    hipError_t e = launch_tiles<false, kOutF32>(t, p, st);
+    const bool in16 = parts_in_16_bits(g);
+    const hipError_t e = in16 ? launch_tiles<false, kOutPart>(t, p, st) : launch_tiles<false, kOutF32>(t, p, st);
     if (e != hipSuccess) return (int)e;
     const int64_t T = g.P / a.top_k;
-    const dim3 grid((unsigned)cdiv(T * (g.R / 8), 256));
-    if (g.f16) hipLaunchKernelGGL(combine_kernel<true>, grid, dim3(256), 0, st, a.part, a.weights, static_cast<uint16_t*>(a.out), T, (int)a.top_k, g.R);
-    else hipLaunchKernelGGL(combine_kernel<false>, grid, dim3(256), 0, st, a.part, a.weights, static_cast<uint16_t*>(a.out), T, (int)a.top_k, g.R);
+    const dim3 grid((unsigned)cdiv(T * (g.R / 8), 256)), block(256);
+    uint16_t* const out = static_cast<uint16_t*>(a.out);
+    const int k = (int)a.top_k;
+    if (in16) hipLaunchKernelGGL((combine_kernel<false, true>), grid, block, 0, st, a.part, a.part_scales, a.weights, out, T, k, g.R);
+    else if (g.f16) hipLaunchKernelGGL((combine_kernel<true, false>), grid, block, 0, st, a.part, a.part_scales, a.weights, out, T, k, g.R);
+    else hipLaunchKernelGGL((combine_kernel<false, false>), grid, block, 0, st, a.part, a.part_scales, a.weights, out, T, k, g.R);
     return (int)hipGetLastError();
 }
 

@@ -52,7 +52,9 @@ struct Tiling {
     int64_t grid() const
     {
         const int64_t n = 8 * cdiv(na * nb, 8);
-        return places && n > places ? places : n;
+        if (!places || n <= places) return n;
+        const int64_t least = 8 * cdiv(n, 8 * 64);       // a workgroup knows 64 of its units
+        return places > least ? places : least;
     }
 };
 
@@ -106,8 +108,13 @@ inline bool valid(const Geometry& g)
     return t.na * t.nb + 8 < (int64_t)1 << 23;     // workgroups of at most 512 threads within a grid's 2^32 - 1
 }
 
+// The projection back: whether the pairs' results, which the weighted sum reads, are kept in 16 bits, 11 of them
+// significant, with a power of two for each 32 (mhc_experts.hip): for bf16, which has 8, in tiles.
+inline bool parts_in_16_bits(const Geometry& g) { return g.op == kDown && !g.f16 && make_tiling(g).shape != kSkinny; }
+MHC_EXPERTS_HOST_DEVICE inline int64_t part_scales(int64_t R) { return (R + 31) / 32; }
+
 struct Workspace {
-    size_t off_codes = 0, off_scales = 0, off_part = 0, bytes = 0;
+    size_t off_codes = 0, off_scales = 0, off_part = 0, off_part_scales = 0, bytes = 0;
 };
 // quantise: x comes in 16 bits
 inline Workspace make_workspace(const Geometry& g, bool quantise)
@@ -119,7 +126,10 @@ inline Workspace make_workspace(const Geometry& g, bool quantise)
     w.off_scales = off;
     if (quantise) off = align_up(off + (size_t)g.X * (size_t)g.sb(), 256);
     w.off_part = off;
-    if (g.op == kDown) off = align_up(off + (size_t)g.P * (size_t)g.R * 4, 256);
+    const bool in16 = parts_in_16_bits(g);
+    if (g.op == kDown) off = align_up(off + (size_t)g.P * (size_t)g.R * (in16 ? 2 : 4), 256);
+    w.off_part_scales = off;
+    if (in16) off = align_up(off + (size_t)g.P * (size_t)part_scales(g.R), 256);
     w.bytes = off;
     return w;
 }
@@ -144,7 +154,8 @@ struct Args {
     const int32_t* pairs;         // [P]
     const float* weights;         // [P] (kDown)
     void* out;                    // [P, R] 16-bit (kDown: [P / k, R])
-    float* part;                  // kDown: [P, R]
+    void* part;                   // kDown: [P, R] fp32, or 16-bit with part_scales
+    uint8_t* part_scales;         // [P, ceil(R / 32)]
     int64_t top_k;                // kDown
 };
 

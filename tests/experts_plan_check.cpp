@@ -41,7 +41,9 @@ static int check_units(const experts::Geometry& g, const std::vector<int64_t>& l
     if (!t.places && (per - 1) * 8 + 7 >= grid && units > 0) return fail("grid", per, grid);
     std::vector<char> seen((size_t)units, 0);
     for (int64_t b = 0; b < grid; ++b) {
+      int64_t taken = 0;
       for (int64_t i = b / 8; i < per; i += t.places ? grid / 8 : per) {
+        if (++taken > 64) return fail("a workgroup's units", grid, per);
         const int64_t u = (b % 8) * per + i;
         if (u >= units) break;
         const int64_t q = u / t.na;
@@ -84,7 +86,9 @@ int main()
         if (check_units(g, one)) return 1;
         for (int q = 0; q < 2; ++q) {
             const experts::Workspace w = experts::make_workspace(g, q == 1);
-            const int64_t need = (q ? g.X * (g.kb() + g.sb()) : 0) + (g.op == experts::kDown ? g.P * g.R * 4 : 0);
+            const bool in16 = experts::parts_in_16_bits(g);
+            const int64_t need = (q ? g.X * (g.kb() + g.sb()) : 0) + (g.op != experts::kDown ? 0 : in16 ? g.P * g.R * 2 + g.P * experts::part_scales(g.R) : g.P * g.R * 4);
+            if (in16 && (w.off_part_scales % 256 || (int64_t)(w.off_part_scales - w.off_part) < g.P * g.R * 2)) return fail("parts", g.P, g.R);
             if ((int64_t)w.bytes < need || w.off_codes % 256 || w.off_scales % 256 || w.off_part % 256) return fail("workspace", (long long)w.bytes, need);
             if (q && (int64_t)(w.off_scales - w.off_codes) < g.X * g.kb()) return fail("codes", (long long)w.off_scales, g.X);
             if (q && g.op == experts::kDown && (int64_t)(w.off_part - w.off_scales) < g.X * g.sb()) return fail("scales", (long long)w.off_part, g.X);

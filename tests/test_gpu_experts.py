@@ -1,10 +1,13 @@
 """The products with 4-bit weights on the GPU against the definition in 64 bits.
 
 Where codes and scale bytes are such that every partial sum is a whole number of a quantum and within 2^24 of them, fp32 sums are
-exact in any order, and results are the correctly rounded ones, bit for bit. Else a sum of K products whose magnitudes add up
+exact in any order, and results are the correctly rounded ones, bit for bit (of the weighted sum in fp16: bf16's terms are first
+rounded to 11 bits). Else a sum of K products whose magnitudes add up
 to A is off by experts_helpers.sum_error(K, A), and the gated projection's h, with eg and eu for g and u, by 1.13 eg |u| +
 |act(g)| eu + 2^-21 |h| before its rounding (|act'| is at most 1.13; 2^-21 for the exponential, the reciprocal and the
-products). The weighted sum of k terms adds k 2^-24 of their magnitudes."""
+products). The weighted sum of k terms adds k 2^-24 of their magnitudes, and in bf16 each term has been rounded to fp16 under the power
+of two that takes the largest of 32 to [2^14, 2^15): by 2^-11 of itself, or half of fp16's least step, 2^-25, under that power: 2^-39 of
+the largest of 32 at most."""
 import sys
 
 import numpy as np
@@ -33,6 +36,13 @@ def a_plan(e, E, dev):
     import mhc_hyper_connection_amd as mhc
     o, p = plan(e, E)
     return mhc.ExpertsPlan(to_dev(o, dev), to_dev(p, dev), e.shape)
+
+
+def part_error(v):
+    """What rounding the pairs' results v [P, D] to 16 bits adds, at most."""
+    P, D = v.shape
+    b = np.pad(np.abs(v), ((0, 0), (0, -D % 32))).reshape(P, -1, 32).max(-1)
+    return 2.0 ** -11 * np.abs(v) + 2.0 ** -39 * np.repeat(b, 32, -1)[:, :D]
 
 
 def is_exact(x, w, quantum, K):
@@ -123,7 +133,10 @@ def test_experts(T, k, E, D, F, f16):
         at = flat == x
         y[at], mag[at] = hv[at] @ dv[x].T, np.abs(hv[at]) @ np.abs(dv[x]).T
     wt = weights.astype(float).reshape(T * k, 1)
-    lim = (wt * sum_error(F, mag)).reshape(T, k, D).sum(1) + (k + 1) * U * (wt * np.abs(y)).reshape(T, k, D).sum(1)
+    err = sum_error(F, mag)
+    if not f16:
+        err = err + part_error(np.abs(y) + err)
+    lim = (wt * err).reshape(T, k, D).sum(1) + (k + 1) * U * (wt * np.abs(y)).reshape(T, k, D).sum(1)
     want = (wt * y).reshape(T, k, D).sum(1)
     down = to_mxfp4(*wd, F, f16, dev)
     full = torch.full((T + 1, D), 7.0, dtype=dt, device=dev)
@@ -150,8 +163,40 @@ def test_exact_sums_with_uneven_loads(E, loads):
     assert is_exact(hv, wv, 0.25, F)
     print(f"[case] loads {loads[:8]}", file=sys.stderr, flush=True)
     want = np.stack([hv[t] @ wv[x].T if x >= 0 else np.zeros(D) for t, x in enumerate(e[:, 0])])
-    y = mhc.mhc_experts_down(to_mxfp4(*h, F, False, dev), p, torch.ones((T, 1), device=dev), to_mxfp4(*w, F, False, dev))
-    assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.bfloat16))
+    ones = torch.ones((T, 1), device=dev)
+    y = mhc.mhc_experts_down(to_mxfp4(*h, F, True, dev), p, ones, to_mxfp4(*w, F, True, dev))
+    assert torch.equal(y.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.float16))
+    y = mhc.mhc_experts_down(to_mxfp4(*h, F, False, dev), p, ones, to_mxfp4(*w, F, False, dev))
+    check("y", y, want, part_error(want), False)
+
+
+@pytest.mark.parametrize("T,E", [(3, 2), (70, 3), (900, 2)])
+def test_results_of_any_size_in_bf16(T, E):
+    # results far past fp16's range, and neighbours far smaller; an infinite and a NaN one
+    import mhc_hyper_connection_amd as mhc
+    import torch
+    dev = device()
+    rng = np.random.default_rng(T)
+    F, D, k = 64, 200, 2
+    e = some_experts(rng, T, k, E, masked=False)
+    h, w = mxfp4(rng, T, k, F, low=127, high=129), mxfp4(rng, E, D, F, low=127, high=129)
+    # a row's power of two: in the first columns to 2^60 apart, then even, then near the ends of fp32's range
+    up = np.concatenate([rng.integers(-30, 31, 96), np.zeros(32), np.full(36, 110), np.full(36, -115)]).astype(int)
+    w[1][..., :2] = np.clip(w[1][..., :2].astype(int) + up[None, :, None], 0, 254)
+    h[1][0, 0, 0] = 255
+    hv, wv = values(*h, F).reshape(T * k, F), values(*w, F)
+    flat = e.reshape(-1)
+    y, mag = np.zeros((T * k, D)), np.zeros((T * k, D))
+    for x in range(E):
+        y[flat == x], mag[flat == x] = hv[flat == x] @ wv[x].T, np.abs(hv[flat == x]) @ np.abs(wv[x]).T
+    wt = rng.random((T, k)).astype(np.float32)
+    print(f"[case] any size T={T} E={E}", file=sys.stderr, flush=True)
+    got = mhc.mhc_experts_down(to_mxfp4(*h, F, False, dev), a_plan(e, E, dev), to_dev(wt, dev), to_mxfp4(*w, F, False, dev))
+    wd = wt.astype(float).reshape(T * k, 1)
+    err = sum_error(F, mag)
+    err = err + part_error(np.abs(y) + err) + 2.0 ** -149
+    lim = (wd * err).reshape(T, k, D).sum(1) + (k + 1) * U * (wd * np.abs(y)).reshape(T, k, D).sum(1)
+    check("y", got, (wd * y).reshape(T, k, D).sum(1), lim, False)
 
 
 def test_nan_and_infinity_stay_in_their_rows():
