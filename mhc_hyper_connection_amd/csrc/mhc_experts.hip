@@ -292,7 +292,7 @@ __device__ __forceinline__ uint32_t part_down(uint32_t exponent) { return (expon
 //                            group's last stage) a third of those of the next group's scales
 // Loads past the end of the reduction bring zeros.
 template <bool GATED, int OUT, int WA, int WB, int IA, int IB>
-__global__ void __launch_bounds__(64 * WA * WB, WA * WB == 4 && IA * IB == 64 ? 1 : 2)
+__global__ void __launch_bounds__(64 * WA * WB, 2)
 tile_kernel(TileArgs p)
 {
     constexpr int NW = WA * WB;
@@ -533,20 +533,33 @@ tile_kernel(TileArgs p)
             else results(Number<0>{});
             return;
         }
-        // They are stored once the next unit's first loads are there, and are on their way while its first stages are
-        // multiplied. A store takes four (fp32: eight) neighbouring lanes to a column, whose 16-byte pieces are one run of memory.
+        // A store takes eight neighbouring lanes to a column, whose 16-byte pieces are a whole line of memory (of two runs of 32
+        // 16-bit results, or one of fp32); stored from where they are, 16 lanes apart and half a line at a time, they took longer:
+        // 592 against 571 us for T = 16384, K = 4096, N = 16384, and 634 through the caches. (The gated projection's stores go out
+        // between the activations, and gain nothing by it.)
+        auto from = [](int lane4, uint32_t v) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_ds_bpermute(lane4, (int)v); };
+        // columns 8 c .. of a block of 16: piece ln % 8 of column ln / 8, of run 0 (w) or 1 (v) of the two
+        auto line = [=](int c, const uint32_t (&w)[4], const uint32_t (&v)[4]) __attribute__((always_inline)) {
+            const int src = 4 * (8 * c + ln / 8 + 16 * (ln & 3));
+            u32x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = from(src, w[e]), y = from(src, v[e]);
+                o[e] = ln & 4 ? y : x;
+            }
+            return o;
+        };
+        // They are stored once the next unit's first loads are there, and are on their way while its first stages are multiplied.
         if (more && next.e < p.E) {
             set_up(ln, next, l);
             first_loads(l);
         }
-        constexpr int LC = OUT == kOutF32 ? 8 : 4, NC = 64 / LC; // lanes to a column, columns to a store
-        int pair[IB][16 / NC];
+        int pair[IB][2];
 #pragma unroll
         for (int q = 0; q < IB; ++q)
 #pragma unroll
-            for (int c = 0; c < 16 / NC; ++c) pair[q][c] = (int)pair_of(p, u, 16 * (wb * IB + q) + NC * c + ln / LC);
+            for (int c = 0; c < 2; ++c) pair[q][c] = (int)pair_of(p, u, 16 * (wb * IB + q) + 8 * c + ln / 8);
         wait_loads_and_barrier<0>();
-        auto from = [](int lane4, uint32_t v) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_ds_bpermute(lane4, (int)v); };
         const int64_t RS = part_scales(R);
 #pragma unroll
         for (int q = 0; q < IB; ++q) {
@@ -566,29 +579,41 @@ tile_kernel(TileArgs p)
                         }
                         if (pair[q][c] >= 0 && f < R) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<float*>(p.t.part) + (int64_t)pair[q][c] * R + f));
                     }
-                } else {
-                    const int64_t f = a0 + 32 * i + 8 * (ln & 3);
-                    const int src = 4 * (ln / 4 + 16 * (ln & 3));
-                    float scale = 1.f;
+                } else if (i % 2 == 0) {
+                    float scale[2] = {1.f, 1.f};
                     if constexpr (OUT == kOutPart) {
-                        const uint32_t e = exponent_of(acc[2 * i][q], acc[2 * i + 1][q]);
-                        scale = __uint_as_float(part_up(e));
-                        exponent = (ln >> 4) == i ? e : exponent;
-                    }
-                    u32x4 w;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float lo = acc[2 * i + e / 2][q][2 * (e % 2)], hi = acc[2 * i + e / 2][q][2 * (e % 2) + 1];
-                        w[e] = from(src, OUT == kOutPart ? pack_f16x2(lo * scale, hi * scale) : pack_x16<OUT == kOutF16>(lo, hi));
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t e = exponent_of(acc[2 * i + 2 * h][q], acc[2 * i + 2 * h + 1][q]);
+                            scale[h] = __uint_as_float(part_up(e));
+                            exponent = (ln >> 4) == i + h ? e : exponent;
+                        }
                     }
-                    if (pair[q][0] >= 0 && f < R)
-                        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(OUT == kOutPart ? p.t.part : p.t.out) + (int64_t)pair[q][0] * R + f));
+                    uint32_t w[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float lo = acc[2 * i + 2 * h + e / 2][q][2 * (e % 2)], hi = acc[2 * i + 2 * h + e / 2][q][2 * (e % 2) + 1];
+                            w[h][e] = OUT == kOutPart ? pack_f16x2(lo * scale[h], hi * scale[h]) : pack_x16<OUT == kOutF16>(lo, hi);
+                        }
+                    const int64_t f = a0 + 32 * i + 8 * (ln & 7);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const u32x4 o = line(c, w[0], w[1]);
+                        if (pair[q][c] >= 0 && f < R)
+                            __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(OUT == kOutPart ? p.t.part : p.t.out) + (int64_t)pair[q][c] * R + f));
+                    }
                 }
             }
             if constexpr (OUT == kOutPart) {
-                const uint32_t e = from(4 * (ln / 4 + 16 * (ln & 3)), exponent);
-                const int64_t run = a0 / 32 + (ln & 3);
-                if (pair[q][0] >= 0 && (ln & 3) < IA / 2 && run < RS) p.t.part_scales[(int64_t)pair[q][0] * RS + run] = (uint8_t)e;
+                // a byte for each run of the wave's
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t e = from(4 * (8 * c + ln / 8 + 16 * (ln & 3)), exponent);
+                    const int64_t run = a0 / 32 + (ln & 3);
+                    if (pair[q][c] >= 0 && (ln & 7) < IA / 2 && run < RS) p.t.part_scales[(int64_t)pair[q][c] * RS + run] = (uint8_t)e;
+                }
             }
         }
         if (!more) break;
