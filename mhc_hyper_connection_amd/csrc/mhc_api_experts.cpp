@@ -100,9 +100,11 @@ mhc_status run(const Geometry& g, const Operand& o, mhc::experts::Args a, void* 
         if (!aligned(workspace, 256) || workspace_bytes < w.bytes) return MHC_ERR_PARAM_INVALID;
     }
     char* const ws = static_cast<char*>(workspace);
+    const mhc::experts::Tiling t = mhc::experts::make_tiling(g, o.x != nullptr);
     a.x_codes = o.codes;
     a.x_scales = o.scales;
-    if (o.x) {
+    if (t.rounds_x) a.x = o.x;
+    else if (o.x) {
         uint8_t* const codes = reinterpret_cast<uint8_t*>(ws + w.off_codes);
         uint8_t* const scales = reinterpret_cast<uint8_t*>(ws + w.off_scales);
         if (mhc::mx::launch_quantise(g.X, g.K, o.x, codes, scales, g.f16, stream) != 0) return MHC_ERR_RUNTIME;
@@ -113,7 +115,7 @@ mhc_status run(const Geometry& g, const Operand& o, mhc::experts::Args a, void* 
         a.part = ws + w.off_part;
         a.part_scales = reinterpret_cast<uint8_t*>(ws + w.off_part_scales);
     }
-    return status_of(mhc::experts::launch_products(g, a, stream));
+    return status_of(mhc::experts::launch_products(g, t, a, stream));
 }
 
 }  // namespace

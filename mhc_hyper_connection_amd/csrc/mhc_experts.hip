@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "mhc_experts_plan.h"
+#include "mhc_mxfp4_device.h"
 #include "mhc_tile_device.h"
 
 namespace mhc {
@@ -31,7 +32,6 @@ enum Out { kOutBf16, kOutF16, kOutF32, kOutPart };
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kLine = 128;            // bytes of a row's codes in a stage: 256 values, 8 scale bytes
 
@@ -69,6 +69,7 @@ struct TileArgs {
     uint32_t kb, sb;       // bytes of a row's codes and scales
     uint32_t na, share;
     uint32_t x_rows;
+    int K, cols, f16;      // cols: of a streaming unit; f16: x's format
 };
 
 // A unit: of expert e the units' row a and the pairs [first, first + cols). An XCD (workgroups b, b + 8, ..) takes a
@@ -88,8 +89,7 @@ __device__ __forceinline__ int scalar(int x)
     return s;
 }
 // A bucket's first and last pair and its units of BC pairs; bucket E: the pairs without an expert.
-template <int BC>
-__device__ __forceinline__ int bucket(const TileArgs& p, int e, int* begin, int* end)
+__device__ __forceinline__ int bucket(const TileArgs& p, int BC, int e, int* begin, int* end)
 {
     const int P = (int)p.P;
     const int b = e <= p.E ? p.t.offsets[e] : P, n = e < p.E ? p.t.offsets[e + 1] : P;
@@ -97,23 +97,21 @@ __device__ __forceinline__ int bucket(const TileArgs& p, int e, int* begin, int*
     *end = n < *begin ? *begin : (n > P ? P : n);
     return (int)(((int64_t)*end - *begin + BC - 1) / BC);
 }
-template <int BC>
-__device__ __forceinline__ uint32_t count_units(const TileArgs& p)   // along the pairs
+__device__ __forceinline__ uint32_t count_units(const TileArgs& p, int BC)   // along the pairs
 {
     if (!p.t.offsets) return (uint32_t)((p.P + BC - 1) / BC);
     const int lane = threadIdx.x & 63;
     uint32_t total = 0;
     for (int e0 = 0; e0 <= p.E; e0 += 64) {
-        int begin, end, n = bucket<BC>(p, e0 + lane, &begin, &end);
+        int begin, end, n = bucket(p, BC, e0 + lane, &begin, &end);
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
         total += (uint32_t)__builtin_amdgcn_readfirstlane(n);
     }
     return total;
 }
-// Unit i of this workgroup's XCD, of total x na in all; false past the last.
-template <int BC>
-__device__ __forceinline__ bool unit_of(const TileArgs& p, uint32_t total, uint32_t i, Unit* u)
+// Unit i of this XCD's (the streaming kernel's), of total x na in all; false past the last.
+__device__ __forceinline__ bool unit_of(const TileArgs& p, int BC, uint32_t total, uint32_t i, Unit* u)
 {
     const int lane = threadIdx.x & 63;
     const uint32_t units = total * p.na, per = (units + 7) / 8, unit = blockIdx.x % 8 * per + i;
@@ -126,7 +124,7 @@ __device__ __forceinline__ bool unit_of(const TileArgs& p, uint32_t total, uint3
         uint32_t at = 0;
         for (int e0 = 0; e0 <= p.E; e0 += 64) {
             int begin, end;
-            const int n = bucket<BC>(p, e0 + lane, &begin, &end);
+            const int n = bucket(p, BC, e0 + lane, &begin, &end);
             int scan = n;
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
@@ -184,7 +182,7 @@ __device__ __forceinline__ Units units_of(const TileArgs& p, int* lds)
             int at = 0;
             for (int e0 = 0; e0 <= p.E; e0 += 64) {
                 int b, n;
-                const int tiles = bucket<BC>(p, e0 + lane, &b, &n);
+                const int tiles = bucket(p, BC, e0 + lane, &b, &n);
                 int scan = tiles;
 #pragma unroll
                 for (int d = 1; d < 64; d *= 2) {
@@ -624,19 +622,21 @@ tile_kernel(TileArgs p)
 // Few pairs of an expert (16 at most to a unit): reading the weights once is the whole cost. A
 // workgroup takes 32 weight rows (gated: 16 of either weight), its W waves every W-th stage of 256 values; their
 // sums meet in LDS and are added in wave order. A wave keeps a ring of three stages of its own in LDS,
-// so that it waits for its own loads only and meets the others once.
-template <bool GATED, int OUT>
+// so that it waits for its own loads only and meets the others once. X16: the pairs' x rows come in 16 bits and are rounded into
+// LDS, behind the first loads of weights, once for all their stages.
+template <bool GATED, int OUT, bool X16>
 __global__ void __launch_bounds__(256)
 skinny_kernel(TileArgs p)
 {
-    constexpr int W = 4, RING = 3, ROWS = 32 + 16;
+    constexpr int W = 4, RING = 3, ROWS = X16 ? 32 : 32 + 16;
     // loads of scales: 32 rows of a weight, or 16 of either of two; 16 of the pairs (half a load, the other lanes idle)
     constexpr int SW = GATED ? 2 : 1;
-    constexpr int CODES = ROWS * kLine, STAGE = CODES + ROWS * 8, LOADS = ROWS / 8 + SW + 1;
+    constexpr int CODES = ROWS * kLine, STAGE = CODES + ROWS * 8, LOADS = ROWS / 8 + SW + (X16 ? 0 : 1);
     static_assert(RING * STAGE >= 2 * 64 * 16, "a wave's sums fit where its stages were");
-    __shared__ __attribute__((aligned(1024))) char lds[W * RING * STAGE];
+    static_assert(!X16 || W * RING * STAGE + kRoundedX == 81920, "half of the LDS");
+    __shared__ __attribute__((aligned(1024))) char lds[X16 ? 81920 : W * RING * STAGE];
     Unit u;
-    if (!unit_of<16>(p, count_units<16>(p), blockIdx.x / 8, &u)) return;
+    if (!unit_of(p, p.cols, count_units(p, p.cols), blockIdx.x / 8, &u)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15, kg = lane >> 4;
     const uint32_t kb = p.kb, sb = p.sb;
@@ -650,21 +650,23 @@ skinny_kernel(TileArgs p)
         const u32x4 dc0 = descriptor(p.t.w_codes[0] + w0 * kb, arow * kb), ds0 = descriptor(p.t.w_scales[0] + w0 * sb, arow * sb);
         const u32x4 dc1 = GATED ? descriptor(p.t.w_codes[1] + w0 * kb, arow * kb) : dc0;
         const u32x4 ds1 = GATED ? descriptor(p.t.w_scales[1] + w0 * sb, arow * sb) : ds0;
-        const u32x4 dxc = descriptor(p.t.x_codes, p.x_rows * kb), dxs = descriptor(p.t.x_scales, p.x_rows * sb);
+        const u32x4 dxc = descriptor(p.t.x_codes, X16 ? 0 : p.x_rows * kb), dxs = descriptor(p.t.x_scales, X16 ? 0 : p.x_rows * sb);
         const uint32_t mine = __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(lds)) + wave * (RING * STAGE);
         // a load of codes takes 8 rows; chunk c of row r sits at c ^ (r / 2) % 8
         const int lr = lane / 8, lc = lane & 7;
-        uint32_t vx[2], kx[2], vs;
+        uint32_t vx[2] = {0, 0}, kx[2] = {0, 0}, vs = 0;
+        if constexpr (!X16) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 8 * i + lr, c = lc ^ ((r >> 1) & 7);
-            const int64_t q = pair_of(p, u, r);
-            kx[i] = 16 * c;
-            vx[i] = q < 0 ? kOutOfRange : ((uint32_t)q / p.share) * kb + kx[i];
-        }
-        {
-            const int64_t q = pair_of(p, u, lane / 2);           // lanes past 16 rows are idle
-            vs = q < 0 ? kOutOfRange : ((uint32_t)q / p.share) * sb;
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * i + lr, c = lc ^ ((r >> 1) & 7);
+                const int64_t q = pair_of(p, u, r);
+                kx[i] = 16 * c;
+                vx[i] = q < 0 ? kOutOfRange : ((uint32_t)q / p.share) * kb + kx[i];
+            }
+            {
+                const int64_t q = pair_of(p, u, lane / 2);           // lanes past 16 rows are idle
+                vs = q < 0 ? kOutOfRange : ((uint32_t)q / p.share) * sb;
+            }
         }
         auto issue = [=](int step, int slot) __attribute__((always_inline)) {
             const uint32_t k = (uint32_t)step * kLine, s = (uint32_t)step * 8, at = mine + slot * STAGE;
@@ -674,19 +676,45 @@ skinny_kernel(TileArgs p)
                 buffer_to_lds(GATED && i >= 2 ? dc1 : dc0, k + 16 * c < kb ? (uint32_t)r * kb + k + 16 * c : kOutOfRange, at + i * 1024);
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < (X16 ? 0 : 2); ++i)
                 buffer_to_lds(dxc, k + kx[i] < kb ? vx[i] + k : kOutOfRange, at + (4 + i) * 1024);
             const uint32_t w = s + 4 * (lane & 1);               // rows past the weight's are out of range
 #pragma unroll
             for (int i = 0; i < SW; ++i)
                 if (!GATED || lane < 32)
                     word_to_lds(i ? ds1 : ds0, w < sb ? (uint32_t)(lane / 2) * sb + w : kOutOfRange, at + CODES + i * 128);
-            if (lane < 32) word_to_lds(dxs, w < sb ? vs + w : kOutOfRange, at + CODES + 256);
+            if (!X16 && lane < 32) word_to_lds(dxs, w < sb ? vs + w : kOutOfRange, at + CODES + 256);
         };
         const uint32_t at0 = mine + j * kLine + ((kg ^ (j >> 1)) << 4), sc0 = mine + CODES + j * 8 + kg;
         const int steps = (int)((kb + kLine - 1) / kLine);
 #pragma unroll
         for (int s = 0; s < RING - 1; ++s) issue(wave + s * W, s);
+        // the rounded rows: of each column the codes of all stages, then their scales
+        char* const rounded = lds + W * RING * STAGE;
+        if constexpr (X16) {
+            const int octets = steps * 32, row = (int)rounded_row(steps);
+            for (int i = tid; i < u.cols * octets; i += 64 * W) {
+                const int c = i / octets, o = i - c * octets;    // four lanes share a block
+                const int64_t q = pair_of(p, u, c);
+                u32x4 v = {0u, 0u, 0u, 0u};
+                if (q >= 0) {
+                    const uint16_t* const at = p.t.x + (int64_t)((uint32_t)q / p.share) * p.K + 8 * o;
+                    if (p.K % 8 == 0) {
+                        if (8 * o < p.K) v = *reinterpret_cast<const u32x4*>(at);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (8 * o + e < p.K) v[e / 2] |= (uint32_t)at[e] << (16 * (e & 1));
+                    }
+                }
+                uint32_t m = mx_absmax(v);
+                m = mx_dpp_max<kQuadXor2>(mx_dpp_max<kQuadXor1>(m));
+                const uint32_t scale = p.f16 ? mx_scale<true>(m) : mx_scale<false>(m);
+                *reinterpret_cast<uint32_t*>(rounded + c * row + 4 * o) = p.f16 ? mx_encode<true>(v, scale) : mx_encode<false>(v, scale);
+                if ((o & 3) == 0) rounded[c * row + steps * 128 + o / 4] = (char)scale;
+            }
+            __syncthreads();
+        }
         for (int k = wave; k < steps; k += RING * W) {
 #pragma unroll
             for (int s = 0; s < RING; ++s) {
@@ -698,8 +726,19 @@ skinny_kernel(TileArgs p)
                         const uint32_t at = (at0 ^ (h << 6)) + s * STAGE, sc = sc0 + s * STAGE + 4 * h;
                         const i32x4 w0v = *(const MHC_LDS i32x4*)(uintptr_t)at, w1v = *(const MHC_LDS i32x4*)(uintptr_t)(at + 16 * kLine);
                         const int s0 = *(const MHC_LDS uint8_t*)(uintptr_t)sc, s1 = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 128);
-                        const i32x4 x = *(const MHC_LDS i32x4*)(uintptr_t)(at + 32 * kLine);
-                        const int sx = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 256);
+                        i32x4 x = {0, 0, 0, 0};
+                        int sx = 0;
+                        if constexpr (X16) {
+                            const char* const r = rounded + j * (int)rounded_row(steps);
+                            const int block = (k + s * W) * 8 + 4 * h + kg;
+                            if (j < u.cols) {
+                                x = *reinterpret_cast<const i32x4*>(r + 16 * block);
+                                sx = *reinterpret_cast<const uint8_t*>(r + steps * 128 + block);
+                            }
+                        } else {
+                            x = *(const MHC_LDS i32x4*)(uintptr_t)(at + 32 * kLine);
+                            sx = *(const MHC_LDS uint8_t*)(uintptr_t)(sc + 256);
+                        }
                         acc[0] = mfma4<0, 0>(w0v, x, acc[0], s0, sx);
                         acc[1] = mfma4<0, 0>(w1v, x, acc[1], s1, sx);
                     }
@@ -783,7 +822,10 @@ hipError_t launch_tiles(const Tiling& t, const TileArgs& p, hipStream_t st)
     const dim3 grid((unsigned)t.grid()), block((unsigned)t.threads);
     switch (t.shape) {
         case kSkinny:
-            if constexpr (OUT != kOutPart) hipLaunchKernelGGL((skinny_kernel<GATED, OUT>), grid, block, 0, st, p);
+            if constexpr (OUT != kOutPart) {
+                if (t.rounds_x) hipLaunchKernelGGL((skinny_kernel<GATED, OUT, true>), grid, block, 0, st, p);
+                else hipLaunchKernelGGL((skinny_kernel<GATED, OUT, false>), grid, block, 0, st, p);
+            }
             break;
         case kSmall: hipLaunchKernelGGL((tile_kernel<GATED, OUT, 2, 2, 4, 4>), grid, block, 0, st, p); break;
         default: hipLaunchKernelGGL((tile_kernel<GATED, OUT, 2, 4, 8, 4>), grid, block, 0, st, p); break;
@@ -793,12 +835,12 @@ hipError_t launch_tiles(const Tiling& t, const TileArgs& p, hipStream_t st)
 
 }  // namespace
 
-int launch_products(const Geometry& g, const Args& a, void* stream)
+int launch_products(const Geometry& g, const Tiling& t, const Args& a, void* stream)
 {
     clear_pending_error();
     hipStream_t st = (hipStream_t)stream;
-    const Tiling t = make_tiling(g);
-    const TileArgs p = {a, g.P, g.E, g.R, g.act, (uint32_t)g.kb(), (uint32_t)g.sb(), (uint32_t)t.na, (uint32_t)g.share, (uint32_t)g.X};
+    const TileArgs p = {a, g.P, g.E, g.R, g.act, (uint32_t)g.kb(), (uint32_t)g.sb(), (uint32_t)t.na, (uint32_t)g.share, (uint32_t)g.X,
+                        g.K, t.cols, g.f16};
     if (g.op == kGlu) return (int)(g.f16 ? launch_tiles<true, kOutF16>(t, p, st) : launch_tiles<true, kOutBf16>(t, p, st));
     if (g.op == kProduct) return (int)(g.f16 ? launch_tiles<false, kOutF16>(t, p, st) : launch_tiles<false, kOutBf16>(t, p, st));
     const bool in16 = parts_in_16_bits(g);

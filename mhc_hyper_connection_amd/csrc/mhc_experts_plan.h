@@ -49,6 +49,7 @@ struct Tiling {
     int64_t na = 0;           // units along the weight rows
     int64_t nb = 0;           // units along the pairs, at most: every expert may end in a part of one
     int64_t places = 0;       // workgroups that take the units in turn; 0: one for each
+    bool rounds_x = false;    // kSkinny: takes x in 16 bits and rounds it itself
     int64_t grid() const
     {
         const int64_t n = 8 * cdiv(na * nb, 8);
@@ -58,7 +59,11 @@ struct Tiling {
     }
 };
 
-inline Tiling make_tiling(const Geometry& g)
+// The streaming kernel's LDS beside its rings of weights, for rows of x that it rounds itself.
+constexpr int64_t kRoundedX = 81920 - 12 * (32 * 128 + 256);
+MHC_EXPERTS_HOST_DEVICE inline int64_t rounded_row(int64_t stages) { return (stages * 136 + 15) / 16 * 16; }      // codes and scales
+// How the work is cut; x16: x comes in 16 bits.
+inline Tiling make_tiling(const Geometry& g, bool x16 = false)
 {
     Tiling t;
     const int64_t rows = g.op == kGlu ? 2 * (int64_t)g.R : g.R, steps = cdiv(g.kb(), 128);
@@ -86,6 +91,15 @@ inline Tiling make_tiling(const Geometry& g)
     // run beside its first products: T = 16384, K = 4096, N = 16384 643 against 661 us. The gated projection takes
     // one unit each: its activation would hold up the next unit, 714 against 702 us for 65536 pairs, D = 4096, F = 2048.
     if (g.op == kGlu) t.places = 0;
+    // A streaming workgroup can round its pairs' x rows itself, a launch and a workspace less, but each rounds them again. Two launches
+    // against one, us a call: K = 7168, N = 16384: T = 1 17.5, 14.2, 7 17.1, 26.2; K = N = 4096: T = 4 16.7, 13.5, 12 16.2, 16.5;
+    // K = 2048, N = 16384, T = 32 16.5, 24.2; T = 1, 64 experts, top 8: D = 7168, F = 2048 27.8, 29.0; D = 4096, F = 1024 22.1, 17.3.
+    if (t.shape == kSkinny && x16) {
+        const int64_t load = g.op == kProduct ? g.P : 2 * cdiv(g.P, g.E), pairs = load < 16 ? load : 16;
+        t.rounds_x = g.P > 0 && pairs * g.K * cdiv(cdiv(rows, t.rows) * across(16), 2 * kCUs) <= 16384;
+        const int64_t fit = kRoundedX / rounded_row(steps);      // more than `pairs`: 16384 values take 8704 bytes and half a stage each
+        if (t.rounds_x && fit < t.cols) t.cols = (int)fit;
+    }
     t.na = cdiv(rows, t.rows);
     // of the experts' buckets and that of the pairs without one
     t.nb = g.op == kProduct ? cdiv(g.P, t.cols) : g.P / t.cols + g.E + 1;
@@ -104,8 +118,8 @@ inline bool valid(const Geometry& g)
     if (mx::octet_blocks(g.X, g.K) < 0) return false;
     // the weighted sum: workgroups of 256 threads of eight results
     if (g.op == kDown && g.P * g.R / 2048 >= 0xffffff) return false;
-    const Tiling t = make_tiling(g);
-    return t.na * t.nb + 8 < (int64_t)1 << 23;     // workgroups of at most 512 threads within a grid's 2^32 - 1
+    const Tiling t = make_tiling(g), r = make_tiling(g, true);
+    return r.na * r.nb + 8 < (int64_t)1 << 23 && t.na * t.nb + 8 < (int64_t)1 << 23;     // workgroups of at most 512 threads within a grid's 2^32 - 1
 }
 
 // The projection back: whether the pairs' results, which the weighted sum reads, are kept in 16 bits, 11 of them
@@ -121,6 +135,7 @@ inline Workspace make_workspace(const Geometry& g, bool quantise)
 {
     Workspace w;
     size_t off = 0;
+    quantise = quantise && !make_tiling(g, true).rounds_x;
     w.off_codes = off;
     if (quantise) off = align_up(off + (size_t)g.X * (size_t)g.kb(), 256);
     w.off_scales = off;
@@ -146,6 +161,7 @@ MHC_EXPERTS_HOST_DEVICE inline void place(uint32_t t, uint32_t na, uint32_t nb, 
 }
 
 struct Args {
+    const uint16_t* x;            // [X, K] in 16 bits (a tiling that rounds it), or
     const uint8_t* x_codes;       // [X, kb]
     const uint8_t* x_scales;      // [X, sb]
     const uint8_t* w_codes[2];    // [E, R, kb] (the gated projection: gate and up)
@@ -160,7 +176,7 @@ struct Args {
 };
 
 // Implemented in mhc_experts.hip. Returns 0 or the HIP error code.
-int launch_products(const Geometry& g, const Args& a, void* stream);
+int launch_products(const Geometry& g, const Tiling& t, const Args& a, void* stream);
 
 }  // namespace experts
 }  // namespace mhc

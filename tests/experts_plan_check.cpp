@@ -24,9 +24,12 @@ static int fail(const char* what, long long a, long long b)
     return 1;
 }
 
-static int check_units(const experts::Geometry& g, const std::vector<int64_t>& load)
+static int check_units(const experts::Geometry& g, const std::vector<int64_t>& load, bool x16)
 {
-    const experts::Tiling t = experts::make_tiling(g);
+    const experts::Tiling t = experts::make_tiling(g, x16);
+    if (t.cols < 1 || (t.rounds_x && (!x16 || t.shape != experts::kSkinny || t.cols > 16 ||
+                                      t.cols * experts::rounded_row(experts::cdiv(g.kb(), 128)) > experts::kRoundedX)))
+        return fail("rounded rows", t.cols, g.K);
     const int64_t rows = g.op == experts::kGlu ? 2 * (int64_t)g.R : g.R;
     if (t.na * t.rows < rows || (t.na - 1) * t.rows >= rows) return fail("rows", t.na, rows);
     // what the kernel counts: the buckets' units, expert by expert
@@ -64,12 +67,12 @@ static int check_units(const experts::Geometry& g, const std::vector<int64_t>& l
 
 int main()
 {
-    long long n = 0;
+    long long n = 0, rounds = 0;
     for (int it = 0; it < 4000; ++it) {
         experts::Geometry g;
         g.op = (int)rnd(3);
         g.E = g.op == experts::kProduct ? 1 : 1 + (int)rnd(it % 3 ? 20 : 300);
-        g.K = 1 + (int)rnd(300);
+        g.K = 1 + (int)rnd(it % 4 ? 300 : 20000);
         g.R = 8 * (1 + (int)rnd(it % 5 ? 60 : 600));
         std::vector<int64_t> load;
         const uint32_t most = 1 + rnd(it % 7 ? 80 : 2000);
@@ -79,22 +82,25 @@ int main()
         g.X = g.P;
         if (g.P == 0) continue;
         if (!experts::valid(g)) return fail("valid", g.P, g.R);
-        if (check_units(g, load)) return 1;
+        if (check_units(g, load, false) || check_units(g, load, true)) return 1;
         // the same pairs all with one expert
         std::vector<int64_t> one(load.size(), 0);
         one[rnd((uint32_t)load.size())] = g.P;
-        if (check_units(g, one)) return 1;
+        if (check_units(g, one, false) || check_units(g, one, true)) return 1;
         for (int q = 0; q < 2; ++q) {
             const experts::Workspace w = experts::make_workspace(g, q == 1);
+            const bool quantised = q == 1 && !experts::make_tiling(g, true).rounds_x;
+            rounds += q == 1 && !quantised;
             const bool in16 = experts::parts_in_16_bits(g);
-            const int64_t need = (q ? g.X * (g.kb() + g.sb()) : 0) + (g.op != experts::kDown ? 0 : in16 ? g.P * g.R * 2 + g.P * experts::part_scales(g.R) : g.P * g.R * 4);
+            const int64_t need = (quantised ? g.X * (g.kb() + g.sb()) : 0) + (g.op != experts::kDown ? 0 : in16 ? g.P * g.R * 2 + g.P * experts::part_scales(g.R) : g.P * g.R * 4);
             if (in16 && (w.off_part_scales % 256 || (int64_t)(w.off_part_scales - w.off_part) < g.P * g.R * 2)) return fail("parts", g.P, g.R);
             if ((int64_t)w.bytes < need || w.off_codes % 256 || w.off_scales % 256 || w.off_part % 256) return fail("workspace", (long long)w.bytes, need);
-            if (q && (int64_t)(w.off_scales - w.off_codes) < g.X * g.kb()) return fail("codes", (long long)w.off_scales, g.X);
-            if (q && g.op == experts::kDown && (int64_t)(w.off_part - w.off_scales) < g.X * g.sb()) return fail("scales", (long long)w.off_part, g.X);
+            if (quantised && (int64_t)(w.off_scales - w.off_codes) < g.X * g.kb()) return fail("codes", (long long)w.off_scales, g.X);
+            if (quantised && g.op == experts::kDown && (int64_t)(w.off_part - w.off_scales) < g.X * g.sb()) return fail("scales", (long long)w.off_part, g.X);
         }
         ++n;
     }
+    if (rounds < 100) return fail("few that round x", rounds, n);
     // the routing plan's chunks cover the pairs once
     for (int it = 0; it < 20000; ++it) {
         route::Plan p;

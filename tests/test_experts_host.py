@@ -91,8 +91,8 @@ FIELDS = {"mhc_mxfp4_product": (B.ProductTensors, B.PRODUCT_TENSOR_FIELDS, "x", 
 
 def params(name, **kw):
     if name == "mhc_mxfp4_product":
-        return B.Mxfp4ProductParams(*{**dict(T=4, K=64, N=64, dt=0, reserved=0), **kw}.values())
-    return B.ExpertsParams(*{**dict(T=4, E=8, top_k=2, D=64, F=64, act=0, dt=0), **kw}.values())
+        return B.Mxfp4ProductParams(*{**dict(T=400, K=4096, N=64, dt=0, reserved=0), **kw}.values())
+    return B.ExpertsParams(*{**dict(T=400, E=8, top_k=2, D=4096, F=4096, act=0, dt=0), **kw}.values())
 
 
 def product(name, ws=FAKE, ws_bytes=1 << 40, p={}, **ptrs):
@@ -135,6 +135,8 @@ def test_products_refusals(name):
     assert get(None, 0, ctypes.byref(size)) == get(ctypes.byref(params(name)), 0, None) == NULL
     assert get(ctypes.byref(params(name)), 2, ctypes.byref(size)) == BAD
     assert B.products_workspace_size(name, params(name), False) > 0
+    few = params(name, T=1)                   # the streaming kernel rounds x itself
+    assert (B.products_workspace_size(name, few, False) > 0) == (name == "mhc_experts_down")
     assert (B.products_workspace_size(name, params(name), True) > 0) == (name == "mhc_experts_down")
 
 
