@@ -10,7 +10,7 @@
 // The weighted sum is a pass of its own over the pairs' results, which wait in the workspace: for bf16 (in tiles) as
 // fp16 with a power of two for each 32 of a pair, by which the largest is in [2^14, 2^15). That keeps 11
 // significant bits down to 2^-28 of the largest, three more than the sum's result has, and halves what is written and
-// read again: 847 to 600 us a call (65536 pairs, D = 4096, F = 2048), and the result's distance from 64 bits, 1.7e-3 of its norm, stays. fp16
+// read again: 848 to 692 us a call (65536 pairs, D = 4096, F = 2048), and the result's distance from 64 bits, 1.7e-3 of its norm, stays. fp16
 // results, which have 11 bits themselves, and those of few pairs wait in fp32.
 //
 // A unit of work is a run of weight rows and up to a tile's columns of one expert's pairs, which are
