@@ -288,7 +288,9 @@ __device__ __forceinline__ uint32_t part_down(uint32_t exponent) { return (expon
 //   wait for all loads, meet the other waves (whose reads of stage m are then done)
 //   second half of stage m   read the first half of m + 1, send off the loads of stage m + 2 and (but for the
 //                            group's last stage) a third of those of the next group's scales
-// Loads past the end of the reduction bring zeros.
+// Loads past the end of the reduction bring zeros. T = 16384, K = 4096, N = 16384: 570 us, 3.9 PFLOP/s; a stage takes 1.7 to
+// 1.9 us, of which its products alone would take 1.2: the operands' way from LDS (16-byte reads keep it busy for 0.9 us
+// of a stage) and the wait at its middle make up the rest.
 template <bool GATED, int OUT, int WA, int WB, int IA, int IB>
 __global__ void __launch_bounds__(64 * WA * WB, 2)
 tile_kernel(TileArgs p)
@@ -672,7 +674,8 @@ tile_kernel(TileArgs p)
 // Few pairs of an expert (16 at most to a unit): reading the weights once is the whole cost. A
 // workgroup takes 32 weight rows (gated: 16 of either weight), its W waves every W-th stage of 256 values; their
 // sums meet in LDS and are added in wave order. A wave keeps a ring of three stages of its own in LDS,
-// so that it waits for its own loads only and meets the others once. X16: the pairs' x rows come in 16 bits and are rounded into
+// so that it waits for its own loads only and meets the others once. K = 7168, N = 16384, one token: 13.3 us for 62 MB of weights;
+// 64 experts, top 8, D = 7168, F = 2048, gated: 25.5 for 125 MB: 4.7 and 4.9 TB/s, with some 2 us to start and to join. X16: the pairs' x rows come in 16 bits and are rounded into
 // LDS, behind the first loads of weights, once for all their stages.
 template <bool GATED, int OUT, bool X16>
 __global__ void __launch_bounds__(256)
@@ -829,7 +832,8 @@ skinny_kernel(TileArgs p)
     }
 }
 
-// A token's results by its weights: fp32 terms in the order of its slots, one rounding. A thread takes eight values.
+// A token's results by its weights: fp32 terms in the order of its slots, one rounding. A thread takes eight values. HBM bounds it:
+// 8192 tokens of 8 slots, D = 4096, 604 MB in 100 us, 6.0 TB/s.
 template <bool H, bool PART>
 __global__ void __launch_bounds__(256)
 combine_kernel(const void* __restrict__ part, const uint8_t* __restrict__ scales, const float* __restrict__ weights, uint16_t* __restrict__ out, int64_t T, int k,

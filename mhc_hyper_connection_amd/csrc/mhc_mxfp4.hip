@@ -1,7 +1,8 @@
 // mhc_mxfp4.hip -- gfx950 kernels of the microscaled 4-bit floats: 16-bit rows to codes and block
 // scales, and back. The format and its arithmetic are in mhc_mxfp4_device.h.
 //
-// Both stream: per value 2 bytes against 17/32, and some two vector instructions.
+// Both stream: per value 2 bytes against 17/32, and some two vector instructions. HBM bounds them: T = 16384, D = 7168
+// (297 MB either way) 67 us there, 4.4 TB/s, and 50 back, 5.9 (a large copy moves 5.2). Small tensors take 2 to 3 us whatever is done.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -10,7 +10,8 @@
 // The choice is first made in fp32, with a bound on its error. Where two neighbours in the order are nearer than that,
 // experts are taken on until one is surely the last, and those few are put in order by their fp64 values; where
 // the last group in and the first one out are, or no expert is surely the last in time, the token's choice is made again
-// in fp64. (All in fp64: 35 us at T = 16384, E = 256, top 8, 4 of 8 groups.)
+// in fp64. T = 16384, E = 256, top 8, 4 of 8 groups, sigmoid and bias: 20 us (all in fp64 35). Instructions bound it, not the 19 MB
+// (3.7 us at a copy's rate): some 1700 vector instructions of a wave, four waves to a SIMD, which issues them 58 % of the time.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -535,7 +536,8 @@ __device__ __forceinline__ void store_grad(void* out, int64_t i, float v)
 //   sigmoid                 dl_j = w_j (1 - s_j) g_j
 //   softmax                 dl_e = [e chosen] w_j g_j - s_e sum_j w_j g_j
 // at the chosen experts, and zero elsewhere but in the last. The k terms are fp64, the rest of a
-// softmax's row fp32.
+// softmax's row fp32. T = 16384, E = 256, top 8: 9.1 us, of which the 19 MB would take 3.6: the chosen experts' logits are
+// read one by one before the row is written.
 template <int DT, int L, int V>
 __global__ void __launch_bounds__(kThr)
 backward_kernel(RouteArgs p)
@@ -622,7 +624,8 @@ backward_kernel(RouteArgs p)
     }
 }
 
-// --- the plan. Wave w of a workgroup takes a contiguous part of its chunk, 64 pairs at a time in
+// --- the plan: 3.4 us to count and 8.4 to place 131072 pairs of 256 experts (1 MB), latency: a workgroup adds up the
+// chunks' counts, 64 here, 16 loads at a time, and then places 64 pairs of each wave after the other. 8 pairs in one workgroup: 2.6 us. Wave w of a workgroup takes a contiguous part of its chunk, 64 pairs at a time in
 // order: the pairs of an expert keep their order, whatever runs when.
 
 // Which lanes have this lane's value (of kBits bits).

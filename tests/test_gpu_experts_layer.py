@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import synth
+import test_gpu_experts as products
 from experts_helpers import U, act_ref, check, half_step, mxfp4, plan, rounded, route, sum_error, to_16, to_mxfp4, values
 from gpu_helpers import device, to_dev
 
@@ -221,3 +222,15 @@ def test_the_forms_in_16_and_in_4_bits_agree():
         act = np.abs(act_ref(gs, "silu"))
         lim = 1.13 * sum_error(D, np.abs(xr) @ np.abs(g).T) * np.abs(us) + act * sum_error(D, np.abs(xr) @ np.abs(u).T) + 2.0 ** -21 * act * np.abs(us)
         assert (np.abs(a - b) <= 2 * (lim + half_step(act * np.abs(us) + lim, False))).all()
+
+
+@pytest.mark.parametrize("T,k,E,D,F,f16", [(20000, 1, 150, 1288, 264, False), (40000, 1, 3, 1032, 264, True), (30000, 1, 2, 1024, 264, False),
+                                           (6000, 4, 90, 256, 520, True)])
+def test_workgroups_that_take_several_units(T, k, E, D, F, f16):
+    # more units than places for workgroups, small tiles and large, reductions that end inside a group of stages and with one
+    products.test_experts(T, k, E, D, F, f16)
+
+
+@pytest.mark.parametrize("T,K,N", [(9000, 1032, 4104), (20000, 2048, 1032)])
+def test_a_product_of_several_units(T, K, N):
+    products.test_product(T, K, N, False)
