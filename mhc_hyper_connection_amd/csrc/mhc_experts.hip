@@ -325,29 +325,30 @@ tile_kernel(TileArgs p)
     // scales, 8 rows of 8 words a load; the pair of words of a row's stage n of 4 sits at n ^ (r / 8) % 4, so that the
     // rows of a block of results, 8 apart or 16 in a run, meet different banks
     const uint32_t ks = 4 * ((lane & 7) ^ (2 * (wave & 3)));
-    // where a unit's loads begin: the weights, and the rows of x (those past the last are out of range)
+    // where a unit's loads begin
     struct Loads {
         u32x4 dc0, dc1, ds0, ds1;
-        uint32_t x[QB];
+        uint32_t vb[QB], vs[SB];
     };
     const uint32_t va = (uint32_t)r0 * kb + ka, vsa = (uint32_t)r0 * sb + ks;
     static_assert(SB == QB && SA == QA, "a load of scales has the rows of one of codes");
-    auto set_weights = [=](const Unit& u, Loads& l) __attribute__((always_inline)) {
+    // ln: the lane, hidden from the compiler, which would keep all that follows from it through the products
+    auto set_up = [=](int ln, const Unit& u, Loads& l) __attribute__((always_inline)) {
         const int64_t a0 = (int64_t)u.a * ROWS, w0 = u.e * R + a0;
-        const uint32_t arow = u.e < p.E ? (uint32_t)(R - a0 < ROWS ? R - a0 : ROWS) : 0;
+        const uint32_t arow = (uint32_t)(R - a0 < ROWS ? R - a0 : ROWS);
         l.dc0 = descriptor(p.t.w_codes[0] + w0 * kb, arow * kb);
         l.dc1 = GATED ? descriptor(p.t.w_codes[1] + w0 * kb, arow * kb) : l.dc0;
         l.ds0 = descriptor(p.t.w_scales[0] + w0 * sb, arow * sb);
         l.ds1 = GATED ? descriptor(p.t.w_scales[1] + w0 * sb, arow * sb) : l.ds0;
-    };
-    // ln: the lane, hidden from the compiler, which would keep all that follows from it through the products
-    auto get_pairs = [=](int ln, const Unit& u, int (&pair)[QB]) __attribute__((always_inline)) {
+        const int r0 = 8 * wave + ln / 8;
+        const uint32_t kx = 16 * ((ln & 7) ^ swizzle(r0 & 15));
 #pragma unroll
-        for (int q = 0; q < QB; ++q) pair[q] = (int)pair_of(p, u, 8 * wave + ln / 8 + 8 * NW * q);
-    };
-    auto set_rows = [=](const int (&pair)[QB], Loads& l) __attribute__((always_inline)) {
-#pragma unroll
-        for (int q = 0; q < QB; ++q) l.x[q] = pair[q] < 0 ? p.x_rows : (uint32_t)pair[q] / p.share;
+        for (int q = 0; q < QB; ++q) {
+            const int64_t pair = pair_of(p, u, r0 + 8 * NW * q);
+            const uint32_t x = pair < 0 ? 0u : (uint32_t)pair / p.share;
+            l.vb[q] = pair < 0 ? kOutOfRange : x * kb + kx;
+            l.vs[q] = pair < 0 ? kOutOfRange : x * sb + ks;
+        }
     };
     // where this wave's loads go
     const uint32_t codes_at = (uint32_t)scalar((int)(lds0 + wave * 1024)), scales_at = (uint32_t)scalar((int)(lds0 + 2 * STAGE + wave * 256));
@@ -356,23 +357,19 @@ tile_kernel(TileArgs p)
         asm volatile("" : "+s"(v));
         return v;
     };
-    // load q of this wave's part of a stage of the weights, of the pairs, of either's scales; other: all ones for unit m, else 0
+    // load q of this wave's part of a stage of the weights, of the pairs, of either's scales
     auto issue_a = [=](const Loads& l, int step, int slot, int q) __attribute__((always_inline)) {
         const uint32_t k = hidden((uint32_t)step * kLine);
-        buffer_to_lds(!GATED || q < QA / 2 ? l.dc0 : l.dc1, k + ka < kb ? va + (k + (8 * NW * q) % ROWS * kb) : kOutOfRange,
-                      hidden(codes_at) + slot * STAGE + q * NW * 1024);
+        buffer_to_lds(!GATED || q < QA / 2 ? l.dc0 : l.dc1, k + ka < kb ? va + (k + (8 * NW * q) % ROWS * kb) : kOutOfRange, hidden(codes_at) + slot * STAGE + q * NW * 1024);
     };
     auto issue_b = [=](const Loads& l, int step, int slot, int q) __attribute__((always_inline)) {
-        const uint32_t k = hidden((uint32_t)step * kLine), at = l.x[q] * hidden(kb) + (kx + k);
-        buffer_to_lds(dxc, k + kx < kb ? at : kOutOfRange, hidden(codes_at) + slot * STAGE + ASZ + q * NW * 1024);
+        const uint32_t k = hidden((uint32_t)step * kLine);
+        buffer_to_lds(dxc, k + kx < kb ? l.vb[q] + k : kOutOfRange, hidden(codes_at) + slot * STAGE + ASZ + q * NW * 1024);
     };
     auto issue_s = [=](const Loads& l, int group, uint32_t slot, int n) __attribute__((always_inline)) {
         const uint32_t s = hidden((uint32_t)group * 32), at = hidden(scales_at) + slot;
         if (n < SA) word_to_lds(!GATED || n < SA / 2 ? l.ds0 : l.ds1, s + ks < sb ? vsa + (s + (8 * NW * n) % ROWS * sb) : kOutOfRange, at + NW * n * 256);
-        else {
-            const uint32_t x = l.x[n - SA] * hidden(sb) + (ks + s);
-            word_to_lds(dxs, s + ks < sb ? x : kOutOfRange, at + NW * n * 256);
-        }
+        else word_to_lds(dxs, s + ks < sb ? l.vs[n - SA] + s : kOutOfRange, at + NW * n * 256);
     };
 
     // --- operand reads: lane (j, kg) takes block 2 kg + half of row j of each block of 16
@@ -408,7 +405,7 @@ tile_kernel(TileArgs p)
         o.b[q] = *(const MHC_LDS uint16_t*)(uintptr_t)((bsc ^ ((n ^ 2 * (q & 1)) << 3)) + slot + q * 16 * 32);
     };
 
-    // the first unit's first loads: its first group of scales and two stages
+    // a unit's first loads: its first group of scales and two stages
     auto first_loads = [=](const Loads& l) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < SA + SB; ++n) issue_s(l, 0, 0, n);
@@ -421,55 +418,37 @@ tile_kernel(TileArgs p)
         }
     };
 
-    // The gated projection's reduction is whole groups (past its end are zeros), and the next unit's first loads go with the last
-    // group's products: the activation does not hold them up. Others send them off before they store.
-    const int steps = GATED ? (int)((kb + 4 * kLine - 1) / (4 * kLine)) * 4 : (int)((kb + kLine - 1) / kLine);
+    const int steps = (int)((kb + kLine - 1) / kLine);
     static_assert(BC <= 256 && kUnitsLds <= (int)sizeof(lds), "a unit's columns in 8 bits, the buckets where the stages go");
     const Units mine = units_of<BC>(p, reinterpret_cast<int*>(lds));
-    // the n-th unit, or one without an expert, whose loads are out of range
-    auto unit = [=](int n, Unit* u) __attribute__((always_inline)) {
-        if (n < 64 && mine.at(n, u)) return true;
-        *u = {p.E, 0, 0, 0};
-        return false;
-    };
+    int n = 0;
     Unit u, next;
-    if (!unit(0, &u)) return;
-    Loads l, after;
-    {
-        int pair[QB];
-        get_pairs(lane, u, pair);
-        set_rows(pair, l);
-        set_weights(u, l);
-        if (u.e < p.E) first_loads(l);
+    if (!mine.at(0, &u)) return;
+    Loads l;
+    if (u.e < p.E) {
+        set_up(lane, u, l);
+        first_loads(l);
     }
-    bool more = unit(1, &next);
-    if constexpr (GATED) {
-        int pair[QB];
-        get_pairs(lane, next, pair);
-        set_rows(pair, after);
-        set_weights(next, after);
-    }
-    wait_loads_and_barrier<0>();
-    uint32_t slot = 0;
-    for (int n = 2;; ++n) {
+    wait_loads_and_barrier<GATED ? QA + QB : 0>();
+    while (true) {
         f32x4 acc[IA][IB];
 #pragma unroll
         for (int i = 0; i < IA; ++i)
 #pragma unroll
             for (int q = 0; q < IB; ++q) acc[i][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool more = !GATED && ++n < 64 && mine.at(n, &next);
 
         if (u.e < p.E) {
             Operands op[2];
             Scales sc;
             Pairs sp;
-            Loads to;
 #pragma unroll
-            for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]), read_sb(slot, 0, q, sc);
+            for (int q = 0; q < IB; ++q) read_b(0, 0, q, op[0]), read_sb(0, 0, q, sc);
 #pragma unroll
-            for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]), read_sa(slot, 0, i, sc);
+            for (int i = 0; i < IA; ++i) read_a(0, 0, i, op[0]), read_sa(0, 0, i, sc);
             // half H2 of stage m = 4 group + n: the products of `now` in IA parts, the reads of the next half (and of the next
             // stage's scales) and the loads dealt out over them; `slot`: where the next stage's scales are, `other`: the next group's
-            auto half = [&](auto number, int m, int n, int last, const Operands& now, Operands& next, uint32_t slot,
+            auto half = [&](auto number, int m, int n, const Operands& now, Operands& next, uint32_t slot,
                             uint32_t other) __attribute__((always_inline)) {
                 constexpr int READS = IA + IB, H2 = decltype(number)::value;
                 const int s = n % 2, rs = (s + H2) % 2;
@@ -503,44 +482,30 @@ tile_kernel(TileArgs p)
                     }
                     __builtin_amdgcn_sched_barrier(0);
                     if (H2 == 1) {
-                        const int step = m + 2 - (n >= 2 ? steps & last : 0);
 #pragma unroll
-                        for (int q = i * QA / IA; q < (i + 1) * QA / IA; ++q) issue_a(n < 2 ? l : to, step, s, q);
+                        for (int q = i * QA / IA; q < (i + 1) * QA / IA; ++q) issue_a(l, m + 2, s, q);
 #pragma unroll
-                        for (int q = i * QB / IA; q < (i + 1) * QB / IA; ++q) issue_b(n < 2 ? l : to, step, s, q);
+                        for (int q = i * QB / IA; q < (i + 1) * QB / IA; ++q) issue_b(l, m + 2, s, q);
 #pragma unroll
-                        for (int q = i * QN / IA; q < (i + 1) * QN / IA; ++q) issue_s(to, (m / 4 + 1) & ~last, other, n * (SA + SB) / 3 + q);
+                        for (int q = i * QN / IA; q < (i + 1) * QN / IA; ++q) issue_s(l, m / 4 + 1, other, n * (SA + SB) / 3 + q);
                     }
                 }
             };
+            uint32_t slot = 0;
             for (int m = 0; m < steps; m += 4) {
-                // all ones in the last group, whose loads in its second half, and of scales, are the next unit's. By masks that the compiler does
-                // not see through: it would branch, and the loop's body would no longer be one block
-                const int last = GATED ? scalar(m + 4 >= steps ? -1 : 0) : 0;
-                auto pick = [=](uint32_t a, uint32_t b) __attribute__((always_inline)) { return GATED ? a ^ ((a ^ b) & (uint32_t)last) : a; };
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    to.dc0[w] = pick(l.dc0[w], after.dc0[w]), to.dc1[w] = pick(l.dc1[w], after.dc1[w]);
-                    to.ds0[w] = pick(l.ds0[w], after.ds0[w]), to.ds1[w] = pick(l.ds1[w], after.ds1[w]);
-                }
-#pragma unroll
-                for (int q = 0; q < QB; ++q) to.x[q] = pick(l.x[q], after.x[q]);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     if (m + n < steps) {
-                        half(Number<0>{}, m + n, n, last, op[0], op[1], slot, slot ^ GROUP);
+                        half(Number<0>{}, m + n, n, op[0], op[1], slot, slot ^ GROUP);
                         // stage 1 is there from before; the last unit's stores may still be on their way
-                        if (n == 0) wait_unless_zero_and_barrier(m);
+                        if (!GATED && n == 0) wait_unless_zero_and_barrier(m);
                         else wait_loads_and_barrier<0>();
-                        half(Number<1>{}, m + n, n, last, op[1], op[0], n == 3 ? slot ^ GROUP : slot, slot ^ GROUP);
+                        half(Number<1>{}, m + n, n, op[1], op[0], n == 3 ? slot ^ GROUP : slot, slot ^ GROUP);
                     }
                 }
                 slot ^= GROUP;
             }
-            if constexpr (!GATED) {
-                wait_loads_and_barrier<0>();   // no load is left behind in LDS, and every wave has read it
-                slot = 0;
-            }
+            wait_loads_and_barrier<0>();   // no load is left behind in LDS, and every wave has read it
         }
 
         // --- results: lane (j, kg) holds rows 4 kg .. 4 kg + 3 of column j of each 16 x 16 block: 8 kg .. 8 kg + 7 of the 32 rows of
@@ -549,36 +514,25 @@ tile_kernel(TileArgs p)
         int ln = lane;
         asm volatile("" : "+v"(ln));
         if constexpr (GATED) {
-            Unit third;
-            const bool goes_on = unit(n, &third);
-            int rows[QB];
-            get_pairs(ln, third, rows);
             auto results = [&](auto act) __attribute__((always_inline)) {
 #pragma unroll
                 for (int q = 0; q < IB; ++q) {
-                    const int64_t pair = pair_of(p, u, 16 * (wb * IB + q) + (ln & 15));
+                    const int64_t pair = pair_of(p, u, 16 * (wb * IB + q) + j);
 #pragma unroll
                     for (int i = 0; i < IA / 4; ++i) {
-                        const int64_t f = a0 + 32 * i + 8 * (ln >> 4);
+                        const int64_t f = a0 + 32 * i + 8 * kg;
                         float v[8];
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             v[r] = activation<decltype(act)::value>(acc[2 * i + r / 4][q][r % 4]).a * acc[IA / 2 + 2 * i + r / 4][q][r % 4];
-                        if (q == 0 && i == 0) asm volatile("s_waitcnt vmcnt(0)" : : : "memory");   // the next unit's second stage, before stores follow it
                         if (pair >= 0 && f < R) store_results<OUT>(p, pair, f, v);
                     }
                 }
             };
             if (p.act) results(Number<1>{});
             else results(Number<0>{});
-            if (!more) break;
-            u = next;
-            next = third;
-            more = goes_on;
-            l = after;
-            set_rows(rows, after);
-            set_weights(next, after);
-        } else {
+            return;
+        }
         // A store takes eight neighbouring lanes to a column, whose 16-byte pieces are a whole line of memory (of two runs of 32
         // 16-bit results, or one of fp32); stored from where they are, 16 lanes apart and half a line at a time, they took longer:
         // 592 against 571 us for T = 16384, K = 4096, N = 16384, and 634 through the caches. (The gated projection's stores go out
@@ -595,11 +549,9 @@ tile_kernel(TileArgs p)
             }
             return o;
         };
+        // They are stored once the next unit's first loads are there, and are on their way while its first stages are multiplied.
         if (more && next.e < p.E) {
-            int rows[QB];
-            get_pairs(ln, next, rows);
-            set_rows(rows, l);
-            set_weights(next, l);
+            set_up(ln, next, l);
             first_loads(l);
         }
         int pair[IB][2];
@@ -664,10 +616,8 @@ tile_kernel(TileArgs p)
                 }
             }
         }
-            if (!more) break;
-            u = next;
-            more = unit(n, &next);
-        }
+        if (!more) break;
+        u = next;
     }
 }
 
@@ -675,8 +625,8 @@ tile_kernel(TileArgs p)
 // workgroup takes 32 weight rows (gated: 16 of either weight), its W waves every W-th stage of 256 values; their
 // sums meet in LDS and are added in wave order. A wave keeps a ring of three stages of its own in LDS,
 // so that it waits for its own loads only and meets the others once. K = 7168, N = 16384, one token: 13.3 us for 62 MB of weights;
-// 64 experts, top 8, D = 7168, F = 2048, gated: 25.5 for 125 MB: 4.7 and 4.9 TB/s, with some 2 us to start and to join. X16: the pairs' x rows come in 16 bits and are rounded into
-// LDS, behind the first loads of weights, once for all their stages.
+// 64 experts, top 8, D = 7168, F = 2048, gated: 25.5 for 125 MB: 4.7 and 4.9 TB/s, with some 2 us to start and to join. X16: the
+// pairs' x rows come in 16 bits and are rounded into LDS, behind the first loads of weights, once for all their stages.
 template <bool GATED, int OUT, bool X16>
 __global__ void __launch_bounds__(256)
 skinny_kernel(TileArgs p)
