@@ -289,8 +289,8 @@ __device__ __forceinline__ uint32_t part_down(uint32_t exponent) { return (expon
 //   second half of stage m   read the first half of m + 1, send off the loads of stage m + 2 and (but for the
 //                            group's last stage) a third of those of the next group's scales
 // Loads past the end of the reduction bring zeros. T = 16384, K = 4096, N = 16384: 570 us, 3.9 PFLOP/s; a stage takes 1.7 to
-// 1.9 us, of which its products alone would take 1.2: the operands' way from LDS (16-byte reads keep it busy for 0.9 us
-// of a stage) and the wait at its middle make up the rest.
+// 1.9 us, of which its products alone would take 1.2: the matrix cores are busy 47 % of the cycles, and the waves in a wait for
+// 30 % (for the middle's loads and each other).
 template <bool GATED, int OUT, int WA, int WB, int IA, int IB>
 __global__ void __launch_bounds__(64 * WA * WB, 2)
 tile_kernel(TileArgs p)
