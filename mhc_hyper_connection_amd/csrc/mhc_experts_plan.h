@@ -84,8 +84,10 @@ inline Tiling make_tiling(const Geometry& g, bool x16 = false)
     const double small = (double)cdiv(ns, 2 * kCUs) * (0.85 * (double)steps + 4);
     if (skinny < (small > once / 5 ? small : once / 5) + once / 20) t = {kSkinny, 32, 16, 256, 0, 0, 0};
     // A round of large units takes half as long again as one of small ones, two to a compute unit (large, small; us a call): 64 experts,
-    // D = 4096, F = 2048, top 8: T = 512 172, 167, 1024 197, 221, 2048 266, 321; N = K = 4096: T = 2048 37, 32, 4096 50, 55.
-    else if (3 * cdiv(nl, kCUs) <= 2 * cdiv(ns, 2 * kCUs)) t = {kLarge, 256, 256, 512, 0, 0, kCUs};
+    // D = 4096, F = 2048, top 8: T = 512 172, 167, 2048 266, 321; N = K = 4096: T = 2048 37, 32, 4096 50, 55. Where
+    // that makes them equal, the gated projection takes large ones, the others small: T = 1024, 64 experts, top 8, D = 4096, F = 2048
+    // 200, 213 and the projection back 156, 147.
+    else if (3 * cdiv(nl, kCUs) < 2 * cdiv(ns, 2 * kCUs) + (g.op == kGlu ? 1 : 0)) t = {kLarge, 256, 256, 512, 0, 0, kCUs};
     else t = {kSmall, 128, 128, 256, 0, 0, 2 * kCUs};
     // Workgroups that take units in turn send off a unit's first loads before the last one's results are stored, and the stores
     // run beside its first products: T = 16384, K = 4096, N = 16384 643 against 661 us. The gated projection takes
