@@ -754,13 +754,13 @@ mhc_status mhc_mxfp4_restore(const mhc_mxfp4_params* params, const uint8_t* code
  *
  * y = x w^T, both in microscaled 4-bit floats on the matrix cores: sums in fp32 of products that are exact, one
  * rounding to x_dtype. For serving: there is no gradient of a rounding to 4 bits. x comes in 16
- * bits and is rounded to 4 as mhc_mxfp4 does, into the workspace, or in 4 bits.
+ * bits and is rounded to 4 as mhc_mxfp4 does, into the workspace or (few rows) within the product, or in 4 bits.
  *   T >= 0; 1 <= K <= 65536; N a multiple of 8 in [8, 65536]; T * 16 ceil(K / 32) < 2^31
  *   x x_dtype [T, K] (16-byte aligned), or x_codes and x_scales (as mhc_mxfp4 lays them out);
  *   w_codes [N, 16 ceil(K / 32)], w_scales [N, 4 ceil(K / 128)];
  *   y x_dtype [T, N], 16-byte aligned
  * With T == 0 nothing is launched, and x and y may be NULL. The workspace (256-byte aligned, of
- * mhc_mxfp4_product_workspace_size bytes; x_mxfp4 1 where x comes in 4 bits, which needs
+ * mhc_mxfp4_product_workspace_size bytes, NULL if that is 0; x_mxfp4 1 where x comes in 4 bits, which needs
  * none, else 0) needs no initialisation, and calls that may overlap need distinct ones. Asynchronous on
  * `stream`, no allocation; every sum in a fixed order. y must not alias the inputs. Errors: NULLPTR
  * (neither form of x given, or codes without scales), PARAM_INVALID (both forms given), RUNTIME. */
@@ -789,7 +789,7 @@ mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_m
 /* The experts' products, over the pairs of mhc_experts_plan:
  *   mhc_experts_glu    h[t, j] = act(x[t] Wg[e]^T) (.) (x[t] Wu[e]^T),  e = experts[t, j]
  *   mhc_experts_down   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
- * with the weights of E experts in 4 bits, x and h in 16 bits (rounded to 4 into the workspace) or in 4. act as
+ * with the weights of E experts in 4 bits, x and h in 16 bits (rounded to 4, as there) or in 4. act as
  * mhc_glu's. h is zero, and adds weights times zero, for pairs without an expert. Sums, activations and
  * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype; but in bf16
  * the terms that are added up may have been rounded to 11 significant bits (bf16 has 8), or to 2^-39 of
