@@ -75,7 +75,7 @@ def ctypes_void(handle):
 
 
 def _check(t, name, dtype, shape, device):
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
         return
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -701,6 +701,11 @@ def mhc_glu_backward(grad_h, x, w_gate, w_up, *, act="silu", need_h=False, out=N
     return out
 
 
+def _check_contiguous(t, name):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 def _launch(device, what, raw, *args):
     """raw(*args, the current stream on `device`) with that device as the current one; raises for any status but success."""
     torch = _torch()
@@ -715,20 +720,24 @@ def _launch(device, what, raw, *args):
         raise MhcError(st, what)
 
 
-_LOGITS = {"bfloat16": 0, "float16": 1, "float32": 2}   # mhc_route_params.logits_dtype
+_LOGITS = {}    # mhc_route_params.logits_dtype by torch's dtypes, which are there once torch is
 
 
 def _route_params(logits, top_k, groups, top_groups, group_top, score, renormalise, scale):
     if score not in SCORES:
         raise ValueError(f"score: {score!r}, expected one of {sorted(SCORES)}")
-    dt = _LOGITS.get(str(logits.dtype)[6:])
+    if not _LOGITS:
+        torch = _torch()
+        _LOGITS.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    dt = _LOGITS.get(logits.dtype)
     if dt is None:
         raise ValueError(f"logits: dtype {logits.dtype}, expected torch.float32, torch.bfloat16 or torch.float16")
     if logits.dim() < 1:
         raise ValueError("logits: at least one dimension expected")
     if top_k < 1:
         raise ValueError(f"top_k: {top_k}, expected 1 or more")
-    return RouteParams(math.prod(logits.shape[:-1]), logits.shape[-1], top_k, groups, top_groups, group_top, SCORES[score],
+    *lead, E = logits.shape
+    return RouteParams(math.prod(lead), E, top_k, groups, top_groups, group_top, SCORES[score],
                        int(bool(renormalise)), dt, scale)
 
 
@@ -745,7 +754,7 @@ def mhc_route(logits, top_k, *, bias=None, score="softmax", groups=1, top_groups
     torch = _torch()
     params = _route_params(logits, top_k, groups, top_groups, group_top, score, renormalise, scale)
     shape, dev = (*logits.shape[:-1], top_k), logits.device
-    _check(logits, "logits", logits.dtype, logits.shape, dev)
+    _check_contiguous(logits, "logits")
     _check(bias, "bias", torch.float32, (logits.shape[-1],), dev)
     if out is None:
         weights = torch.empty(*shape, dtype=torch.float32, device=dev)
@@ -769,14 +778,14 @@ def mhc_route_backward(grad_weights, logits, weights, experts, *, score="softmax
         raise ValueError("experts: at least one dimension expected")
     params = _route_params(logits, experts.shape[-1], 1, 1, 1, score, renormalise, scale)
     shape, dev = (*logits.shape[:-1], experts.shape[-1]), logits.device
-    _check(logits, "logits", logits.dtype, logits.shape, dev)
+    _check_contiguous(logits, "logits")
     for t, name, dt in ((grad_weights, "grad_weights", torch.float32), (weights, "weights", torch.float32),
                         (experts, "experts", torch.int32)):
         if t is None:
             raise ValueError(f"{name} is required")
         _check(t, name, dt, shape, dev)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = torch.empty_like(logits)
     else:
         _check(out, "out", logits.dtype, logits.shape, dev)
     _launch(dev, "mhc_route_backward", raw_route_backward, params, grad_weights.data_ptr(), logits.data_ptr(),
@@ -841,7 +850,7 @@ def mhc_mxfp4(x, *, out=None):
     if x.dim() < 1:
         raise ValueError("x: at least one dimension expected")
     shape, dev = tuple(x.shape), x.device
-    _check(x, "x", xdt, shape, dev)
+    _check_contiguous(x, "x")
     if out is None:
         codes, scales = _mxfp4_shapes(shape)
         out = Mxfp4(torch.empty(*codes, dtype=torch.uint8, device=dev), torch.empty(*scales, dtype=torch.uint8, device=dev),
@@ -890,7 +899,7 @@ def _left(x, name):
     shape, dev = tuple(x.shape), x.device
     if not shape:
         raise ValueError(f"{name}: at least one dimension expected")
-    _check(x, name, xdt, shape, dev)
+    _check_contiguous(x, name)
     return shape, dev, xdt, (_ptr(x), None, None)
 
 
