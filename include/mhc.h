@@ -792,9 +792,9 @@ mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_m
  * with the weights of E experts in 4 bits, x and h in 16 bits (rounded to 4, as there) or in 4. act as
  * mhc_glu's. h is zero, and adds weights times zero, for pairs without an expert. Sums, activations and
  * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype; but in bf16
- * the terms that are added up may have been rounded to 11 significant bits (bf16 has 8), or to 2^-39 of
- * the largest of 32 neighbours where that is more. A token's result does
- * not depend on the other tokens but through the sizes T, E and top_k, which choose the order of the sums.
+ * the terms that are added up may have been rounded to 11 significant bits (bf16 has 8; from 2^128 - 2^116 on they
+ * become infinite), or to 2^-39 of the largest finite one of 32 neighbours where that is more. A NaN or an infinite term is that of
+ * its own column alone. A token's result does not depend on the other tokens but through the sizes T, E and top_k, which choose the order of the sums.
  *   T >= 0, T * top_k < 2^31; 1 <= E <= 1024; 1 <= top_k <= 32; D, F multiples of 8 in [8, 65536];
  *   of x (T rows of D values) and h (T * top_k rows of F): rows * 16 ceil(width / 32) < 2^31;
  *   of mhc_experts_down: T * top_k * D < 2^35

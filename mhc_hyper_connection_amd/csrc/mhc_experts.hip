@@ -8,7 +8,7 @@
 // values, and its scale byte that block's. Products accumulate in fp32; the activation and the
 // weighted sum are fp32, one rounding to the 16-bit result.
 // The weighted sum is a pass of its own over the pairs' results, which wait in the workspace: for bf16 (in tiles) as
-// fp16 with a power of two for each 32 of a pair, by which the largest is in [2^14, 2^15). That keeps 11
+// fp16 with a power of two for each 32 of a pair, by which the largest finite one is in [2^14, 2^15). That keeps 11
 // significant bits down to 2^-28 of the largest, three more than the sum's result has, and halves what is written and
 // read again: 848 to 692 us a call (65536 pairs, D = 4096, F = 2048), and the result's distance from 64 bits, 1.7e-3 of its norm, stays. fp16
 // results, which have 11 bits themselves, and those of few pairs wait in fp32.
@@ -255,23 +255,24 @@ __device__ __forceinline__ void store_results(const TileArgs& p, int64_t pair, i
     }
 }
 
-// The exponent field of the largest magnitude among 32 results of a column, eight in each of four lanes 16 apart; at least
-// 15, so that the powers of two below are normal numbers. 255: an infinity or a NaN, which stay what they are.
+// The exponent field of the largest finite magnitude among 32 results of a column, eight in each of four lanes 16 apart; at least
+// 15, so that the powers of two below are normal numbers. An infinity or a NaN has no part in it: under any of those
+// powers it stays what it is, and a neighbour's is that of the finite ones.
 __device__ __forceinline__ uint32_t exponent_of(f32x4 a, f32x4 b)
 {
-    // as whole numbers, which order like the values, NaN above all
+    // as whole numbers, which order like the values; twice them (without the sign) plus one in the exponent: 255 becomes 0
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t x = __float_as_uint(a[e]) & 0x7fffffffu, y = __float_as_uint(b[e]) & 0x7fffffffu;
+        const uint32_t x = (__float_as_uint(a[e]) << 1) + 0x01000000u, y = (__float_as_uint(b[e]) << 1) + 0x01000000u;
         m = m > x ? m : x;
         m = m > y ? m : y;
     }
     const auto s = __builtin_amdgcn_permlane16_swap(m, m, false, false);
     m = s[0] > s[1] ? s[0] : s[1];
     const auto t = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    m = (t[0] > t[1] ? t[0] : t[1]) >> 23;
-    return m < 15 ? 15 : m;
+    m = (t[0] > t[1] ? t[0] : t[1]) >> 24;
+    return (m < 16 ? 16 : m) - 1;
 }
 // The power of two that takes such results to [2^14, 2^15), and back.
 __device__ __forceinline__ uint32_t part_up(uint32_t exponent) { return (268u - exponent) << 23; }

@@ -1,0 +1,32 @@
+"""The tests of the products in tiles run in tiles: the launch plan's choice at their sizes, on the host."""
+import os
+import subprocess
+
+from experts_tiles import DOWN, FAR, FAR_RESULTS, GLU, LARGE, PRODUCTS, SMALL
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PRODUCT_OP, GLU_OP, DOWN_OP = 0, 1, 2
+
+
+def test_sizes_run_in_the_tiles_they_are_for(tmp_path):
+    exe = tmp_path / "experts_shape"
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "mhc_hyper_connection_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "experts_shape.cpp"), "-o", str(exe)], check=True)
+    lines, want = [], []
+    for x16 in (0, 1):
+        for T, K, N, shape in PRODUCTS:
+            lines.append((PRODUCT_OP, T, 1, 1, K, N, x16))
+            want.append(shape)
+        for op, cases in ((GLU_OP, GLU + FAR), (DOWN_OP, DOWN + FAR + FAR_RESULTS)):
+            for *size, shape in cases:
+                lines.append((op, *size, x16))
+                want.append(shape)
+    r = subprocess.run([str(exe)], input="\n".join(" ".join(map(str, l)) for l in lines), capture_output=True, text=True, check=True, timeout=60)
+    got = [tuple(map(int, l.split())) for l in r.stdout.splitlines()]
+    assert len(got) == len(lines)
+    for l, w, (valid, shape, units, places) in zip(lines, want, got):
+        assert valid == 1 and shape == w, (l, w, shape)
+    # each op in both shapes, and workgroups with several units among them
+    for op in (PRODUCT_OP, GLU_OP, DOWN_OP):
+        assert {w for l, w in zip(lines, want) if l[0] == op} == {SMALL, LARGE}
+    assert any(places and units > 2 * places for _, _, units, places in got)
