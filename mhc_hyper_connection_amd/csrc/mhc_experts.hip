@@ -91,24 +91,21 @@ __device__ __forceinline__ int scalar(int x)
 // A bucket's first and last pair and its units of BC pairs; bucket E: the pairs without an expert.
 __device__ __forceinline__ int bucket(const TileArgs& p, int BC, int e, int* begin, int* end)
 {
-    const int P = (int)p.P;
-    const int b = e <= p.E ? p.t.offsets[e] : P, n = e < p.E ? p.t.offsets[e + 1] : P;
-    *begin = b < 0 ? 0 : (b > P ? P : b);
-    *end = n < *begin ? *begin : (n > P ? P : n);
+    bucket_pairs(p.t.offsets, p.E, (int)p.P, e, begin, end);
     return (int)(((int64_t)*end - *begin + BC - 1) / BC);
 }
 __device__ __forceinline__ uint32_t count_units(const TileArgs& p, int BC)   // along the pairs
 {
     if (!p.t.offsets) return (uint32_t)((p.P + BC - 1) / BC);
-    const int lane = threadIdx.x & 63;
-    uint32_t total = 0;
+    const int lane = threadIdx.x & 63, most = most_units(p.P, BC, p.E);
+    int total = 0;
     for (int e0 = 0; e0 <= p.E; e0 += 64) {
         int begin, end, n = bucket(p, BC, e0 + lane, &begin, &end);
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-        total += (uint32_t)__builtin_amdgcn_readfirstlane(n);
+        total = units_sum(total, __builtin_amdgcn_readfirstlane(n), most);
     }
-    return total;
+    return (uint32_t)total;
 }
 // Unit i of this XCD's (the streaming kernel's), of total x na in all; false past the last.
 __device__ __forceinline__ bool unit_of(const TileArgs& p, int BC, uint32_t total, uint32_t i, Unit* u)
@@ -179,6 +176,7 @@ __device__ __forceinline__ Units units_of(const TileArgs& p, int* lds)
     uint32_t total = (uint32_t)((p.P + BC - 1) / BC);
     if (p.t.offsets) {
         if (threadIdx.x < 64) {
+            const int most = most_units(p.P, BC, p.E);
             int at = 0;
             for (int e0 = 0; e0 <= p.E; e0 += 64) {
                 int b, n;
@@ -190,11 +188,11 @@ __device__ __forceinline__ Units units_of(const TileArgs& p, int* lds)
                     if (lane >= d) scan += o;
                 }
                 if (e0 + lane <= p.E) {
-                    before[e0 + lane] = at + scan - tiles;
+                    before[e0 + lane] = units_sum(at, scan - tiles, most);
                     begin[e0 + lane] = b;
                     end[e0 + lane] = n;
                 }
-                at += __builtin_amdgcn_readlane(scan, 63);
+                at = units_sum(at, __builtin_amdgcn_readlane(scan, 63), most);
             }
             if (lane == 0) before[p.E + 1] = at;
         }
@@ -206,19 +204,15 @@ __device__ __forceinline__ Units units_of(const TileArgs& p, int* lds)
     if (i < per && unit < units) {
         uint32_t a, b;
         int e = 0, b0 = 0, b1 = (int)p.P;
+        int64_t first;
         if (p.t.offsets) {
-            const int q = (int)(unit / p.na);
-            int up = p.E + 1;                      // before[e] <= q < before[up]
-            while (up - e > 1) {
-                const int mid = (e + up) / 2;
-                if (before[mid] <= q) e = mid;
-                else up = mid;
-            }
+            find_unit(before, begin, p.E, p.na, BC, unit, &e, &a, &first);
             b0 = begin[e];
             b1 = end[e];
-            place(unit - (uint32_t)before[e] * p.na, p.na, (uint32_t)(before[e + 1] - before[e]), &a, &b);
-        } else place(unit, p.na, total, &a, &b);
-        const int64_t first = b0 + (int64_t)b * BC;
+        } else {
+            place(unit, p.na, total, &a, &b);
+            first = (int64_t)b * BC;
+        }
         if (first >= b0 && first < b1) {           // of a plan's offsets always
             u.first = (int)first;
             u.place = (uint32_t)e | a << 11 | (uint32_t)((b1 - first < BC ? (int)(b1 - first) : BC) - 1) << 21;

@@ -162,6 +162,36 @@ MHC_EXPERTS_HOST_DEVICE inline void place(uint32_t t, uint32_t na, uint32_t nb, 
     *a = group * kGroup + (r - *b * rows);
 }
 
+// Bucket e's pairs [begin, end) by the plan's offsets, e = E those without an expert (and past that none). Whatever the
+// offsets hold, pairs stay in [0, P).
+MHC_EXPERTS_HOST_DEVICE inline void bucket_pairs(const int32_t* offsets, int E, int P, int e, int* begin, int* end)
+{
+    const int b = e <= E ? offsets[e] : P, n = e < E ? offsets[e + 1] : P;
+    *begin = b < 0 ? 0 : (b > P ? P : b);
+    *end = n < *begin ? *begin : (n > P ? P : n);
+}
+// Units of BC pairs that the buckets of a plan have at most. Sums of buckets' units stop there: offsets that are no plan's
+// may name every pair in every bucket, and the sum of 1025 times P / BC units does not fit 32 bits. (64 buckets' does: valid() keeps
+// P / BC under 2^23.)
+MHC_EXPERTS_HOST_DEVICE inline int most_units(int64_t P, int BC, int E) { return (int)(P / BC) + E + 1; }
+MHC_EXPERTS_HOST_DEVICE inline int units_sum(int at, int more, int most) { return at + more < most ? at + more : most; }
+// Unit `unit` of before[E + 1] * na: its bucket e, its rows of units a and first pair; before[e]: the units along the pairs of the buckets before e.
+MHC_EXPERTS_HOST_DEVICE inline void find_unit(const int* before, const int* begin, int E, uint32_t na, int BC, uint32_t unit, int* e, uint32_t* a,
+                                              int64_t* first)
+{
+    const int q = (int)(unit / na);
+    int at = 0, up = E + 1;                        // before[at] <= q < before[up]
+    while (up - at > 1) {
+        const int mid = (at + up) / 2;
+        if (before[mid] <= q) at = mid;
+        else up = mid;
+    }
+    uint32_t b;
+    place(unit - (uint32_t)before[at] * na, na, (uint32_t)(before[at + 1] - before[at]), a, &b);
+    *e = at;
+    *first = begin[at] + (int64_t)b * BC;
+}
+
 struct Args {
     const uint16_t* x;            // [X, K] in 16 bits (a tiling that rounds it), or
     const uint8_t* x_codes;       // [X, kb]

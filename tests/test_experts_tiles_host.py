@@ -30,3 +30,12 @@ def test_sizes_run_in_the_tiles_they_are_for(tmp_path):
     for op in (PRODUCT_OP, GLU_OP, DOWN_OP):
         assert {w for l, w in zip(lines, want) if l[0] == op} == {SMALL, LARGE}
     assert any(places and units > 2 * places for _, _, units, places in got)
+
+
+def test_units_of_offsets_of_any_content(tmp_path):
+    exe = tmp_path / "experts_units_check"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Wextra", "-Werror", "-fsanitize=undefined", "-fno-sanitize-recover=all",
+                    "-I", os.path.join(ROOT, "mhc_hyper_connection_amd", "csrc"), os.path.join(ROOT, "tests", "experts_units_check.cpp"),
+                    "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
