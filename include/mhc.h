@@ -693,8 +693,8 @@ mhc_status mhc_route(const mhc_route_params* params, const void* logits, const f
  *   sigmoid                dl_j = weights_j (1 - s_j) g_j             at the chosen experts
  *   softmax                dl_e = [e chosen] weights_e g_e - s_e sum_j weights_j g_j
  * and zero elsewhere. Slots with an expert that is not in [0, E) count for nothing; a token
- * with a NaN weight gets NaN. The terms of a token's slots are fp64, the scores of its other
- * experts fp32, with one rounding to logits_dtype. An expert in two slots of a token gets their sum.
+ * with a NaN weight gets NaN. Both terms of a token's slots are fp64, the scores of its other
+ * experts and their part of the softmax's sum fp32, with one rounding to logits_dtype. An expert in two slots of a token gets their sum.
  *   params as in the forward (groups, top_groups and group_top are checked and not used)
  *   grad_weights f32 [T, top_k]; logits, weights, experts as in the forward;
  *   grad_logits logits_dtype [T, E]: overwritten, must not alias the inputs
