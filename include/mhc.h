@@ -659,7 +659,7 @@ mhc_status mhc_glu_backward(const mhc_glu_params* params, const mhc_glu_bwd_tens
  * are left (none, say, for a padded token whose logits are all -inf), the remaining slots hold expert
  * -1 and weight 0; weights of scores that are all 0 are 0. A NaN among a token's logits
  * or the biases, or with softmax a logit of +inf, makes all its weights NaN and its experts -1.
- *   0 <= T <= 2^26, T * top_k < 2^31; 1 <= E <= 1024; 1 <= groups <= 16, a divisor of E;
+ *   0 <= T <= 2^26 (2^26 - 4 for E > 256), T * top_k < 2^31; 1 <= E <= 1024; 1 <= groups <= 16, a divisor of E;
  *   1 <= top_groups <= groups; 1 <= top_k <= min(32, E / groups * top_groups); 0 < scale <= 1e30
  *   logits  logits_dtype [T, E]     bias f32 [E] or NULL     weights f32 [T, top_k]
  *   experts int32 [T, top_k]

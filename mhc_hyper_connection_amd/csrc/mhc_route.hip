@@ -754,6 +754,7 @@ place_kernel(const int32_t* __restrict__ experts, const int32_t* __restrict__ co
 template <int DT, int L, int V>
 hipError_t route_shape(const RouteArgs& p, bool groups, bool backward, hipStream_t st)
 {
+    static_assert(kThr == 256 && (L == 16 || L == 64), "what the plan's bound on T assumes");
     const dim3 grid((unsigned)((p.T + kThr / L - 1) / (kThr / L))), block(kThr);
     if (backward && p.score == kSoftmax && !p.renormalise) hipLaunchKernelGGL((backward_kernel<DT, L, V, true>), grid, block, 0, st, p);
     else if (backward) hipLaunchKernelGGL((backward_kernel<DT, L, V, false>), grid, block, 0, st, p);
@@ -771,7 +772,7 @@ hipError_t launch(const Geometry& g, const Args& a, bool backward, hipStream_t s
     const bool groups = g.groups > 1;
     if (g.E <= 64) return route_shape<DT, 16, 4>(p, groups, backward, st);
     if (g.E <= 128) return route_shape<DT, 16, 8>(p, groups, backward, st);
-    if (g.E <= 256) return route_shape<DT, 16, 16>(p, groups, backward, st);
+    if (g.E <= kFewExperts) return route_shape<DT, 16, 16>(p, groups, backward, st);
     if (g.E <= 512) return route_shape<DT, 64, 8>(p, groups, backward, st);
     return route_shape<DT, 64, 16>(p, groups, backward, st);
 }

@@ -13,7 +13,10 @@ namespace route {
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr int kMaxGroups = 16;
-constexpr int64_t kMaxT = (int64_t)1 << 26;       // workgroups of 4 tokens and 256 threads within a grid's 2^32 - 1 threads
+constexpr int64_t kMaxT = (int64_t)1 << 26;
+constexpr int64_t kMaxGrid = 0xffffff;            // workgroups of 256 threads within a grid's 2^32 - 1
+constexpr int kFewExperts = 256;                  // up to here 16 lanes take a token, above 64
+inline int64_t tokens_of_a_workgroup(int E) { return E <= kFewExperts ? 16 : 4; }
 constexpr int64_t kMaxPairs = 0x7fffffff;         // pairs are numbered in 32 bits
 
 enum Dtype { kBf16 = 0, kF16 = 1, kF32 = 2 };
@@ -30,6 +33,7 @@ inline bool make_geometry(int64_t T, int E, int k, int groups, int top_groups, i
                           int dtype, double scale, Geometry* g)
 {
     if (T < 0 || T > kMaxT || E < 1 || E > kMaxE || k < 1 || k > kMaxK || T * k > kMaxPairs) return false;
+    if (T > kMaxGrid * tokens_of_a_workgroup(E)) return false;
     if (groups < 1 || groups > kMaxGroups || E % groups != 0 || top_groups < 1 || top_groups > groups) return false;
     if (k > E / groups * top_groups) return false;
     if (group_top != 1 && group_top != 2) return false;

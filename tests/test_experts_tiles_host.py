@@ -1,6 +1,8 @@
-"""The tests of the products in tiles run in tiles: the launch plan's choice at their sizes, on the host."""
+"""The tests of the products in tiles run in tiles: the launch plan's choice at their sizes, on the host. And bounds of the launch plans."""
 import os
 import subprocess
+
+from mhc_hyper_connection_amd import _binding as B
 
 from experts_tiles import DOWN, FAR, FAR_RESULTS, GLU, LARGE, PRODUCTS, SMALL
 
@@ -39,3 +41,12 @@ def test_units_of_offsets_of_any_content(tmp_path):
                     "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.startswith("ok "), r.stdout + r.stderr
+
+
+def test_the_routings_grid_is_bounded():
+    # workgroups of 16 tokens up to 256 experts, of 4 above: 2^26 tokens are 2^24 workgroups of 256 threads there, one more than a grid holds.
+    # Within the bound the refusal is that of the missing tensors.
+    for E, most in ((256, 1 << 26), (257, (1 << 26) - 4), (1024, (1 << 26) - 4)):
+        for call, n in ((B.raw_route, 4), (B.raw_route_backward, 5)):
+            for T, status in ((most, B.MHC_ERR_NULLPTR), (most + 1, B.MHC_ERR_PARAM_INVALID)):
+                assert call(B.RouteParams(T, E, 2, 1, 1, 2, 0, 1, 2, 1.0), *(None,) * n, None) == status, (E, T)
