@@ -791,10 +791,11 @@ mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_m
  *   mhc_experts_down   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
  * with the weights of E experts in 4 bits, x and h in 16 bits (rounded to 4, as there) or in 4. act as
  * mhc_glu's. h is zero, and adds weights times zero, for pairs without an expert. Sums, activations and
- * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype; but in bf16
- * the terms that are added up may have been rounded to 11 significant bits (bf16 has 8; from 2^128 - 2^116 on they
- * become infinite), or to 2^-39 of the largest finite one of 32 neighbours where that is more. A NaN or an infinite term is that of
- * its own column alone. A token's result does not depend on the other tokens but through the sizes T, E and top_k, which choose the order of the sums.
+ * the weighted sum (in the order of the slots) are fp32, with one rounding to x_dtype. With MHC_SHORT_TERMS added to
+ * x_dtype mhc_experts_down may round the terms of a bf16 result before it adds them up, to 11 significant bits (bf16 has 8; from
+ * 2^128 - 2^116 on they become infinite), or to 2^-39 of the largest finite one of 32 neighbours where that is more: less
+ * time and workspace where there are many tokens. A NaN or an infinite term is that of its own column alone. A token's result does not
+ * depend on the other tokens but through the sizes T, E and top_k, which choose the order of the sums.
  *   T >= 0, T * top_k < 2^31; 1 <= E <= 1024; 1 <= top_k <= 32; D, F multiples of 8 in [8, 65536];
  *   of x (T rows of D values) and h (T * top_k rows of F): rows * 16 ceil(width / 32) < 2^31;
  *   of mhc_experts_down: T * top_k * D < 2^35
@@ -806,7 +807,9 @@ mhc_status mhc_mxfp4_product(const mhc_mxfp4_product_params* params, const mhc_m
  *   weights f32 [T, top_k]      y x_dtype [T, D]
  * 16-bit tensors and codes 16-byte, the others 4-byte aligned. With T == 0 nothing is launched, and
  * the tensors of tokens and pairs may be NULL. Workspace, order and errors as mhc_mxfp4_product's (the
- * workspace of mhc_experts_down holds T * top_k results of D values in 16 or 32 bits too). */
+ * workspace of mhc_experts_down holds T * top_k results of D values in 32 bits, or 16 with MHC_SHORT_TERMS, too). */
+#define MHC_SHORT_TERMS 0x100
+
 typedef struct mhc_experts_params {
     int64_t T;
     int32_t E;
@@ -814,7 +817,7 @@ typedef struct mhc_experts_params {
     int32_t D;
     int32_t F;
     int32_t act;        /* MHC_ACT_SILU or MHC_ACT_GELU_TANH (mhc_experts_down: not used, but checked) */
-    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16 */
+    int32_t x_dtype;    /* MHC_DTYPE_BF16 or MHC_DTYPE_F16 (mhc_experts_down: plus MHC_SHORT_TERMS or not) */
 } mhc_experts_params;
 
 typedef struct mhc_experts_glu_tensors {

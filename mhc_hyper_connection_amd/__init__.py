@@ -22,7 +22,7 @@ from ._binding import (FORWARD_EVENTS, MHC_ERR_NULLPTR, MHC_ERR_PARAM_INVALID,
                        forward_path, raw_inv_rms, raw_post, raw_sinkhorn, raw_checkpoint,
                        ACTS, glu_backward_workspace_size, make_glu_params, raw_glu, raw_glu_backward,
                        SCORES, ExpertsDownTensors, ExpertsGluTensors, ExpertsParams, Mxfp4ProductParams, ProductTensors,
-                       RouteParams, experts_plan_workspace_size, products_workspace_size, raw_experts_plan, raw_mxfp4,
+                       RouteParams, SHORT_TERMS, experts_plan_workspace_size, products_workspace_size, raw_experts_plan, raw_mxfp4,
                        raw_mxfp4_restore, raw_products, raw_route, raw_route_backward,
                        raw_checkpoint_restore, raw_post_checkpoint, raw_post_backward, raw_backward_checkpoint,
                        load, make_bwd_params, make_params, packed_size, raw_backward,
@@ -972,14 +972,14 @@ def mhc_experts_glu(x, plan, w_gate, w_up, *, act="silu", out=None):
     return out
 
 
-def mhc_experts_down(h, plan, weights, w_down, *, out=None):
+def mhc_experts_down(h, plan, weights, w_down, *, short_terms=False, out=None):
     """The experts' projection back and each token's weighted sum: y[t] = sum over its slots of weights[t, j]
     (h[t, j] w_down[e]^T), e the slot's expert. h [..., top_k, F] (mhc_experts_glu's) in bf16 or fp16, which is rounded
     to 4 bits as mhc_mxfp4 does, or an Mxfp4; plan as there; weights f32 [..., top_k], mhc_route's; w_down
     Mxfp4 [E, D, F]. Returns (or fills) y [..., D] in h's dtype (what mhc_post takes): fp32 sums, in the slots'
-    order, one rounding (in bf16 of terms with at least 11 significant bits: include/mhc.h). A pair without an
-    expert adds its weight times zero. For serving (there is no backward). The workspace is the call's own, with a
-    result for each pair."""
+    order, one rounding. short_terms allows a bf16 sum's terms to be rounded first, to 11 significant bits or 2^-39 of the
+    largest of 32 neighbouring columns (include/mhc.h): a quarter less time for many tokens. A pair without an expert adds its
+    weight times zero. For serving (there is no backward). The workspace is the call's own, with a result for each pair."""
     torch = _torch()
     shape, dev, xdt, ptrs = _left(h, "h")
     if not isinstance(w_down, Mxfp4) or w_down.codes.dim() != 3:
@@ -997,7 +997,7 @@ def mhc_experts_down(h, plan, weights, w_down, *, out=None):
         out = torch.empty((*lead, D), dtype=xdt, device=dev)
     else:
         _check(out, "out", xdt, (*lead, D), dev)
-    params = ExpertsParams(math.prod(lead), E, plan.shape[-1], D, F, 0, int(xdt == torch.float16))
+    params = ExpertsParams(math.prod(lead), E, plan.shape[-1], D, F, 0, int(xdt == torch.float16) | (SHORT_TERMS if short_terms else 0))
     tensors = ExpertsDownTensors(*ptrs, _ptr(plan.offsets), _ptr(plan.pairs), _ptr(weights), _ptr(w_down.codes),
                                  _ptr(w_down.scales), _ptr(out))
     _run_products("mhc_experts_down", params, tensors, isinstance(h, Mxfp4), dev)

@@ -146,6 +146,9 @@ class ExpertsParams(ctypes.Structure):
                 ("F", ctypes.c_int32), ("act", ctypes.c_int32), ("x_dtype", ctypes.c_int32)]
 
 
+SHORT_TERMS = 0x100     # MHC_SHORT_TERMS
+
+
 PRODUCT_TENSOR_FIELDS = ("x", "x_codes", "x_scales", "w_codes", "w_scales", "y")
 EXPERTS_GLU_TENSOR_FIELDS = ("x", "x_codes", "x_scales", "offsets", "pairs", "w_gate_codes", "w_gate_scales", "w_up_codes",
                              "w_up_scales", "h")

@@ -54,7 +54,8 @@ mhc_status geometry_of(const mhc_mxfp4_product_params* p, Geometry* g)
 mhc_status geometry_of(const mhc_experts_params* p, bool down, Geometry* g)
 {
     if (!p) return MHC_ERR_NULLPTR;
-    if (!is_x_dtype(p->x_dtype) || p->T < 0 || p->T > 0x7fffffff || p->top_k < 1 || p->top_k > mhc::experts::kMaxTopK)
+    const int32_t dtype = down ? p->x_dtype & ~MHC_SHORT_TERMS : p->x_dtype;
+    if (!is_x_dtype(dtype) || p->T < 0 || p->T > 0x7fffffff || p->top_k < 1 || p->top_k > mhc::experts::kMaxTopK)
         return MHC_ERR_PARAM_INVALID;
     // both widths are rows of results of one of the two products
     if (p->D < 8 || p->D % 8 != 0 || p->F < 8 || p->F % 8 != 0) return MHC_ERR_PARAM_INVALID;
@@ -66,7 +67,8 @@ mhc_status geometry_of(const mhc_experts_params* p, bool down, Geometry* g)
     g->K = down ? p->F : p->D;
     g->R = down ? p->D : p->F;
     g->act = p->act;
-    g->f16 = p->x_dtype == MHC_DTYPE_F16;
+    g->f16 = dtype == MHC_DTYPE_F16;
+    g->short_terms = dtype != p->x_dtype;
     return mhc::experts::valid(*g) ? MHC_OK : MHC_ERR_PARAM_INVALID;
 }
 

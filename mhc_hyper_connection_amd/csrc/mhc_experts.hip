@@ -7,11 +7,12 @@
 // codes and scale bytes as they are in memory: a lane's 16 bytes of codes are one block of 32
 // values, and its scale byte that block's. Products accumulate in fp32; the activation and the
 // weighted sum are fp32, one rounding to the 16-bit result.
-// The weighted sum is a pass of its own over the pairs' results, which wait in the workspace: for bf16 (in tiles) as
-// fp16 with a power of two for each 32 of a pair, by which the largest finite one is in [2^14, 2^15). That keeps 11
-// significant bits down to 2^-28 of the largest, three more than the sum's result has, and halves what is written and
-// read again: 848 to 692 us a call (65536 pairs, D = 4096, F = 2048), and the result's distance from 64 bits, 1.7e-3 of its norm, stays. fp16
-// results, which have 11 bits themselves, and those of few pairs wait in fp32.
+// The weighted sum is a pass of its own over the pairs' results, which wait in the workspace in fp32. Where the caller allows it
+// (MHC_SHORT_TERMS), those of bf16 tiles wait as fp16 with a power of two for each 32 of a pair, by which the largest finite one
+// is in [2^14, 2^15). That keeps 11 significant bits down to 2^-28 of the largest, three more than the sum's result has, and
+// halves what is written and read again: 823 against 634 us a call (65536 pairs, D = 4096, F = 2048). The results differ by 8.9e-4 of their
+// norm, some by a bf16 step, and their distance from 64 bits is 1.673e-3 of the norm instead of 1.660e-3. fp16 results, which
+// have 11 bits themselves, and the streaming kernel's always wait in fp32.
 //
 // A unit of work is a run of weight rows and up to a tile's columns of one expert's pairs, which are
 // gathered by the plan's list as their x rows are loaded. Pairs without an expert are a bucket of their own

@@ -36,6 +36,7 @@ struct Geometry {
     int E = 1, share = 1;
     int K = 0, R = 0;
     int act = 0, f16 = 0;
+    int short_terms = 0;      // kDown: the caller allows its terms in 16 bits
     int64_t kb() const { return mx::code_bytes(K); }
     int64_t sb() const { return mx::scale_bytes(K); }
 };
@@ -125,8 +126,8 @@ inline bool valid(const Geometry& g)
 }
 
 // The projection back: whether the pairs' results, which the weighted sum reads, are kept in 16 bits, 11 of them
-// significant, with a power of two for each 32 (mhc_experts.hip): for bf16, which has 8, in tiles.
-inline bool parts_in_16_bits(const Geometry& g) { return g.op == kDown && !g.f16 && make_tiling(g).shape != kSkinny; }
+// significant, with a power of two for each 32 (mhc_experts.hip): where the caller allows it, for bf16, which has 8, in tiles.
+inline bool parts_in_16_bits(const Geometry& g) { return g.op == kDown && g.short_terms && !g.f16 && make_tiling(g).shape != kSkinny; }
 MHC_EXPERTS_HOST_DEVICE inline int64_t part_scales(int64_t R) { return (R + 31) / 32; }
 
 struct Workspace {

@@ -2,6 +2,8 @@
 import os
 import subprocess
 
+import pytest
+
 from mhc_hyper_connection_amd import _binding as B
 
 from experts_tiles import DOWN, FAR, FAR_RESULTS, GLU, LARGE, PRODUCTS, SMALL
@@ -50,3 +52,15 @@ def test_the_routings_grid_is_bounded():
         for call, n in ((B.raw_route, 4), (B.raw_route_backward, 5)):
             for T, status in ((most, B.MHC_ERR_NULLPTR), (most + 1, B.MHC_ERR_PARAM_INVALID)):
                 assert call(B.RouteParams(T, E, 2, 1, 1, 2, 0, 1, 2, 1.0), *(None,) * n, None) == status, (E, T)
+
+
+def test_terms_in_16_bits_are_the_callers_choice():
+    size = lambda name, dtype: B.products_workspace_size(name, B.ExpertsParams(8192, 64, 8, 4096, 2048, 0, dtype), True)
+    down, glu, pairs, bf16, f16 = "mhc_experts_down", "mhc_experts_glu", 8192 * 8, 0, 1
+    assert size(down, bf16) == size(down, f16) == size(down, f16 | B.SHORT_TERMS) == pairs * 4096 * 4       # fp16's are not shortened
+    assert size(down, bf16 | B.SHORT_TERMS) == pairs * (4096 * 2 + 4096 // 32)
+    assert size(glu, bf16) == size(glu, f16) == 0
+    for name, dtype in ((down, 2 | B.SHORT_TERMS), (down, B.SHORT_TERMS << 1), (down, -1), (glu, bf16 | B.SHORT_TERMS), (glu, f16 | B.SHORT_TERMS)):
+        with pytest.raises(B.MhcError) as e:
+            size(name, dtype)
+        assert e.value.status == B.MHC_ERR_PARAM_INVALID, (name, dtype)

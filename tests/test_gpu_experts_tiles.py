@@ -1,5 +1,5 @@
 """The products with 4-bit weights in tiles on the GPU, at sizes for which the launch plan takes them (tests/test_experts_tiles_host.py),
-against the definition in 64 bits; the errors are those of tests/test_gpu_experts.py."""
+against the definition in 64 bits; the errors are those of tests/test_gpu_experts.py, whose rounding of bf16's terms is that of short_terms alone."""
 import sys
 
 import numpy as np
@@ -26,16 +26,19 @@ def pairs_of(x, w, flat, tok):
     return out
 
 
-@pytest.mark.parametrize("f16", [False, True])
+FORMS = [(False, False), (False, True), (True, False), (True, True)]      # f16, short_terms
+
+
+@pytest.mark.parametrize("f16,short", FORMS)
 @pytest.mark.parametrize("T,k,E,D,F,shape", DOWN)
-def test_finite_results_beside_a_nan_or_an_infinity(T, k, E, D, F, shape, f16):
+def test_finite_results_beside_a_nan_or_an_infinity(T, k, E, D, F, shape, f16, short):
     # A weight row with a block of NaN spoils its column of y for its expert's tokens, and one whose sums overflow makes them
     # infinite; the columns beside them are those of weights without either. Whole numbers, whose fp32 sums are exact.
     import mhc_hyper_connection_amd as mhc
     import torch
     dev = device()
     rng = np.random.default_rng(T + D)
-    case(f"finite beside NaN T={T} k={k} E={E} D={D} F={F} f16={f16}")
+    case(f"finite beside NaN T={T} k={k} E={E} D={D} F={F} f16={f16} short={short}")
     e = some_experts(rng, T, k, E, masked=True)
     flat = e.reshape(-1)
     h, w = mxfp4(rng, T, k, F, low=127, high=129), mxfp4(rng, E, D, F, low=127, high=129)
@@ -44,16 +47,16 @@ def test_finite_results_beside_a_nan_or_an_infinity(T, k, E, D, F, shape, f16):
     w[0][0, nan] = w[0][1, inf] = 0
     wt = (1 + rng.integers(0, 4, (T, k))).astype(np.float32) / 4
     p, hm, wd = a_plan(e, E, dev), to_mxfp4(*h, F, f16, dev), to_dev(wt, dev)
-    clean = mhc.mhc_experts_down(hm, p, wd, to_mxfp4(*w, F, f16, dev))
+    clean = mhc.mhc_experts_down(hm, p, wd, to_mxfp4(*w, F, f16, dev), short_terms=short)
     hv, wv = values(*h, F).reshape(T * k, F), values(*w, F)
     y = pairs_of(hv, wv, flat, np.arange(T * k))
-    err = np.zeros_like(y) if f16 else part_error(y)
+    err = part_error(y) if short and not f16 else np.zeros_like(y)
     weighted = lambda v: (wt.astype(float).reshape(T * k, 1) * v).reshape(T, k, D).sum(1)
     check("clean", clean, weighted(y), weighted(err) + (k + 1) * U * weighted(np.abs(y)), f16)
 
     w[1][0, nan, 1] = 255                                    # a block of the reduction's second 32 values
     w[0][1, inf, 0], w[1][1, inf, 0] = 7, 254                # 6 2^127 6 2^0, or 2^1, is past fp32's range
-    got = mhc.mhc_experts_down(hm, p, wd, to_mxfp4(*w, F, f16, dev)).cpu()
+    got = mhc.mhc_experts_down(hm, p, wd, to_mxfp4(*w, F, f16, dev), short_terms=short).cpu()
     clean = clean.cpu()
     has = lambda x: torch.from_numpy((e == x).any(1))
     rest = torch.ones(D, dtype=torch.bool)
@@ -163,31 +166,33 @@ def test_projection_back_with_uneven_loads(T, k, E, D, F, shape):
     alone = np.zeros((T, k), np.float32)
     alone[np.arange(T), rng.integers(0, k, T)] = 1
     some = np.where(e < 0, 0, rng.random((T, k))).astype(np.float32)
-    for f16 in (False, True):
-        case(f"experts_down T={T} k={k} E={E} D={D} F={F} f16={f16}")
-        err = np.zeros_like(y) if f16 else part_error(y)
+    for f16, short in FORMS:
+        case(f"experts_down T={T} k={k} E={E} D={D} F={F} f16={f16} short={short}")
+        rounds = short and not f16
+        err = part_error(y) if rounds else np.zeros_like(y)
         wd, hm = to_mxfp4(*w, F, f16, dev), to_mxfp4(*h, F, f16, dev)
         for wt in (alone, some):
             weighted = lambda v: (wt.astype(float).reshape(T * k, 1) * v).reshape(T, k, D).sum(1)
             full = torch.full((T + 1, D), 7.0, dtype=torch_dtype(f16), device=dev)
-            got = mhc.mhc_experts_down(hm, p, to_dev(wt, dev), wd, out=full[:T])
+            got = mhc.mhc_experts_down(hm, p, to_dev(wt, dev), wd, short_terms=short, out=full[:T])
             want = weighted(y)
-            if f16 and wt is alone:
-                assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch.float16))
+            if not rounds and wt is alone:
+                assert torch.equal(got.cpu(), torch.from_numpy(want.astype(np.float32)).to(torch_dtype(f16)))
             check("y", got, want, weighted(err) + (k + 1) * U * weighted(np.abs(y)), f16)
             assert (full[T] == 7.0).all()
         # h in 16 bits whose 4-bit form is h itself
         h16 = mhc.mhc_mxfp4_restore(hm)
-        assert torch.equal(mhc.mhc_experts_down(h16, p, to_dev(some, dev), wd), mhc.mhc_experts_down(mhc.mhc_mxfp4(h16), p, to_dev(some, dev), wd))
+        assert torch.equal(*(mhc.mhc_experts_down(v, p, to_dev(some, dev), wd, short_terms=short) for v in (h16, mhc.mhc_mxfp4(h16))))
 
 
+@pytest.mark.parametrize("short", [False, True])
 @pytest.mark.parametrize("T,k,E,D,F,shape", DOWN)
-def test_results_of_any_size_in_bf16(T, k, E, D, F, shape):
+def test_results_of_any_size_in_bf16(T, k, E, D, F, shape, short):
     # a run of 32 results far past fp16's range or far below it, and neighbours 2^60 apart; a pair whose h is NaN
     import mhc_hyper_connection_amd as mhc
     dev = device()
     rng = np.random.default_rng(T)
-    case(f"any size T={T} k={k} E={E} D={D} F={F}")
+    case(f"any size T={T} k={k} E={E} D={D} F={F} short={short}")
     e = some_experts(rng, T, k, E, masked=False)
     flat = e.reshape(-1)
     h, w = mxfp4(rng, T, k, F, low=127, high=129), mxfp4(rng, E, D, F, low=127, high=129)
@@ -198,10 +203,10 @@ def test_results_of_any_size_in_bf16(T, k, E, D, F, shape):
     hv, wv = values(*h, F).reshape(T * k, F), values(*w, F)
     y, mag = pairs_of(hv, wv, flat, np.arange(T * k)), pairs_of(np.abs(hv), np.abs(wv), flat, np.arange(T * k))
     wt = rng.random((T, k)).astype(np.float32)
-    got = mhc.mhc_experts_down(to_mxfp4(*h, F, False, dev), a_plan(e, E, dev), to_dev(wt, dev), to_mxfp4(*w, F, False, dev))
+    got = mhc.mhc_experts_down(to_mxfp4(*h, F, False, dev), a_plan(e, E, dev), to_dev(wt, dev), to_mxfp4(*w, F, False, dev), short_terms=short)
     weighted = lambda v: (wt.astype(float).reshape(T * k, 1) * v).reshape(T, k, D).sum(1)
     err = sum_error(F, mag)
-    err = err + part_error(np.abs(y) + err) + 2.0 ** -149
+    err = err + (part_error(np.abs(y) + err) if short else 0) + 2.0 ** -149
     check("y", got, weighted(y), weighted(err) + (k + 1) * U * weighted(np.abs(y)), False)
 
 
@@ -234,10 +239,11 @@ def test_a_plan_that_is_none(T, k, E, D, F, shape, kind):
     assert (full[0] == 7).all() and (full[T + 1] == 7).all()
     # back: [T k, D] to F columns, as the gated projection's rows
     h, down, ones = randn(T, k, D), mhc.mhc_mxfp4(randn(E, F, D)), torch.ones(T, k, device=dev)
-    back = torch.full((T + 2, F), 7.0, dtype=torch.bfloat16, device=dev)
-    mhc.mhc_experts_down(h, plan, ones, down, out=back[1:T + 1])
-    torch.cuda.synchronize()
-    assert (back[0] == 7).all() and (back[T + 1] == 7).all()
+    for short in (False, True):
+        back = torch.full((T + 2, F), 7.0, dtype=torch.bfloat16, device=dev)
+        mhc.mhc_experts_down(h, plan, ones, down, short_terms=short, out=back[1:T + 1])
+        torch.cuda.synchronize()
+        assert (back[0] == 7).all() and (back[T + 1] == 7).all()
     if kind == 3:
         good = mhc.mhc_experts_glu(x, plan._replace(pairs=to_dev(np.arange(P, dtype=np.int32), dev)), gate, gate)
         named = torch.zeros(P, dtype=torch.bool, device=dev)
@@ -288,16 +294,18 @@ def test_results_past_32_bits(T, k, E, D, F, shape):
     case(f"results past 32 bits T={T} E={E} D={D} F={F}")
     rng = np.random.default_rng(T)
     assert (T - 100) * k * D * 2 >= 1 << 32
-    for f16 in (False, True):
+    for f16, short in FORMS:
         w = to_mxfp4(*mxfp4(rng, E, D, F, low=127, high=128), F, f16, dev)
         h = to_mxfp4(*mxfp4(rng, T, k, F, low=127, high=128), F, f16, dev)
         e = rng.integers(0, E, (T, k)).astype(np.int32)
         wt = torch.ones(T, k, device=dev)
-        y = mhc.mhc_experts_down(h, a_plan(e, E, dev), wt, w)
+        y = mhc.mhc_experts_down(h, a_plan(e, E, dev), wt, w, short_terms=short)
         for rows in (slice(0, 100), slice(T - 100, T)):
             few = h._replace(codes=h.codes[rows].contiguous(), scales=h.scales[rows].contiguous())
             v = mhc.mhc_experts_down(few, a_plan(e[rows], E, dev), wt[rows], w)
-            # multiples of 1/4 under 2^12: bf16's terms in 11 bits and the few tokens' in fp32 differ by 2^-11 of them, and each is rounded once
-            near = (y[rows].double() - v.double()).abs() <= v.double().abs() * (2.0 ** -11 + 2 * 2.0 ** -8) + 2.0 ** -39 * 4096
-            assert torch.equal(y[rows], v) if f16 else near.all()
+            if f16 or not short:
+                assert torch.equal(y[rows], v)
+            else:   # multiples of 1/4 under 2^12: terms in 11 bits and the few tokens' in fp32 differ by 2^-11 of them, and each is rounded once
+                near = v.double().abs() * (2.0 ** -11 + 2 * 2.0 ** -8) + 2.0 ** -39 * 4096
+                assert ((y[rows].double() - v.double()).abs() <= near).all()
         del w, h, y
