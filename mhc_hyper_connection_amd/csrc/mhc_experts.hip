@@ -284,7 +284,7 @@ __device__ __forceinline__ uint32_t part_down(uint32_t exponent) { return (expon
 //   wait for all loads, meet the other waves (whose reads of stage m are then done)
 //   second half of stage m   read the first half of m + 1, send off the loads of stage m + 2 and (but for the
 //                            group's last stage) a third of those of the next group's scales
-// Loads past the end of the reduction bring zeros. T = 16384, K = 4096, N = 16384: 570 us, 3.9 PFLOP/s; a stage takes 1.7 to
+// Loads past the end of the reduction bring zeros. T = 16384, K = 4096, N = 16384: 554 us, 4.0 PFLOP/s; a stage takes 1.7 to
 // 1.9 us, of which its products alone would take 1.2: the matrix cores are busy 47 % of the cycles, and the waves in a wait for
 // 30 % (for the middle's loads and each other).
 template <bool GATED, int OUT, int WA, int WB, int IA, int IB>
@@ -779,7 +779,7 @@ skinny_kernel(TileArgs p)
 }
 
 // A token's results by its weights: fp32 terms in the order of its slots, one rounding. A thread takes eight values. HBM bounds it:
-// 8192 tokens of 8 slots, D = 4096, 604 MB in 100 us, 6.0 TB/s.
+// 8192 tokens of 8 slots, D = 4096, 1.14 GB in 210 us, 5.4 TB/s; PART, terms in 16 bits: 604 MB in 100 us, 6.0 TB/s.
 template <bool H, bool PART>
 __global__ void __launch_bounds__(256)
 combine_kernel(const void* __restrict__ part, const uint8_t* __restrict__ scales, const float* __restrict__ weights, uint16_t* __restrict__ out, int64_t T, int k,

@@ -91,8 +91,11 @@ inline Tiling make_tiling(const Geometry& g, bool x16 = false)
     else if (3 * cdiv(nl, kCUs) < 2 * cdiv(ns, 2 * kCUs) + (g.op == kGlu ? 1 : 0)) t = {kLarge, 256, 256, 512, 0, 0, kCUs};
     else t = {kSmall, 128, 128, 256, 0, 0, 2 * kCUs};
     // Workgroups that take units in turn send off a unit's first loads before the last one's results are stored, and the stores
-    // run beside its first products: T = 16384, K = 4096, N = 16384 643 against 661 us. The gated projection takes
-    // one unit each: its activation would hold up the next unit, 714 against 702 us for 65536 pairs, D = 4096, F = 2048.
+    // run beside its first products: T = 16384, K = 4096, N = 16384 643 against 661 us. The gated projection takes one unit each: in
+    // this order its activation holds up the next unit, 714 against 702 us for 65536 pairs, D = 4096, F = 2048. (With the next unit's loads
+    // beside the last products it took 655, but one run under a profiler's counters did not end, and no cause was found: not to be
+    // taken up again without one. That loop had a second set of loads chosen by masks within the products, no meeting of the waves between
+    // reduction and results, and scalar registers spilled to vector lanes, none of which the loop that is here has.)
     if (g.op == kGlu) t.places = 0;
     // A streaming workgroup can round its pairs' x rows itself, a launch and a workspace less, but each rounds them again. Two launches
     // against one, us a call: K = 7168, N = 16384: T = 1 17.5, 14.2, 7 17.1, 26.2; K = N = 4096: T = 4 16.7, 13.5, 12 16.2, 16.5;
